@@ -18,7 +18,12 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libtb.so")
 
 TB_OK, TB_ERR_INVALID_ARGUMENT, TB_ERR_UNSUPPORTED, TB_ERR_HIP = 0, 1, 2, 3
-TB_F32, TB_BF16 = 0, 1
+TB_F32, TB_BF16, TB_E4M3 = 0, 1, 2
+TB_SCALE_F32, TB_SCALE_E8M0 = 0, 1
+FP8_BLOCK = 128
+FP8_MAX_IN_DIM = 1 << 25
+MAX_HEAD_DIM = 1024
+MAX_HEADS = 65535
 MAX_GROUP = 8
 WORKSPACE_CONTROL_BYTES = MAX_GROUP * 65536
 FROBENIUS_WORKSPACE_BYTES = 65536
@@ -30,6 +35,8 @@ EXPORTED = (
     "tb_shared_block", "tb_row_scale", "tb_lowrank_factors_workspace_size", "tb_lowrank_factors",
     "tb_lowrank_factors_batch", "tb_refine_shared_block_workspace_size", "tb_refine_shared_block",
     "tb_debug_set_wait_polls", "tb_status_string", "tb_last_error", "tb_linear_forward_no_alloc",
+    "tb_quantize_activations", "tb_reconstruct_weight_fp8", "tb_dense_forward_fp8_workspace_size",
+    "tb_dense_forward_fp8", "tb_head_norm_rotate",
 )
 NO_ALLOC_SCRATCH_BYTES = 96 << 20
 DEFAULT_WAIT_POLLS = 1 << 20
@@ -42,6 +49,13 @@ class Projection(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("s", ctypes.c_void_p), ("w0", ctypes.c_void_p), ("u", ctypes.c_void_p),
                 ("v", ctypes.c_void_p), ("y", ctypes.c_void_p), ("out_dim", ctypes.c_int64),
                 ("in_dim", ctypes.c_int64), ("rank", ctypes.c_int64)]
+
+
+class HeadPart(ctypes.Structure):
+    """tb_head_part: one tensor of heads in tb_head_norm_rotate."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("y_token_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64)]
 
 
 class TBError(RuntimeError):
@@ -81,6 +95,15 @@ def _load() -> ctypes.CDLL:
     lib.tb_debug_set_wait_polls.argtypes = [c_i32]
     lib.tb_linear_forward_no_alloc.argtypes = [c_p, c_p, c_p, c_p, c_p, c_p, c_i64, c_i64, c_i64, c_i64, ctypes.c_int,
                                                c_p]
+    lib.tb_quantize_activations.argtypes = [c_p, c_p, c_p, c_i64, c_i64, ctypes.c_int, ctypes.c_int, c_p]
+    lib.tb_reconstruct_weight_fp8.argtypes = [c_p, c_p, c_p, c_p, c_p, c_p, c_i64, c_i64, c_i64, ctypes.c_int,
+                                              ctypes.c_int, c_p]
+    lib.tb_dense_forward_fp8_workspace_size.argtypes = [c_i64, c_i64, c_i64, ctypes.c_int, ctypes.c_int,
+                                                        ctypes.POINTER(c_sz)]
+    lib.tb_dense_forward_fp8.argtypes = [c_p, c_p, c_p, c_p, c_p, c_i64, c_i64, c_i64, ctypes.c_int, ctypes.c_int,
+                                         ctypes.c_int, c_p, c_sz, c_p]
+    lib.tb_head_norm_rotate.argtypes = [c_i32, ctypes.POINTER(HeadPart), c_i64, c_i64, c_i64, c_i32, c_p, c_p,
+                                        ctypes.c_float, ctypes.c_float, ctypes.c_int, c_p]
     lib.tb_status_string.argtypes = [ctypes.c_int]
     lib.tb_status_string.restype = ctypes.c_char_p
     lib.tb_last_error.argtypes = []
@@ -414,6 +437,213 @@ def reconstruction_error(original: torch.Tensor, s: torch.Tensor, W0: torch.Tens
                                        _dtype_code(W0.dtype), _dtype_code(original.dtype), _ptr(out), _ptr(ws),
                                        ws.numel(), _stream()))
     return out
+
+
+# ---------------------------------------------------------------------------
+# 8-bit blocks: e4m3 numbers with a scale per 128 columns of a token and per
+# 128 x 128 block of a weight
+# ---------------------------------------------------------------------------
+E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _scale_code(dt: torch.dtype) -> int:
+    if dt == torch.float32:
+        return TB_SCALE_F32
+    if dt == E8M0:
+        return TB_SCALE_E8M0
+    raise TBError(TB_ERR_UNSUPPORTED, f"scales are float32 or float8_e8m0fnu, not {dt}")
+
+
+def _fp8_blocks(n: int) -> int:
+    return -(-n // FP8_BLOCK)
+
+
+def quantize_activations(x: torch.Tensor, scale_dtype: torch.dtype = torch.float32) -> tuple:
+    """(e4m3 [m, in], scales [m, ceil(in / 128)]) of x [m, in], via tb_quantize_activations."""
+    if x.dim() != 2:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [m, in]")
+    code, sc = _dtype_code(x.dtype), _scale_code(scale_dtype)
+    m, in_dim = x.shape
+    _need_cuda(x)
+    q = torch.empty((m, in_dim), dtype=E4M3, device=x.device)
+    scale = torch.empty((m, _fp8_blocks(in_dim)), dtype=scale_dtype, device=x.device)
+    _check(lib.tb_quantize_activations(_ptr(x), _ptr(q), _ptr(scale), m, in_dim, code, sc, _stream()))
+    return q, scale
+
+
+def reconstruct_weight_fp8(s: torch.Tensor | None, W0: torch.Tensor, U: torch.Tensor | None, V: torch.Tensor | None,
+                           scale_dtype: torch.dtype = torch.float32, out=None) -> tuple:
+    """diag(s) @ W0 + U @ V.T as (e4m3 [out, in], scales [ceil(out / 128), ceil(in / 128)]) without forming it wide,
+    via tb_reconstruct_weight_fp8 (s None: unit scale; into the pair `out` when given, whose scale dtype wins)."""
+    if s is None:
+        if W0.dim() != 2:
+            raise TBError(TB_ERR_INVALID_ARGUMENT, "W0 must be [out, in]")
+        out_dim, in_dim, rank, U, V = _bundle_dims(W0.new_empty(W0.shape[0]), W0, U, V)
+    else:
+        out_dim, in_dim, rank, U, V = _bundle_dims(s, W0, U, V)
+    q = scale = None
+    if out is not None:
+        q, scale = out
+        scale_dtype = scale.dtype
+    sc = _scale_code(scale_dtype)
+    shapes = (out_dim, in_dim), (_fp8_blocks(out_dim), _fp8_blocks(in_dim))
+    _expect_out(q, shapes[0], E4M3)
+    _expect_out(scale, shapes[1], scale_dtype)
+    _need_cuda(s, W0, U, V, q, scale)
+    q = _output(q, shapes[0], E4M3, W0)
+    scale = _output(scale, shapes[1], scale_dtype, W0)
+    _check(lib.tb_reconstruct_weight_fp8(_ptr(s), _ptr(W0), _ptr(U), _ptr(V), _ptr(q), _ptr(scale), out_dim, in_dim,
+                                         rank, _dtype_code(W0.dtype), sc, _stream()))
+    return q, scale
+
+
+def quantize_weight(W: torch.Tensor, scale_dtype: torch.dtype = torch.float32, out=None) -> tuple:
+    """A dense weight [out, in] as (e4m3, block scales): reconstruct_weight_fp8 with unit scale and rank 0."""
+    return reconstruct_weight_fp8(None, W, None, None, scale_dtype, out)
+
+
+def dense_forward_fp8_workspace_size(m: int, out_dim: int, in_dim: int, x_dtype: torch.dtype,
+                                     scale_dtype: torch.dtype) -> int:
+    out = ctypes.c_size_t(0)
+    code = TB_E4M3 if x_dtype == E4M3 else _dtype_code(x_dtype)
+    _check(lib.tb_dense_forward_fp8_workspace_size(m, out_dim, in_dim, code, _scale_code(scale_dtype),
+                                                   ctypes.byref(out)))
+    return out.value
+
+
+def dense_forward_fp8(x: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, x_scale: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                      workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y = Q(x) @ Wq.T with the block scales applied, via tb_dense_forward_fp8.
+
+    x [m, in] in bfloat16 or float32 is quantised within the call (scales of w_scale's dtype); in float8_e4m3fn it
+    comes with x_scale (quantize_activations).  y has out's dtype, out_dtype, x's dtype, or bfloat16 for an e4m3 x."""
+    if x.dim() != 2 or Wq.dim() != 2:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [m, in] and Wq [out, in]")
+    quantised = x.dtype == E4M3
+    x_code = TB_E4M3 if quantised else _dtype_code(x.dtype)
+    m, in_dim = x.shape
+    out_dim = Wq.shape[0]
+    _expect("Wq", Wq, (out_dim, in_dim), E4M3)
+    sc = _scale_code(w_scale.dtype)
+    _expect("w_scale", w_scale, (_fp8_blocks(out_dim), _fp8_blocks(in_dim)))
+    if quantised != (x_scale is not None):
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "x_scale goes with an x in float8_e4m3fn, and only with one")
+    if quantised:
+        _expect("x_scale", x_scale, (m, _fp8_blocks(in_dim)), w_scale.dtype)
+    if out is not None:
+        out_dtype = out.dtype if out_dtype is None else out_dtype
+    elif out_dtype is None:
+        out_dtype = torch.bfloat16 if quantised else x.dtype
+    y_code = _dtype_code(out_dtype)
+    _expect_out(out, (m, out_dim), out_dtype)
+    _need_cuda(x, Wq, w_scale, x_scale, out)
+    out = _output(out, (m, out_dim), out_dtype, x)
+    ws, need = workspace, 0
+    if ws is None:
+        need = dense_forward_fp8_workspace_size(m, out_dim, in_dim, x.dtype, w_scale.dtype)
+        # From torch's allocator, per call: it follows the stream and, under graph capture, the graph's own pool,
+        # so no two graphs share it.
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    _check(lib.tb_dense_forward_fp8(_ptr(x), _ptr(x_scale), _ptr(Wq), _ptr(w_scale), _ptr(out), m, out_dim, in_dim,
+                                    x_code, y_code, sc, _ptr(ws), 0 if ws is None else _workspace_bytes(ws), _stream()))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Head norms with the position rotation, and the path that ends in them
+# ---------------------------------------------------------------------------
+
+
+def _rotated_dims(positions, freqs, tokens: int, dim: int) -> int:
+    """rot_dim after checking positions [tokens] and freqs [rot_dim / 2] (both None: 0) against heads of dim."""
+    if (positions is None) != (freqs is None):
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "positions and freqs are given together or not at all")
+    if freqs is None:
+        return 0
+    if freqs.dim() != 1:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "freqs must be [rot_dim / 2]")
+    rot = 2 * freqs.shape[0]
+    if rot > dim:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, f"{rot} rotated dimensions, but heads of {dim}")
+    _expect("freqs", freqs, (rot // 2,), torch.float64)
+    _expect("positions", positions, (tokens,), torch.int64)
+    return rot
+
+
+def head_norm_rotate(parts, positions: torch.Tensor | None, freqs: torch.Tensor | None, eps: float = 1e-6,
+                     weight_offset: float = 0.0, interleaved: bool = False, outs=None) -> list:
+    """Per-head norm and position rotation of several tensors of heads in one pass, via tb_head_norm_rotate.
+
+    parts: (x [tokens, heads, head_dim], weight [head_dim] or None) pairs of one dtype, e.g. queries and keys; x may
+    be strided (a view of packed rows) with adjacent elements.  positions int64 [tokens], freqs float64 [rot_dim / 2]
+    (radians per position; both None: no rotation).  Returns new tensors, or writes `outs` (x itself for in place, or
+    a view of a cache)."""
+    if not 1 <= len(parts) <= MAX_GROUP:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, f"a call takes 1..{MAX_GROUP} parts")
+    if outs is not None and len(outs) != len(parts):
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "one output per part")
+    x0 = parts[0][0]
+    if x0.dim() != 3:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [tokens, heads, head_dim]")
+    code = _dtype_code(x0.dtype)
+    tokens, _, dim = x0.shape
+    rot = _rotated_dims(positions, freqs, tokens, dim)
+    for j, (x, w) in enumerate(parts):
+        if x.dim() != 3:
+            raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [tokens, heads, head_dim]")
+        _expect(f"part {j}", x, (tokens, x.shape[1], dim), x0.dtype)
+        if w is not None:
+            _expect(f"weight {j}", w, (dim,), x0.dtype)
+        if outs is not None:
+            _expect("out", outs[j], x.shape, x0.dtype)
+    _need_cuda(positions, freqs, *(w for _, w in parts))
+    arr = (HeadPart * len(parts))()
+    ys = []
+    for j, (x, w) in enumerate(parts):
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if outs is None else outs[j]
+        for t in (x, y):
+            if not t.is_cuda:
+                raise TBError(TB_ERR_INVALID_ARGUMENT, "tensors must live on the GPU")
+            if t.device.index != torch.cuda.current_device():
+                raise TBError(TB_ERR_INVALID_ARGUMENT,
+                              f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+            if dim > 1 and t.stride(2) != 1:
+                raise TBError(TB_ERR_UNSUPPORTED, "the elements of a head must be adjacent")
+        arr[j] = HeadPart(_ptr(x), _ptr(y), _ptr(w), x.shape[1], x.stride(0), x.stride(1), y.stride(0), y.stride(1))
+        ys.append(y)
+    _check(lib.tb_head_norm_rotate(len(parts), arr, tokens, dim, rot, int(interleaved), _ptr(positions), _ptr(freqs),
+                                   eps, weight_offset, code, _stream()))
+    return ys
+
+
+def qkv_forward(x: torch.Tensor, q, k, v, head_dim: int, positions: torch.Tensor | None, freqs: torch.Tensor | None,
+                q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                weight_offset: float = 0.0, interleaved: bool = False) -> tuple:
+    """The input half of an attention layer: (queries, keys, values), each [m, heads, head_dim], of x [m, in].
+
+    q, k, v are the layer's projections, all as bundles (s, W0, U, V) in one grouped launch, or all in 8-bit blocks
+    (Wq, w_scale) with x quantised once; queries and keys then get their head norms and rotation in place."""
+    kinds = {len(p) for p in (q, k, v)}
+    if kinds not in ({4}, {2}):
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "q, k and v are all (s, W0, U, V) or all (Wq, w_scale)")
+    at = 1 if kinds == {4} else 0
+    for name, p in zip("qkv", (q, k, v)):
+        if head_dim < 1 or p[at].dim() != 2 or p[at].shape[0] % head_dim:
+            raise TBError(TB_ERR_INVALID_ARGUMENT, f"{name}: {list(p[at].shape)} is not rows of heads of {head_dim}")
+    _rotated_dims(positions, freqs, x.shape[0], head_dim)
+    for w in (q_weight, k_weight):
+        if w is not None:
+            _expect("head weight", w, (head_dim,), x.dtype)
+    _need_cuda(positions, freqs, q_weight, k_weight)
+    if kinds == {4}:
+        ys = linear_forward_group([(x, *p) for p in (q, k, v)])
+    else:
+        xq, xs = quantize_activations(x, q[1].dtype)
+        ys = [dense_forward_fp8(xq, *p, x_scale=xs, out_dtype=x.dtype) for p in (q, k, v)]
+    yq, yk, yv = (y.view(y.shape[0], -1, head_dim) for y in ys)
+    head_norm_rotate([(yq, q_weight), (yk, k_weight)], positions, freqs, eps, weight_offset, interleaved, [yq, yk])
+    return yq, yk, yv
 
 
 # ---------------------------------------------------------------------------

@@ -657,3 +657,168 @@ const char* tb_status_string(tb_status status) {
 const char* tb_last_error(void) { return g_last_error; }
 
 }  // extern "C"
+
+// ---- 8-bit blocks and head norms ---------------------------------------------
+namespace tb {
+namespace {
+
+bool valid_scale(tb_scale s) { return s == TB_SCALE_F32 || s == TB_SCALE_E8M0; }
+size_t scale_bytes(tb_scale s) { return s == TB_SCALE_E8M0 ? 1 : 4; }
+static_assert(TB_FP8_BLOCK == kFp8Block, "one block size");
+
+// m may be 0 (an empty batch); a launch has one workgroup or more per block.
+tb_status check_fp8_dims(int64_t m, int64_t out_dim, int64_t in_dim, int64_t step) {
+  if (m < 0 || out_dim < 1 || in_dim < 1)
+    return fail(TB_ERR_INVALID_ARGUMENT, "need m >= 0, out_dim >= 1, in_dim >= 1 (got %lld, %lld, %lld)", (long long)m,
+                (long long)out_dim, (long long)in_dim);
+  if (m > kMaxDim || out_dim > kMaxDim) return fail(TB_ERR_UNSUPPORTED, "a dimension exceeds 2^30");
+  if (in_dim > TB_FP8_MAX_IN_DIM)
+    return fail(TB_ERR_UNSUPPORTED, "in_dim %lld exceeds %d", (long long)in_dim, TB_FP8_MAX_IN_DIM);
+  if (in_dim % step != 0)
+    return fail(TB_ERR_UNSUPPORTED, "in_dim %lld is not a multiple of %lld", (long long)in_dim, (long long)step);
+  if (fp8_blocks(out_dim) * fp8_blocks(std::max(in_dim, m)) >= (int64_t(1) << 31) ||
+      fp8_blocks(m) * fp8_blocks(in_dim) >= (int64_t(1) << 31))
+    return fail(TB_ERR_UNSUPPORTED, "matrix too large");
+  return TB_OK;
+}
+
+// Whether the rows of a [tokens, heads, dim] output of these strides are apart.
+bool rows_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t ts, int64_t hs) {
+  if (tokens <= 1 && heads <= 1) return true;
+  if (tokens <= 1) return hs >= dim;
+  if (heads <= 1) return ts >= dim;
+  return (hs >= dim && ts >= (heads - 1) * hs + dim) || (ts >= dim && hs >= (tokens - 1) * ts + dim);
+}
+
+}  // namespace
+}  // namespace tb
+
+extern "C" {
+
+tb_status tb_quantize_activations(const void* x, void* q, void* scale, int64_t m, int64_t in_dim, tb_dtype dtype,
+                                  tb_scale scale_type, void* stream) {
+  if (!valid_dtype(dtype)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(dtype));
+  if (!valid_scale(scale_type)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown scale type %d", int(scale_type));
+  tb_status st = check_fp8_dims(m, 1, in_dim, 8);
+  if (st != TB_OK) return st;
+  if (m == 0) return ok();
+  if (!x || !q || !scale) return fail(TB_ERR_INVALID_ARGUMENT, "x, q and scale must be non-NULL");
+  if (!aligned16(x) || !aligned16(q)) return fail(TB_ERR_UNSUPPORTED, "x and q must be 16-byte aligned");
+  if (!aligned_to(scale, scale_bytes(scale_type)))
+    return fail(TB_ERR_UNSUPPORTED, "scale must be aligned to its element size");
+  hipError_t e = launch_quantize_rows(dtype, scale_type, x, q, scale, m, in_dim, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "launching the activation quantiser");
+  return ok();
+}
+
+tb_status tb_reconstruct_weight_fp8(const void* s, const void* w0, const void* u, const void* v, void* q, void* scale,
+                                    int64_t out_dim, int64_t in_dim, int64_t rank, tb_dtype dtype, tb_scale scale_type,
+                                    void* stream) {
+  if (!valid_dtype(dtype)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(dtype));
+  if (!valid_scale(scale_type)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown scale type %d", int(scale_type));
+  tb_status st = check_fp8_dims(1, out_dim, in_dim, 8);
+  if (st != TB_OK) return st;
+  if (rank < 0) return fail(TB_ERR_INVALID_ARGUMENT, "rank %lld < 0", (long long)rank);
+  if (rank > kMaxDim) return fail(TB_ERR_UNSUPPORTED, "a dimension exceeds 2^30");
+  if (!w0 || !q || !scale) return fail(TB_ERR_INVALID_ARGUMENT, "w0, q and scale must be non-NULL");
+  if (rank > 0 && (!u || !v)) return fail(TB_ERR_INVALID_ARGUMENT, "u and v must be non-NULL when rank > 0");
+  if (!aligned16(w0) || !aligned16(q) || (rank > 0 && (!aligned16(u) || !aligned16(v))))
+    return fail(TB_ERR_UNSUPPORTED, "w0, u, v and q must be 16-byte aligned");
+  if (!aligned_to(s, esize(dtype)) || !aligned_to(scale, scale_bytes(scale_type)))
+    return fail(TB_ERR_UNSUPPORTED, "s and scale must be aligned to their element size");
+  hipError_t e = launch_rebuild_blocks(dtype, scale_type, s, w0, u, v, q, scale, out_dim, in_dim, rank,
+                                       static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "launching the 8-bit rebuild");
+  return ok();
+}
+
+tb_status tb_dense_forward_fp8_workspace_size(int64_t m, int64_t out_dim, int64_t in_dim, tb_dtype x_dtype,
+                                              tb_scale scale_type, size_t* bytes_out) {
+  if (bytes_out == nullptr) return fail(TB_ERR_INVALID_ARGUMENT, "bytes_out is NULL");
+  if (!valid_dtype(x_dtype) && x_dtype != TB_E4M3)
+    return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(x_dtype));
+  if (!valid_scale(scale_type)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown scale type %d", int(scale_type));
+  tb_status st = check_fp8_dims(m, out_dim, in_dim, 16);
+  if (st != TB_OK) return st;
+  *bytes_out = 0;
+  if (m == 0) return ok();
+  int cus = 0;
+  if (int e = device_cu_count(&cus)) return hip_fail(hipError_t(e), "querying the compute-unit count");
+  *bytes_out = plan_fp8(m, out_dim, in_dim, x_dtype == TB_E4M3, scale_type, cus).bytes;
+  return ok();
+}
+
+tb_status tb_dense_forward_fp8(const void* x, const void* x_scale, const void* wq, const void* w_scale, void* y,
+                               int64_t m, int64_t out_dim, int64_t in_dim, tb_dtype x_dtype, tb_dtype y_dtype,
+                               tb_scale scale_type, void* workspace, size_t workspace_bytes, void* stream) {
+  const bool quantised = x_dtype == TB_E4M3;
+  if (!valid_dtype(x_dtype) && !quantised) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(x_dtype));
+  if (!valid_dtype(y_dtype)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(y_dtype));
+  if (!valid_scale(scale_type)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown scale type %d", int(scale_type));
+  tb_status st = check_fp8_dims(m, out_dim, in_dim, 16);
+  if (st != TB_OK) return st;
+  if (quantised ? (m > 0 && !x_scale) : x_scale != nullptr)
+    return fail(TB_ERR_INVALID_ARGUMENT, "x_scale goes with an x in e4m3, and only with one");
+  if (m == 0) return ok();
+  if (!x || !wq || !w_scale || !y) return fail(TB_ERR_INVALID_ARGUMENT, "x, wq, w_scale and y must be non-NULL");
+  if (!aligned16(x) || !aligned16(wq)) return fail(TB_ERR_UNSUPPORTED, "x and wq must be 16-byte aligned");
+  if (!aligned_to(x_scale, scale_bytes(scale_type)) || !aligned_to(w_scale, scale_bytes(scale_type)) ||
+      !aligned_to(y, esize(y_dtype)))
+    return fail(TB_ERR_UNSUPPORTED, "scales and y must be aligned to their element size");
+  int cus = 0;
+  if (int e = device_cu_count(&cus)) return hip_fail(hipError_t(e), "querying the compute-unit count");
+  const Fp8Plan p = plan_fp8(m, out_dim, in_dim, quantised, scale_type, cus);
+  if (p.bytes > 0) {
+    if (!workspace) return fail(TB_ERR_INVALID_ARGUMENT, "workspace must be non-NULL");
+    if (!aligned_to(workspace, 256)) return fail(TB_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
+    if (workspace_bytes < p.bytes)
+      return fail(TB_ERR_INVALID_ARGUMENT, "workspace of %zu bytes is below the %zu needed", workspace_bytes, p.bytes);
+  }
+  hipError_t e = launch_fp8_product(p, x_dtype, y_dtype, scale_type, x, x_scale, wq, w_scale, y, m, out_dim, in_dim,
+                                    static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "launching the 8-bit product");
+  return ok();
+}
+
+tb_status tb_head_norm_rotate(int32_t n, const tb_head_part* parts, int64_t tokens, int64_t head_dim, int64_t rot_dim,
+                              int32_t interleaved, const int64_t* positions, const double* freqs, float eps,
+                              float weight_offset, tb_dtype dtype, void* stream) {
+  if (!valid_dtype(dtype)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(dtype));
+  if (n < 1 || n > TB_MAX_GROUP) return fail(TB_ERR_INVALID_ARGUMENT, "n %d outside [1, %d]", n, TB_MAX_GROUP);
+  if (!parts) return fail(TB_ERR_INVALID_ARGUMENT, "parts is NULL");
+  if (tokens < 0 || head_dim < 1 || rot_dim < 0 || rot_dim > head_dim || rot_dim % 2 != 0)
+    return fail(TB_ERR_INVALID_ARGUMENT, "need tokens >= 0, head_dim >= 1 and an even rot_dim in [0, head_dim] (got %lld, %lld, %lld)",
+                (long long)tokens, (long long)head_dim, (long long)rot_dim);
+  if (!(eps >= 0.f)) return fail(TB_ERR_INVALID_ARGUMENT, "eps must be >= 0");
+  if (head_dim > TB_MAX_HEAD_DIM || tokens > kMaxDim)
+    return fail(TB_ERR_UNSUPPORTED, "head_dim exceeds %d or tokens 2^30", TB_MAX_HEAD_DIM);
+  int64_t heads = 0;
+  for (int j = 0; j < n; ++j) {
+    const tb_head_part& p = parts[j];
+    if (p.heads < 0) return fail(TB_ERR_INVALID_ARGUMENT, "part %d: heads < 0", j);
+    if (p.heads > TB_MAX_HEADS || (heads += p.heads) > TB_MAX_HEADS)
+      return fail(TB_ERR_UNSUPPORTED, "more than %d heads", TB_MAX_HEADS);
+    if (tokens == 0 || p.heads == 0) continue;
+    if (!p.x || !p.y) return fail(TB_ERR_INVALID_ARGUMENT, "part %d: x and y must be non-NULL", j);
+    const int64_t strides[4] = {p.x_token_stride, p.x_head_stride, p.y_token_stride, p.y_head_stride};
+    for (int64_t s : strides) {
+      if (s < 0) return fail(TB_ERR_INVALID_ARGUMENT, "part %d: a stride is negative", j);
+      if (s > (int64_t(1) << 40)) return fail(TB_ERR_UNSUPPORTED, "part %d: a stride exceeds 2^40", j);
+    }
+    if (!rows_apart(tokens, p.heads, head_dim, p.y_token_stride, p.y_head_stride))
+      return fail(TB_ERR_INVALID_ARGUMENT, "part %d: the rows of y overlap", j);
+    if (!aligned_to(p.x, esize(dtype)) || !aligned_to(p.y, esize(dtype)) || !aligned_to(p.weight, esize(dtype)))
+      return fail(TB_ERR_UNSUPPORTED, "part %d: pointers must be aligned to their element size", j);
+  }
+  if (tokens == 0 || heads == 0) return ok();
+  if (rot_dim > 0 && (!positions || !freqs))
+    return fail(TB_ERR_INVALID_ARGUMENT, "positions and freqs must be non-NULL when rot_dim > 0");
+  if (rot_dim > 0 && (!aligned_to(positions, 8) || !aligned_to(freqs, 8)))
+    return fail(TB_ERR_UNSUPPORTED, "positions and freqs must be 8-byte aligned");
+  hipError_t e = launch_heads(dtype, n, parts, tokens, int(head_dim), int(rot_dim), interleaved != 0, positions, freqs,
+                              eps, weight_offset, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "launching the head norms");
+  return ok();
+}
+
+}  // extern "C"

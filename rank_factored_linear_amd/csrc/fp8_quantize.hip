@@ -1,0 +1,214 @@
+// 8-bit blocks of activations and of weights (the formats are in
+// fp8_device.h).
+#include "fp8_device.h"
+#include "tb_rebuild.h"
+
+namespace tb {
+
+namespace {
+
+using namespace fp8;
+
+constexpr int kThreads = 256;
+
+// ---- activations: one scale per row and 128 columns -------------------------
+//
+// Sixteen lanes hold a block, eight elements each, so a block is one 16-byte
+// (bf16) load, four cross-lane maxima and one 8-byte store per lane: one pass
+// over the data, bound by HBM for long inputs and by launch latency for a few
+// rows.  A wave takes kSeg blocks of one row (four at a time); the row's
+// segments go over blockIdx.y so that a few long rows still fill the chip.
+constexpr int kSeg = 8;
+
+template <typename E, int SC>
+__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const E* __restrict__ x, uint8_t* __restrict__ q,
+                                                                 scale_t<SC>* __restrict__ scale, int64_t M, int I,
+                                                                 int KB) {
+  const int l = int(threadIdx.x) & 63;
+  const int64_t row = int64_t(blockIdx.x) * (kThreads / kWave) + (threadIdx.x >> 6);
+  if (row >= M) return;
+  const E* xr = x + row * I;
+  uint8_t* qr = q + row * I;
+  Frag8<E> f[kSeg / 4];
+#pragma unroll
+  for (int p = 0; p < kSeg / 4; ++p) {
+    const int c = (int(blockIdx.y) * kSeg + p * 4) * kBlock + l * 8;   // I % 8 == 0: all eight or none
+    f[p] = load_frag_if<E>(xr + c, c < I);
+  }
+#pragma unroll
+  for (int p = 0; p < kSeg / 4; ++p) {
+    const int kb = int(blockIdx.y) * kSeg + p * 4 + (l >> 4), c = kb * kBlock + (l & 15) * 8;
+    float t[8];
+    unpack8(f[p], t);
+    uint32_t a = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a = max(a, abs_bits(t[e]));
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) a = max(a, uint32_t(__shfl_xor(int(a), d)));
+    scale_t<SC> st;
+    float by;
+    block_scale<SC>(a, st, by);
+    if (c < I)
+      *reinterpret_cast<u32x2*>(qr + c) = u32x2{pack4(t[0] * by, t[1] * by, t[2] * by, t[3] * by),
+                                                pack4(t[4] * by, t[5] * by, t[6] * by, t[7] * by)};
+    if ((l & 15) == 0 && kb < KB) scale[row * KB + kb] = st;
+  }
+}
+
+// ---- weights: W = diag(s) W0 + U V^T, one scale per 128 x 128 block ---------
+//
+// One workgroup makes one block: the product U V^T on the matrix cores, then
+// through LDS (fp32) so that sixteen lanes cover a row of 128: W0 is read in
+// 16- or 32-byte pieces per lane and the e4m3 bytes leave 128 to a row.  The
+// W0 loads are issued ahead of the product and arrive under it.  Each thread
+// keeps its 64 rebuilt values in registers between the block's maximum and
+// their rounding, so W is formed once, in fp32, and never written wide: bf16
+// bundles move 3 bytes per weight through HBM.
+constexpr int kPitch = 132;  // floats per row of the tile in LDS: 16-byte aligned, rows 4 banks apart
+
+enum Product { kNone, kMfma, kAny };
+
+template <typename EI, int SC, int PROD>
+__global__ __launch_bounds__(kThreads, 2) void rebuild_blocks_kernel(const EI* __restrict__ s,
+                                                                     const EI* __restrict__ w0,
+                                                                     const EI* __restrict__ u,
+                                                                     const EI* __restrict__ v,
+                                                                     uint8_t* __restrict__ q,
+                                                                     scale_t<SC>* __restrict__ scale, int O, int I,
+                                                                     int R, int KB) {
+  constexpr int kTile = PROD == kNone ? 16 : kBlock * kPitch * 4;
+  static_assert(kTile == 16 || kTile >= rebuild::t128::kLdsBytes, "the product's staging fits the tile's room");
+  __shared__ __attribute__((aligned(16))) unsigned char lds[kTile];
+  __shared__ uint32_t wave_max[kThreads / kWave];
+  const int tid = int(threadIdx.x), w = tid >> 6, l = tid & 63;
+  const int ob = int(blockIdx.x) / KB, kb = int(blockIdx.x) % KB;
+  const int o0 = ob * kBlock, i0 = kb * kBlock;
+  const int c = (tid & 15) * 8, r0 = tid >> 4;   // thread: columns c..c+7 of rows r0 + 16 p
+
+  Frag8<EI> f[8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int o = o0 + r0 + 16 * p;
+    f[p] = load_frag_if<EI>(w0 + size_t(o) * I + i0 + c, o < O && i0 + c < I);   // I % 8 == 0
+  }
+
+  float* tile = reinterpret_cast<float*>(lds);
+  if constexpr (PROD == kMfma) {
+    namespace t = rebuild::t128;
+    t::f32x16 acc[2][2];
+    t::product(u, v, O, I, R, o0, i0, lds, acc);
+    __syncthreads();   // every wave has read the last k-tile
+    const int wi = w & 1, wo = w >> 1, h = l >> 5, lr = l & 31;
+#pragma unroll
+    for (int cb = 0; cb < 2; ++cb)
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const t::f32x16& a = acc[rb][cb];
+          *reinterpret_cast<f32x4*>(tile + (wo * 64 + cb * 32 + lr) * kPitch + wi * 64 + rb * 32 + 8 * b + 4 * h) =
+              f32x4{a[4 * b], a[4 * b + 1], a[4 * b + 2], a[4 * b + 3]};
+        }
+    __syncthreads();
+  } else if constexpr (PROD == kAny) {
+    namespace t = rebuild::t64;
+    for (int qd = 0; qd < 4; ++qd) {
+      const int to = (qd >> 1) * t::BT, ti = (qd & 1) * t::BT;
+      f32x4 acc[4];
+      t::product<EI>(u, v, O, I, R, o0 + to, i0 + ti, acc);
+#pragma unroll
+      for (int ct = 0; ct < 4; ++ct)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          tile[(to + w * 16 + (l >> 4) * 4 + e) * kPitch + ti + ct * 16 + (l & 15)] = acc[ct][e];
+    }
+    __syncthreads();
+  }
+
+  float val[8][8];
+  uint32_t a = 0;
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int row = r0 + 16 * p, o = o0 + row;
+    unpack8(f[p], val[p]);
+    const float so = s != nullptr && o < O ? to_f32<EI>(s[o]) : 1.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float t = s != nullptr ? so * val[p][e] : val[p][e];
+      if constexpr (PROD != kNone) t = tile[row * kPitch + c + e] + t;
+      val[p][e] = t;
+      // Rows and columns past the matrix hold zeros (W0, U and V read as zero there).
+      a = max(a, abs_bits(t));
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) a = max(a, uint32_t(__shfl_xor(int(a), d)));
+  if (l == 0) wave_max[w] = a;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kThreads / kWave; ++j) a = max(a, wave_max[j]);
+  scale_t<SC> st;
+  float by;
+  block_scale<SC>(a, st, by);
+  if (tid == 0) scale[size_t(ob) * KB + kb] = st;
+  if (i0 + c >= I) return;
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int o = o0 + r0 + 16 * p;
+    if (o >= O) continue;
+    const float(&t)[8] = val[p];
+    *reinterpret_cast<u32x2*>(q + size_t(o) * I + i0 + c) =
+        u32x2{pack4(t[0] * by, t[1] * by, t[2] * by, t[3] * by), pack4(t[4] * by, t[5] * by, t[6] * by, t[7] * by)};
+  }
+}
+
+template <typename E, int SC>
+hipError_t rows_typed(const void* x, void* q, void* scale, int64_t m, int64_t in_dim, hipStream_t stream) {
+  const int KB = int(fp8_blocks(in_dim));
+  const dim3 grid(unsigned((m + kThreads / kWave - 1) / (kThreads / kWave)), unsigned((KB + kSeg - 1) / kSeg));
+  hipLaunchKernelGGL((quantize_rows_kernel<E, SC>), grid, dim3(kThreads), 0, stream, static_cast<const E*>(x),
+                     static_cast<uint8_t*>(q), static_cast<scale_t<SC>*>(scale), m, int(in_dim), KB);
+  return hipGetLastError();
+}
+
+template <typename EI, int SC>
+hipError_t blocks_typed(const void* s, const void* w0, const void* u, const void* v, void* q, void* scale,
+                        int64_t out_dim, int64_t in_dim, int64_t rank, hipStream_t stream) {
+  const int KB = int(fp8_blocks(in_dim));
+  const dim3 grid(unsigned(fp8_blocks(out_dim) * KB));
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, static_cast<const EI*>(s), static_cast<const EI*>(w0),
+                       static_cast<const EI*>(u), static_cast<const EI*>(v), static_cast<uint8_t*>(q),
+                       static_cast<scale_t<SC>*>(scale), int(out_dim), int(in_dim), int(rank), KB);
+    return hipGetLastError();
+  };
+  if (rank == 0) return go(rebuild_blocks_kernel<EI, SC, kNone>);
+  if constexpr (sizeof(EI) == 2)
+    if (rank % 8 == 0) return go(rebuild_blocks_kernel<EI, SC, kMfma>);
+  return go(rebuild_blocks_kernel<EI, SC, kAny>);
+}
+
+}  // namespace
+
+hipError_t launch_quantize_rows(tb_dtype dtype, tb_scale scale_type, const void* x, void* q, void* scale, int64_t m,
+                                int64_t in_dim, hipStream_t stream) {
+  const bool e8 = scale_type == TB_SCALE_E8M0;
+  if (dtype == TB_BF16)
+    return e8 ? rows_typed<bf16_t, TB_SCALE_E8M0>(x, q, scale, m, in_dim, stream)
+              : rows_typed<bf16_t, TB_SCALE_F32>(x, q, scale, m, in_dim, stream);
+  return e8 ? rows_typed<float, TB_SCALE_E8M0>(x, q, scale, m, in_dim, stream)
+            : rows_typed<float, TB_SCALE_F32>(x, q, scale, m, in_dim, stream);
+}
+
+hipError_t launch_rebuild_blocks(tb_dtype dtype, tb_scale scale_type, const void* s, const void* w0, const void* u,
+                                 const void* v, void* q, void* scale, int64_t out_dim, int64_t in_dim, int64_t rank,
+                                 hipStream_t stream) {
+  const bool e8 = scale_type == TB_SCALE_E8M0;
+  if (dtype == TB_BF16)
+    return e8 ? blocks_typed<bf16_t, TB_SCALE_E8M0>(s, w0, u, v, q, scale, out_dim, in_dim, rank, stream)
+              : blocks_typed<bf16_t, TB_SCALE_F32>(s, w0, u, v, q, scale, out_dim, in_dim, rank, stream);
+  return e8 ? blocks_typed<float, TB_SCALE_E8M0>(s, w0, u, v, q, scale, out_dim, in_dim, rank, stream)
+            : blocks_typed<float, TB_SCALE_F32>(s, w0, u, v, q, scale, out_dim, in_dim, rank, stream);
+}
+
+}  // namespace tb

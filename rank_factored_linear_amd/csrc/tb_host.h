@@ -177,4 +177,36 @@ int launch_lowrank_factors(tb_dtype dtype, const void* const* weights, int n, co
                            int64_t out_dim, int64_t in_dim, int64_t rank, const float* omega, int64_t k, int power_iters,
                            float* u_out, float* v_out, void* workspace, int cus, hipStream_t stream, const char** what);
 
+// ---- 8-bit blocks ------------------------------------------------------------
+constexpr int kFp8Block = 128;
+inline int64_t fp8_blocks(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
+
+// x [m, in_dim] -> e4m3 and one scale per row and 128 columns.
+hipError_t launch_quantize_rows(tb_dtype dtype, tb_scale scale_type, const void* x, void* q, void* scale, int64_t m,
+                                int64_t in_dim, hipStream_t stream);
+// diag(s) . W0 + U . V^T (s NULL: unit scale) -> e4m3 and one scale per 128 x 128 block.
+hipError_t launch_rebuild_blocks(tb_dtype dtype, tb_scale scale_type, const void* s, const void* w0, const void* u,
+                                 const void* v, void* q, void* scale, int64_t out_dim, int64_t in_dim, int64_t rank,
+                                 hipStream_t stream);
+
+// Up to this many tokens the few-token kernel quantises x itself.
+constexpr int kFp8FusedTokens = 16;
+
+struct Fp8Plan {
+  int decode;              // 1: the few-token kernel (m <= kDecodeMaxTokens)
+  int fused;               // x is quantised inside it
+  int tiles_m, tiles_n, S; // tiles of the many-token kernel and slices of in_dim
+  size_t off_xq, off_xs, off_part, bytes;   // Q(x), its scales and the slices' sums in the workspace
+};
+// quantised: x comes in e4m3 with its scales.
+Fp8Plan plan_fp8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, tb_scale scale_type, int cus);
+hipError_t launch_fp8_product(const Fp8Plan& p, tb_dtype x_dtype, tb_dtype y_dtype, tb_scale scale_type, const void* x,
+                              const void* xs, const void* w, const void* ws, void* y, int64_t m, int64_t out_dim,
+                              int64_t in_dim, char* data, hipStream_t stream);
+
+// ---- head norms with the position rotation ----------------------------------
+hipError_t launch_heads(tb_dtype dtype, int n, const tb_head_part* parts, int64_t tokens, int head_dim, int rot_dim,
+                        bool interleaved, const int64_t* positions, const double* freqs, float eps, float offset,
+                        hipStream_t stream);
+
 }  // namespace tb
