@@ -417,8 +417,8 @@ tb_status tb_refine_shared_block(const void *const *weights, const float *const 
  * one scale per row and 128 columns (the last block may be shorter).  With a
  * the block's largest magnitude:
  *   TB_SCALE_E8M0: scale = 2^max(ceil(log2(a / 448)), -127), q = e4m3(x / scale);
- *   TB_SCALE_F32:  scale = a' / 448, q = e4m3(x * (448 / a')), a' = max(a, 2^-100),
- *                  each operation rounded to fp32.
+ *   TB_SCALE_F32:  scale = a' * (1 / 448), q = e4m3(x * (448 * (1 / a'))) with
+ *                  a' = max(a, 2^-100), each operation rounded to fp32.
  * e4m3 rounds to nearest, ties to even.  A block that holds an infinity or NaN
  * gets a NaN scale and NaN entries.
  *   m >= 0 (0: nothing is enqueued), in_dim >= 8, % 8 == 0 and <=
@@ -466,12 +466,11 @@ tb_status tb_reconstruct_weight_fp8(const void *s, const void *w0, const void *u
  *   scales must be finite in fp32.
  *   workspace: at least tb_dense_forward_fp8_workspace_size() bytes, 256-byte
  *   aligned, no initial contents (NULL when 0).  Calls that may run at the same
- *   time must not share it.  The size for a larger m covers smaller ones only
- *   if asked for: query each m.
+ *   time must not share it.  The size does not grow with m everywhere: query each m.
  *   Errors: TB_ERR_INVALID_ARGUMENT, TB_ERR_UNSUPPORTED, TB_ERR_HIP.
  */
 tb_status tb_dense_forward_fp8_workspace_size(int64_t m, int64_t out_dim, int64_t in_dim, tb_dtype x_dtype,
-                                              tb_scale scale_type, size_t *bytes_out);
+                                              tb_dtype y_dtype, tb_scale scale_type, size_t *bytes_out);
 tb_status tb_dense_forward_fp8(const void *x, const void *x_scale, const void *wq, const void *w_scale, void *y,
                                int64_t m, int64_t out_dim, int64_t in_dim, tb_dtype x_dtype, tb_dtype y_dtype,
                                tb_scale scale_type, void *workspace, size_t workspace_bytes, void *stream);

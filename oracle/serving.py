@@ -32,7 +32,8 @@ def to_e4m3(v: np.ndarray) -> np.ndarray:
 
 def quantize_blocks(a: np.ndarray, rows: int, power_of_two: bool):
     """(held e4m3 values [m, n], scales [ceil(m / rows), ceil(n / 128)]) of a [m, n] float64 matrix of fp32 values in
-    blocks of `rows` x 128.  fp32 scales: largest / 448 and value * (448 / largest), each operation rounded to fp32."""
+    blocks of `rows` x 128.  fp32 scales: largest * (1 / 448) and value * (448 * (1 / largest)), each operation rounded
+    to fp32."""
     m, n = a.shape
     held = np.empty((m, n))
     scales = np.empty((-(-m // rows), -(-n // BLOCK)))
@@ -54,8 +55,9 @@ def quantize_blocks(a: np.ndarray, rows: int, power_of_two: bool):
                     held[at] = to_e4m3(b / scales[i, j])
                 else:
                     t = f32(max(top, 2.0 ** -100))
-                    scales[i, j] = f32(t / f32(448))
-                    held[at] = to_e4m3((b.astype(f32) * f32(f32(448) / t)).astype(np.float64))
+                    scales[i, j] = f32(t * f32(f32(1) / f32(448)))
+                    by = f32(f32(448) * f32(f32(1) / t))
+                    held[at] = to_e4m3((b.astype(f32) * by).astype(np.float64))
     return held, scales
 
 

@@ -98,11 +98,11 @@ def _load() -> ctypes.CDLL:
     lib.tb_quantize_activations.argtypes = [c_p, c_p, c_p, c_i64, c_i64, ctypes.c_int, ctypes.c_int, c_p]
     lib.tb_reconstruct_weight_fp8.argtypes = [c_p, c_p, c_p, c_p, c_p, c_p, c_i64, c_i64, c_i64, ctypes.c_int,
                                               ctypes.c_int, c_p]
-    lib.tb_dense_forward_fp8_workspace_size.argtypes = [c_i64, c_i64, c_i64, ctypes.c_int, ctypes.c_int,
+    lib.tb_dense_forward_fp8_workspace_size.argtypes = [c_i64, c_i64, c_i64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                         ctypes.POINTER(c_sz)]
     lib.tb_dense_forward_fp8.argtypes = [c_p, c_p, c_p, c_p, c_p, c_i64, c_i64, c_i64, ctypes.c_int, ctypes.c_int,
                                          ctypes.c_int, c_p, c_sz, c_p]
-    lib.tb_head_norm_rotate.argtypes = [c_i32, ctypes.POINTER(HeadPart), c_i64, c_i64, c_i64, c_i32, c_p, c_p,
+    lib.tb_head_norm_rotate.argtypes = [c_i32, c_p, c_i64, c_i64, c_i64, c_i32, c_p, c_p,
                                         ctypes.c_float, ctypes.c_float, ctypes.c_int, c_p]
     lib.tb_status_string.argtypes = [ctypes.c_int]
     lib.tb_status_string.restype = ctypes.c_char_p
@@ -135,21 +135,30 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _stream() -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+def _stream() -> int:
+    # The raw handle, without building a torch.cuda.Stream around it on every call.
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
-def _need_cuda(*ts):
-    """Every tensor is contiguous and lives on the current GPU (the device the library launches on)."""
+def _need_device(*ts):
+    """Every tensor lives on the current GPU (the device the library launches on)."""
+    dev = None
     for t in ts:
         if t is not None:
             if not t.is_cuda:
                 raise TBError(TB_ERR_INVALID_ARGUMENT, "tensors must live on the GPU")
-            if t.device.index != torch.cuda.current_device():
-                raise TBError(TB_ERR_INVALID_ARGUMENT,
-                              f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-            if not t.is_contiguous():
-                raise TBError(TB_ERR_UNSUPPORTED, "tensors must be contiguous")
+            if dev is None:
+                dev = torch.cuda.current_device()
+            if t.get_device() != dev:
+                raise TBError(TB_ERR_INVALID_ARGUMENT, f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _need_cuda(*ts):
+    """Every tensor is contiguous and lives on the current GPU."""
+    _need_device(*ts)
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            raise TBError(TB_ERR_UNSUPPORTED, "tensors must be contiguous")
 
 
 # Shape and dtype checks run before the device checks and before anything
@@ -158,7 +167,7 @@ def _need_cuda(*ts):
 
 
 def _expect(name: str, t: torch.Tensor, shape, dtype: torch.dtype | None = None) -> None:
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:   # (torch.Size compares as a tuple)
         raise TBError(TB_ERR_INVALID_ARGUMENT, f"{name} must be {list(shape)}, got {list(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TBError(TB_ERR_INVALID_ARGUMENT, f"{name} must be {dtype}, got {t.dtype}")
@@ -347,13 +356,14 @@ def linear_forward_group(members, workspace: torch.Tensor | None = None, outs=No
 
 
 def _bundle_dims(s, W0, U, V):
-    """(out_dim, in_dim, rank, U, V) of a bundle after checking s [out], U [out, rank], V [in, rank] against W0
-    (one dtype); a rank-0 U/V pair becomes None."""
+    """(out_dim, in_dim, rank, U, V) of a bundle after checking s [out] (where there is one), U [out, rank], V [in, rank]
+    against W0 (one dtype); a rank-0 U/V pair becomes None."""
     if W0.dim() != 2:
         raise TBError(TB_ERR_INVALID_ARGUMENT, "W0 must be [out, in]")
     _dtype_code(W0.dtype)
     out_dim, in_dim = W0.shape
-    _expect("s", s, (out_dim,), W0.dtype)
+    if s is not None:
+        _expect("s", s, (out_dim,), W0.dtype)
     if (U is None) != (V is None):
         raise TBError(TB_ERR_INVALID_ARGUMENT, "U and V are given together or not at all")
     rank = 0
@@ -475,12 +485,7 @@ def reconstruct_weight_fp8(s: torch.Tensor | None, W0: torch.Tensor, U: torch.Te
                            scale_dtype: torch.dtype = torch.float32, out=None) -> tuple:
     """diag(s) @ W0 + U @ V.T as (e4m3 [out, in], scales [ceil(out / 128), ceil(in / 128)]) without forming it wide,
     via tb_reconstruct_weight_fp8 (s None: unit scale; into the pair `out` when given, whose scale dtype wins)."""
-    if s is None:
-        if W0.dim() != 2:
-            raise TBError(TB_ERR_INVALID_ARGUMENT, "W0 must be [out, in]")
-        out_dim, in_dim, rank, U, V = _bundle_dims(W0.new_empty(W0.shape[0]), W0, U, V)
-    else:
-        out_dim, in_dim, rank, U, V = _bundle_dims(s, W0, U, V)
+    out_dim, in_dim, rank, U, V = _bundle_dims(s, W0, U, V)
     q = scale = None
     if out is not None:
         q, scale = out
@@ -502,12 +507,12 @@ def quantize_weight(W: torch.Tensor, scale_dtype: torch.dtype = torch.float32, o
     return reconstruct_weight_fp8(None, W, None, None, scale_dtype, out)
 
 
-def dense_forward_fp8_workspace_size(m: int, out_dim: int, in_dim: int, x_dtype: torch.dtype,
+def dense_forward_fp8_workspace_size(m: int, out_dim: int, in_dim: int, x_dtype: torch.dtype, out_dtype: torch.dtype,
                                      scale_dtype: torch.dtype) -> int:
     out = ctypes.c_size_t(0)
     code = TB_E4M3 if x_dtype == E4M3 else _dtype_code(x_dtype)
-    _check(lib.tb_dense_forward_fp8_workspace_size(m, out_dim, in_dim, code, _scale_code(scale_dtype),
-                                                   ctypes.byref(out)))
+    _check(lib.tb_dense_forward_fp8_workspace_size(m, out_dim, in_dim, code, _dtype_code(out_dtype),
+                                                   _scale_code(scale_dtype), ctypes.byref(out)))
     return out.value
 
 
@@ -539,14 +544,19 @@ def dense_forward_fp8(x: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, 
     _expect_out(out, (m, out_dim), out_dtype)
     _need_cuda(x, Wq, w_scale, x_scale, out)
     out = _output(out, (m, out_dim), out_dtype, x)
-    ws, need = workspace, 0
+    ws = workspace
     if ws is None:
-        need = dense_forward_fp8_workspace_size(m, out_dim, in_dim, x.dtype, w_scale.dtype)
+        size = ctypes.c_size_t(0)
+        _check(lib.tb_dense_forward_fp8_workspace_size(m, out_dim, in_dim, x_code, y_code, sc, ctypes.byref(size)))
+        need = size.value
         # From torch's allocator, per call: it follows the stream and, under graph capture, the graph's own pool,
         # so no two graphs share it.
         ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+        nbytes = need
+    else:
+        nbytes = _workspace_bytes(ws)
     _check(lib.tb_dense_forward_fp8(_ptr(x), _ptr(x_scale), _ptr(Wq), _ptr(w_scale), _ptr(out), m, out_dim, in_dim,
-                                    x_code, y_code, sc, _ptr(ws), 0 if ws is None else _workspace_bytes(ws), _stream()))
+                                    x_code, y_code, sc, _ptr(ws), nbytes, _stream()))
     return out
 
 
@@ -589,31 +599,35 @@ def head_norm_rotate(parts, positions: torch.Tensor | None, freqs: torch.Tensor 
     code = _dtype_code(x0.dtype)
     tokens, _, dim = x0.shape
     rot = _rotated_dims(positions, freqs, tokens, dim)
+    dtype, weight_shape = x0.dtype, (dim,)
     for j, (x, w) in enumerate(parts):
         if x.dim() != 3:
             raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [tokens, heads, head_dim]")
-        _expect(f"part {j}", x, (tokens, x.shape[1], dim), x0.dtype)
+        if j:
+            _expect(f"part {j}", x, (tokens, x.shape[1], dim), dtype)
         if w is not None:
-            _expect(f"weight {j}", w, (dim,), x0.dtype)
+            _expect("weight", w, weight_shape, dtype)
         if outs is not None:
-            _expect("out", outs[j], x.shape, x0.dtype)
+            _expect("out", outs[j], x.shape, dtype)
     _need_cuda(positions, freqs, *(w for _, w in parts))
-    arr = (HeadPart * len(parts))()
-    ys = []
+    _need_device(*(x for x, _ in parts), *(outs or ()))
+    ys, fields = [], []
     for j, (x, w) in enumerate(parts):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if outs is None else outs[j]
-        for t in (x, y):
-            if not t.is_cuda:
-                raise TBError(TB_ERR_INVALID_ARGUMENT, "tensors must live on the GPU")
-            if t.device.index != torch.cuda.current_device():
-                raise TBError(TB_ERR_INVALID_ARGUMENT,
-                              f"tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-            if dim > 1 and t.stride(2) != 1:
-                raise TBError(TB_ERR_UNSUPPORTED, "the elements of a head must be adjacent")
-        arr[j] = HeadPart(_ptr(x), _ptr(y), _ptr(w), x.shape[1], x.stride(0), x.stride(1), y.stride(0), y.stride(1))
+        xt, xh, xe = x.stride()
+        if outs is None:
+            y = torch.empty(x.shape, dtype=dtype, device=x.device)
+            yt, yh, ye = x.shape[1] * dim, dim, 1
+        else:
+            y = outs[j]
+            yt, yh, ye = y.stride()
+        if (xe != 1 or ye != 1) and dim > 1:
+            raise TBError(TB_ERR_UNSUPPORTED, "the elements of a head must be adjacent")
+        # tb_head_part, every field eight bytes
+        fields += (x.data_ptr(), y.data_ptr(), 0 if w is None else w.data_ptr(), x.shape[1], xt, xh, yt, yh)
         ys.append(y)
-    _check(lib.tb_head_norm_rotate(len(parts), arr, tokens, dim, rot, int(interleaved), _ptr(positions), _ptr(freqs),
-                                   eps, weight_offset, code, _stream()))
+    _check(lib.tb_head_norm_rotate(len(parts), (ctypes.c_int64 * len(fields))(*fields), tokens, dim, rot,
+                                   int(interleaved), _ptr(positions), _ptr(freqs), eps, weight_offset, code,
+                                   _stream()))
     return ys
 
 

@@ -733,10 +733,11 @@ tb_status tb_reconstruct_weight_fp8(const void* s, const void* w0, const void* u
 }
 
 tb_status tb_dense_forward_fp8_workspace_size(int64_t m, int64_t out_dim, int64_t in_dim, tb_dtype x_dtype,
-                                              tb_scale scale_type, size_t* bytes_out) {
+                                              tb_dtype y_dtype, tb_scale scale_type, size_t* bytes_out) {
   if (bytes_out == nullptr) return fail(TB_ERR_INVALID_ARGUMENT, "bytes_out is NULL");
   if (!valid_dtype(x_dtype) && x_dtype != TB_E4M3)
     return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(x_dtype));
+  if (!valid_dtype(y_dtype)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(y_dtype));
   if (!valid_scale(scale_type)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown scale type %d", int(scale_type));
   tb_status st = check_fp8_dims(m, out_dim, in_dim, 16);
   if (st != TB_OK) return st;
@@ -744,7 +745,7 @@ tb_status tb_dense_forward_fp8_workspace_size(int64_t m, int64_t out_dim, int64_
   if (m == 0) return ok();
   int cus = 0;
   if (int e = device_cu_count(&cus)) return hip_fail(hipError_t(e), "querying the compute-unit count");
-  *bytes_out = plan_fp8(m, out_dim, in_dim, x_dtype == TB_E4M3, scale_type, cus).bytes;
+  *bytes_out = plan_fp8(m, out_dim, in_dim, x_dtype == TB_E4M3, y_dtype, scale_type, cus).bytes;
   return ok();
 }
 
@@ -767,7 +768,7 @@ tb_status tb_dense_forward_fp8(const void* x, const void* x_scale, const void* w
     return fail(TB_ERR_UNSUPPORTED, "scales and y must be aligned to their element size");
   int cus = 0;
   if (int e = device_cu_count(&cus)) return hip_fail(hipError_t(e), "querying the compute-unit count");
-  const Fp8Plan p = plan_fp8(m, out_dim, in_dim, quantised, scale_type, cus);
+  const Fp8Plan p = plan_fp8(m, out_dim, in_dim, quantised, y_dtype, scale_type, cus);
   if (p.bytes > 0) {
     if (!workspace) return fail(TB_ERR_INVALID_ARGUMENT, "workspace must be non-NULL");
     if (!aligned_to(workspace, 256)) return fail(TB_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");

@@ -8,9 +8,9 @@
 //       scale = 2^max(ceil(log2(a / 448)), -127),  q = e4m3(value / scale).
 //     Nothing is rounded but q itself.
 //   fp32 scale, with a' = max(a, 2^-100):
-//       scale = a' / 448,  q = e4m3(value * (448 / a')),
-//     each of the three fp32 operations rounded once.  The floor keeps 448 / a'
-//     finite; a block below it is scaled as if its largest value were 2^-100.
+//       scale = a' * (1 / 448),  q = e4m3(value * (448 * (1 / a'))),
+//     each fp32 operation rounded once.  The floor keeps 448 / a' finite; a
+//     block below it is scaled as if its largest value were 2^-100.
 // q rounds to nearest, ties to even: off by at most 2^-4 of the value (2^-10
 // of the scale below 2^-6 scales).  A block that holds an infinity or NaN gets
 // a NaN scale and NaN in every q: such a value has no finite scale, and a
@@ -57,8 +57,8 @@ __device__ __forceinline__ void block_scale(uint32_t amax, scale_t<SC>& stored, 
     by = finite ? __uint_as_float(uint32_t(254 - e) << 23) : __builtin_nanf("");
   } else {
     const float a = fmaxf(__uint_as_float(amax), kLeast);
-    stored = finite ? a / kMax : __builtin_nanf("");
-    by = finite ? kMax / a : __builtin_nanf("");
+    stored = finite ? a * (1.f / kMax) : __builtin_nanf("");
+    by = finite ? kMax * (1.f / a) : __builtin_nanf("");
   }
 }
 
@@ -134,7 +134,7 @@ __device__ __forceinline__ f32x4 mma(const Operand<true>& a, const Operand<true>
   return c;
 }
 
-__device__ __forceinline__ i32x8 join(const u32x4& lo, const u32x4& hi) {
+__device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi) {
   return i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
 }
 

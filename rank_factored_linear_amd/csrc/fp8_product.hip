@@ -232,7 +232,7 @@ struct GemmArgs {
   int wide;
 };
 
-__device__ __forceinline__ int swz(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
+__device__ __forceinline__ int swz(int row, int piece) { return row * 128 + ((piece ^ ((row >> 1) & 7)) << 4); }
 
 template <int SC, typename YE>
 __global__ __launch_bounds__(kGemmThreads, 2) void fp8_gemm_kernel(GemmArgs a) {
@@ -391,7 +391,8 @@ hipError_t gemm_go(const GemmArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-Fp8Plan plan_fp8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, tb_scale scale_type, int cus) {
+Fp8Plan plan_fp8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, tb_dtype y_dtype, tb_scale scale_type,
+                 int cus) {
   Fp8Plan p{};
   const int64_t KB = fp8_blocks(in_dim);
   p.decode = m <= kDecodeMaxTokens;
@@ -404,7 +405,15 @@ Fp8Plan plan_fp8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, tb_
     p.off_xs = at;
     at = align_up(at + size_t(m) * KB * (scale_type == TB_SCALE_E8M0 ? 1 : 4), 256);
   }
-  if (!p.decode) {
+  // The 256 x 256 kernel makes bf16 results, needs tiles for half the compute
+  // units and addresses a tile's rows with 31-bit offsets.
+  p.big = !p.decode && y_dtype == TB_BF16 && in_dim <= (int64_t(1) << 31) / 256 - 128 &&
+          ((m + 255) / 256) * ((out_dim + 255) / 256) * 2 >= cus;
+  if (p.big) {
+    p.tile = plan_fp8_tiles(m, out_dim, in_dim, cus);
+    p.off_part = at;
+    at += p.tile.part_bytes;
+  } else if (!p.decode) {
     p.tiles_m = int((m + kTile - 1) / kTile);
     p.tiles_n = int((out_dim + kTile - 1) / kTile);
     const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
@@ -441,6 +450,9 @@ hipError_t launch_fp8_product(const Fp8Plan& p, tb_dtype x_dtype, tb_dtype y_dty
       return e8 ? decode_x<TB_SCALE_E8M0, bf16_t>(x_dtype, a, stream) : decode_x<TB_SCALE_F32, bf16_t>(x_dtype, a, stream);
     return e8 ? decode_x<TB_SCALE_E8M0, float>(x_dtype, a, stream) : decode_x<TB_SCALE_F32, float>(x_dtype, a, stream);
   }
+  if (p.big)
+    return launch_fp8_tiles(p.tile, scale_type, x, xs, w, ws, y, reinterpret_cast<float*>(data + p.off_part), m,
+                            out_dim, in_dim, stream);
   const GemmArgs a{static_cast<const uint8_t*>(x), xs, static_cast<const uint8_t*>(w), ws, y,
                    reinterpret_cast<float*>(data + p.off_part), int(m), int(out_dim), int(in_dim), KB, p.tiles_m,
                    p.tiles_n, p.S, wide};

@@ -192,14 +192,29 @@ hipError_t launch_rebuild_blocks(tb_dtype dtype, tb_scale scale_type, const void
 // Up to this many tokens the few-token kernel quantises x itself.
 constexpr int kFp8FusedTokens = 16;
 
+// The 256 x 256 tiles of the many-token kernel for bf16 results.
+struct Fp8TilePlan {
+  int tiles_m, tiles_n;
+  int split_tiles, S;   // the first split_tiles tiles are cut into S slices of in_dim
+  int grid, xcd_major;
+  size_t part_bytes;
+};
+Fp8TilePlan plan_fp8_tiles(int64_t m, int64_t out_dim, int64_t in_dim, int cus);
+hipError_t launch_fp8_tiles(const Fp8TilePlan& p, tb_scale scale_type, const void* x, const void* xs, const void* w,
+                            const void* ws, void* y, float* part, int64_t m, int64_t out_dim, int64_t in_dim,
+                            hipStream_t stream);
+
 struct Fp8Plan {
   int decode;              // 1: the few-token kernel (m <= kDecodeMaxTokens)
   int fused;               // x is quantised inside it
-  int tiles_m, tiles_n, S; // tiles of the many-token kernel and slices of in_dim
+  int big;                 // 1: the 256 x 256 tiles of `tile`; 0: 128 x 128 tiles
+  Fp8TilePlan tile;
+  int tiles_m, tiles_n, S; // 128 x 128 tiles and slices of in_dim
   size_t off_xq, off_xs, off_part, bytes;   // Q(x), its scales and the slices' sums in the workspace
 };
 // quantised: x comes in e4m3 with its scales.
-Fp8Plan plan_fp8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, tb_scale scale_type, int cus);
+Fp8Plan plan_fp8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, tb_dtype y_dtype, tb_scale scale_type,
+                 int cus);
 hipError_t launch_fp8_product(const Fp8Plan& p, tb_dtype x_dtype, tb_dtype y_dtype, tb_scale scale_type, const void* x,
                               const void* xs, const void* w, const void* ws, void* y, int64_t m, int64_t out_dim,
                               int64_t in_dim, char* data, hipStream_t stream);
