@@ -69,7 +69,7 @@ typedef enum tb_scale {
 #define TB_FP8_BLOCK 128
 
 /* Largest in_dim of the 8-bit calls. */
-#define TB_FP8_MAX_IN_DIM (1 << 25)
+#define TB_FP8_MAX_IN_DIM (1 << 22)
 
 /* Largest head of tb_head_norm_rotate, and most heads of one token over all parts. */
 #define TB_MAX_HEAD_DIM 1024

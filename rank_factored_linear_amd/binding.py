@@ -21,7 +21,7 @@ TB_OK, TB_ERR_INVALID_ARGUMENT, TB_ERR_UNSUPPORTED, TB_ERR_HIP = 0, 1, 2, 3
 TB_F32, TB_BF16, TB_E4M3 = 0, 1, 2
 TB_SCALE_F32, TB_SCALE_E8M0 = 0, 1
 FP8_BLOCK = 128
-FP8_MAX_IN_DIM = 1 << 25
+FP8_MAX_IN_DIM = 1 << 22
 MAX_HEAD_DIM = 1024
 MAX_HEADS = 65535
 MAX_GROUP = 8

@@ -37,19 +37,24 @@ __device__ __forceinline__ void store_out4(YE* y, const f32x4& v, int n, bool wi
 // ---------------------------------------------------------------------------
 // Few tokens (m <= 64): the weight streams once, at HBM rate.
 //
-// A workgroup owns 16 RT output rows and its eight waves split in_dim into
-// contiguous runs of blocks, so that even a small weight keeps every compute
-// unit loading; the eight fp32 partials meet in LDS and are added in wave
-// order (no atomics, no workspace).  Fragments go from global memory straight
-// into registers, kDepth blocks ahead: each weight byte is used once.  A lane's
-// 32 bytes of a block are two 16-byte pieces 64 apart, so that one load of a
-// wave covers 64 contiguous bytes of each of 16 rows.
-// XE uint8_t: x comes in e4m3 with its scales.  XE bf16_t or float: each wave
-// quantises the blocks it multiplies, in registers: a block of 16 tokens sits
-// in its 64 lanes exactly as the product wants it, so the block's maximum is
-// two cross-lane steps and no launch or memory is spent on Q(x).
+// Each workgroup owns an equal share of the output rows (decode_rows), in tiles
+// of 16 that need not be full: rows past its share are not loaded.  Its eight
+// waves take blocks of 128 columns in turn, so that together they read runs of
+// a kilobyte of each row (against a contiguous range for each wave: 53 -> 45 us
+// at 64 x 21504 x 5376); the eight fp32 partials meet in LDS and are added in
+// a fixed order (no atomics, no workspace).  Weights go from global memory
+// straight into registers, kDepth blocks ahead: each byte is used once.  A
+// lane's 32 bytes of a block are two 16-byte pieces 64 apart, so that one load
+// of a wave covers 64 contiguous bytes of each of 16 rows.
+//
+// Bound by HBM for large weights (4 x 21504 x 5376: 24.7 us, 4.7 TB/s, 92% of
+// a large copy's rate; 1 x 5376 x 21504: 28.3 us, 4.1 TB/s), by latency for
+// small ones (1 x 1536 x 1152: 4.0 us), and from 33 tokens on by the reads of x,
+// which every workgroup repeats (64 x 21504 x 5376: 47 us).
 // ---------------------------------------------------------------------------
 constexpr int kDecodeWaves = 8;
+constexpr int kDecodeLdsX = 32768;   // bytes of Q(x) a workgroup keeps in LDS
+constexpr int kDepth = 2;            // blocks of each wave in flight (3 and 4 gained nothing and cost occupancy)
 
 struct DecodeArgs {
   const void* x;
@@ -59,43 +64,74 @@ struct DecodeArgs {
   void* y;
   int M, O, I, KB;
   int wide;  // y rows can be written four outputs at a time
+  int rows;  // output rows of a workgroup
 };
 
-template <typename XE> struct XFrag;
-template <> struct XFrag<uint8_t> { u32x4 lo, hi; };
-template <> struct XFrag<bf16_t> { Frag8<bf16_t> f[4]; };
-template <> struct XFrag<float> { Frag8<float> f[4]; };
+constexpr unsigned kRsrcFlags = 0x00020000u;  // buffer descriptor word 3: 32-bit data format
+constexpr int kPast = int(0x80000000u);       // offset past every buffer: the load returns zeros
 
-// The lane's two 16-element pieces of a row's block at p (element pointer),
-// 64 elements apart; a piece past the row's end reads as zeros.
+// Loads go through buffer descriptors: rows, pieces and blocks past the end are
+// given an offset past the buffer and read as zeros, without a branch that
+// would keep the compiler from having many loads in flight.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, int(bytes), kRsrcFlags);
+}
+
+template <typename XE> struct XFrag;
+template <> struct XFrag<uint8_t> { u32x4 v[2]; };
+template <> struct XFrag<bf16_t> { u32x4 v[4]; };
+template <> struct XFrag<float> { u32x4 v[8]; };
+
+// The lane's two 16-element pieces of a row's block, 64 elements apart: at lo
+// and hi (bytes from the descriptor's base, plus soff).
 template <typename XE>
-__device__ __forceinline__ XFrag<XE> load_x(const XE* p, bool lo, bool hi) {
-  XFrag<XE> r;
-  if constexpr (sizeof(XE) == 1) {
-    r.lo = lo ? *reinterpret_cast<const u32x4*>(p) : u32x4{0, 0, 0, 0};
-    r.hi = hi ? *reinterpret_cast<const u32x4*>(p + 64) : u32x4{0, 0, 0, 0};
-  } else {
-    r.f[0] = load_frag_if<XE>(p, lo);
-    r.f[1] = load_frag_if<XE>(p + 8, lo);
-    r.f[2] = load_frag_if<XE>(p + 64, hi);
-    r.f[3] = load_frag_if<XE>(p + 72, hi);
+__device__ __forceinline__ XFrag<XE> load_x(__amdgpu_buffer_rsrc_t r, int lo, int hi, int soff) {
+  constexpr int kN = int(sizeof(XE));   // 16-byte loads per piece
+  XFrag<XE> f;
+#pragma unroll
+  for (int j = 0; j < kN; ++j) {
+    f.v[j] = __builtin_amdgcn_raw_buffer_load_b128(r, lo + 16 * j, soff, 0);
+    f.v[kN + j] = __builtin_amdgcn_raw_buffer_load_b128(r, hi + 16 * j, soff, 0);
   }
-  return r;
+  return f;
+}
+
+__device__ __forceinline__ void unpack_x(const XFrag<bf16_t>& f, float (&t)[4][8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      t[j][2 * e] = __uint_as_float(f.v[j][e] << 16);
+      t[j][2 * e + 1] = __uint_as_float(f.v[j][e] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void unpack_x(const XFrag<float>& f, float (&t)[4][8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[j / 2][(j % 2) * 4 + e] = __uint_as_float(f.v[j][e]);
+}
+
+template <int SC>
+__device__ __forceinline__ scale_t<SC> load_scale(__amdgpu_buffer_rsrc_t r, int off, int soff) {
+  if constexpr (SC == TB_SCALE_E8M0)
+    return __builtin_amdgcn_raw_buffer_load_b8(r, off, soff, 0);
+  else
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off * 4, soff * 4, 0));
 }
 
 template <typename XE, int SC>
 __device__ __forceinline__ i32x8 operand_x(const XFrag<XE>& r, float& scale) {
   if constexpr (sizeof(XE) == 1) {
-    return join(r.lo, r.hi);
+    return join(r.v[0], r.v[1]);
   } else {
     float t[4][8];
     uint32_t a = 0;
+    unpack_x(r, t);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      unpack8(r.f[j], t[j]);
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int e = 0; e < 8; ++e) a = max(a, abs_bits(t[j][e]));
-    }
     a = max(a, uint32_t(__shfl_xor(int(a), 16)));
     a = max(a, uint32_t(__shfl_xor(int(a), 32)));
     scale_t<SC> st;
@@ -112,29 +148,64 @@ __device__ __forceinline__ i32x8 operand_x(const XFrag<XE>& r, float& scale) {
   }
 }
 
-template <int SC, int NT, int RT, typename XE, typename YE>
+// Where the products' x comes from.
+enum XMode {
+  kXGiven,      // e4m3 in memory
+  kXInRegs,     // quantised by every wave, in the registers that hold a block
+  kXInLds,      // quantised by every wave into LDS, token by token
+};
+
+// kXInLds: a wave's blocks w, w + 8, .. of every token, 16 lanes to a block as
+// in quantize_rows_kernel, into LDS ([token][block][128] and [token][block]
+// scales).  Nobody else reads them.
+template <int SC, typename XE>
+__device__ __forceinline__ void quantise_run(const DecodeArgs& a, int w, int nkb, uint8_t* xq, float* xs) {
+  const int l = int(threadIdx.x) % kWave;
+  const int passes = (nkb + 3) / 4;
+  for (int j = 0; j < a.M * passes; ++j) {
+    const int t = j / passes, b = (j % passes) * 4 + (l >> 4), c = (w + b * kDecodeWaves) * kBlock + (l & 15) * 8;
+    float f[8];
+    unpack8(load_frag_if<XE>(static_cast<const XE*>(a.x) + size_t(t) * a.I + c, b < nkb && c < a.I), f);
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, abs_bits(f[e]));
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) m = max(m, uint32_t(__shfl_xor(int(m), d)));
+    scale_t<SC> st;
+    float by;
+    block_scale<SC>(m, st, by);
+    if (b < nkb) {
+      *reinterpret_cast<u32x2*>(xq + (t * nkb + b) * kBlock + (l & 15) * 8) =
+          u32x2{pack4(f[0] * by, f[1] * by, f[2] * by, f[3] * by), pack4(f[4] * by, f[5] * by, f[6] * by, f[7] * by)};
+      if ((l & 15) == 0) xs[t * nkb + b] = scale_value(st);
+    }
+  }
+}
+
+template <int SC, int NT, int RT, int XM, typename XE, typename YE>
 __global__ __launch_bounds__(kDecodeWaves* kWave) void fp8_decode_kernel(DecodeArgs a) {
-  constexpr bool kFused = sizeof(XE) != 1, kExact = sizeof(YE) == 4;
-  constexpr int kDepth = NT * sizeof(XE) >= 4 ? 2 : 4;
-  __shared__ f32x4 red[kDecodeWaves][RT * NT][kWave];
+  constexpr bool kExact = sizeof(YE) == 4;
+  __shared__ f32x4 red[kDecodeWaves / 2][RT * NT][kWave];
+  __shared__ __attribute__((aligned(16))) uint8_t xlds[XM == kXInLds ? kDecodeLdsX : 16];
+  __shared__ float xslds[XM == kXInLds ? kDecodeLdsX / kBlock : 1];
   const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave), l = int(threadIdx.x) % kWave;
   const int lr = l & 15, kq = (l >> 4) * 16;
-  const int o0 = int(blockIdx.x) * 16 * RT;
-  const int kb0 = int(int64_t(w) * a.KB / kDecodeWaves), kb1 = int(int64_t(w + 1) * a.KB / kDecodeWaves);
-  const scale_t<SC>* ws = static_cast<const scale_t<SC>*>(a.ws) + size_t(o0 / kBlock) * a.KB;
+  const int o0 = int(blockIdx.x) * a.rows, rows = min(a.rows, a.O - o0);   // rows <= 16 RT
+  // The waves take blocks in turn, so that together they read runs of a
+  // kilobyte of each row.
+  const int nkb = (a.KB - w + kDecodeWaves - 1) / kDecodeWaves;   // this wave's blocks w, w + 8, ..
 
-  // Rows and tokens past the end repeat the last one; their results are not stored.
-  const uint8_t* wp[RT];
-  const XE* xp[NT];
-  const scale_t<SC>* xsp[NT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) wp[r] = a.w + size_t(min(o0 + r * 16 + lr, a.O - 1)) * a.I + kq;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int t = min(n * 16 + lr, a.M - 1);
-    xp[n] = static_cast<const XE*>(a.x) + size_t(t) * a.I + kq;
-    if constexpr (!kFused) xsp[n] = static_cast<const scale_t<SC>*>(a.xs) + size_t(t) * a.KB;
-  }
+  const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + size_t(o0) * a.I, int64_t(rows) * a.I);
+  const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x, int64_t(a.M) * a.I * int(sizeof(XE)));
+  const __amdgpu_buffer_rsrc_t rxs = rows_rsrc(a.xs, int64_t(a.M) * a.KB * int(sizeof(scale_t<SC>)));
+  // The rows lie in one weight block or, from row `edge` on, in the next one too.
+  const int edge = kBlock - o0 % kBlock;
+  const bool two = edge < rows;
+  const __amdgpu_buffer_rsrc_t rws = rows_rsrc(static_cast<const scale_t<SC>*>(a.ws) + size_t(o0 / kBlock) * a.KB,
+                                               int64_t(two ? 2 : 1) * a.KB * int(sizeof(scale_t<SC>)));
+  const int wrow = lr * a.I + kq;
+  const int lds0 = a.M * (w * (a.KB / kDecodeWaves) + min(w, a.KB % kDecodeWaves));   // blocks of the waves before
+  const int xrow = (lr * a.I + kq) * int(sizeof(XE));
 
   f32x4 acc[RT][NT];
 #pragma unroll
@@ -144,67 +215,123 @@ __global__ __launch_bounds__(kDecodeWaves* kWave) void fp8_decode_kernel(DecodeA
 
   struct Stage {
     u32x4 lo[RT], hi[RT];
-    XFrag<XE> x[NT];
-    scale_t<SC> xs[NT];
-    scale_t<SC> ws;
+    XFrag<XE> x[XM == kXInLds ? 1 : NT];
+    scale_t<SC> xs[NT], ws[2];
   } st[kDepth];
 
-  auto fetch = [&](Stage& s, int kb) {
-    const int k = kb * kBlock;
-    const bool lo = k + kq < a.I, hi = k + kq + 64 < a.I;   // I % 16 == 0: a piece is all in or all out
+  auto fetch = [&](Stage& s, int i) {
+    const int kb = w + i * kDecodeWaves, k = kb * kBlock, left = a.I - k;   // I % 16 == 0: a piece is all in or all out
+    const bool lo = kq < left, hi = kq + 64 < left;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      s.lo[r] = lo ? *reinterpret_cast<const u32x4*>(wp[r] + k) : u32x4{0, 0, 0, 0};
-      s.hi[r] = hi ? *reinterpret_cast<const u32x4*>(wp[r] + k + 64) : u32x4{0, 0, 0, 0};
+      s.lo[r] = __builtin_amdgcn_raw_buffer_load_b128(rw, lo ? wrow : kPast, k + r * 16 * a.I, 0);
+      s.hi[r] = __builtin_amdgcn_raw_buffer_load_b128(rw, hi ? wrow + 64 : kPast, k + r * 16 * a.I, 0);
     }
+    if constexpr (XM != kXInLds) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      s.x[n] = load_x<XE>(xp[n] + k, lo, hi);
-      if constexpr (!kFused) s.xs[n] = xsp[n][kb];
+      for (int n = 0; n < NT; ++n)
+        s.x[n] = load_x<XE>(rx, lo ? xrow : kPast, hi ? xrow + 64 * int(sizeof(XE)) : kPast,
+                            (k + n * 16 * a.I) * int(sizeof(XE)));
     }
-    s.ws = ws[kb];
+    if constexpr (XM == kXGiven) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s.xs[n] = load_scale<SC>(rxs, lr * a.KB, kb + n * 16 * a.KB);
+    }
+    s.ws[0] = load_scale<SC>(rws, 0, kb);
+    s.ws[1] = load_scale<SC>(rws, 0, kb + a.KB);   // (past the descriptor where there is one block: zero)
   };
-  auto multiply = [&](const Stage& s) {
-    const float wsc = scale_value(s.ws);
+  auto multiply = [&](const Stage& s, int i) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float xsc = 0.f;
-      const Operand<kExact> xv = operand<kExact>(operand_x<XE, SC>(s.x[n], xsc));
-      if constexpr (!kFused) xsc = scale_value(s.xs[n]);
-      const float sc = xsc * wsc;
+      float xsc;
+      i32x8 xb;
+      if constexpr (XM == kXInLds) {
+        // Tokens past the last repeat it; their results are not stored.
+        const int t = min(n * 16 + lr, a.M - 1), at = lds0 + t * nkb + i;
+        const uint8_t* p = xlds + at * kBlock + kq;
+        xb = join(*reinterpret_cast<const u32x4*>(p), *reinterpret_cast<const u32x4*>(p + 64));
+        xsc = xslds[at];
+      } else {
+        xb = operand_x<XE, SC>(s.x[n], xsc);
+        if constexpr (XM == kXGiven) xsc = scale_value(s.xs[n]);
+      }
+      const Operand<kExact> xv = operand<kExact>(xb);
+      if constexpr (NT == 1) {
+        const float s0 = xsc * scale_value(s.ws[0]);
+        if (!two) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        acc[r][n] += mma(operand<kExact>(join(s.lo[r], s.hi[r])), xv) * sc;
+          for (int r = 0; r < RT; ++r) acc[r][n] += mma(operand<kExact>(join(s.lo[r], s.hi[r])), xv) * s0;
+        } else {
+          const float s1 = xsc * scale_value(s.ws[1]);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const f32x4 p = mma(operand<kExact>(join(s.lo[r], s.hi[r])), xv);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[r][n][e] += p[e] * (r * 16 + (l >> 4) * 4 + e < edge ? s0 : s1);
+          }
+        }
+      } else {
+        // Workgroups start at multiples of four rows here: a lane's four share a scale.
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          acc[r][n] += mma(operand<kExact>(join(s.lo[r], s.hi[r])), xv) *
+                       (xsc * scale_value(r * 16 + (l >> 4) * 4 < edge ? s.ws[0] : s.ws[1]));
       }
     }
   };
 
 #pragma unroll
   for (int d = 0; d < kDepth; ++d)
-    if (kb0 + d < kb1) fetch(st[d], kb0 + d);
-  for (int kb = kb0; kb < kb1; kb += kDepth) {
+    if (d < nkb) fetch(st[d], d);
+  // The first weight blocks are on their way while x is quantised.
+  if constexpr (XM == kXInLds)
+    quantise_run<SC, XE>(a, w, nkb, xlds + lds0 * kBlock, xslds + lds0);
+  // Rounds without a branch: a branch around a refill would make the compiler
+  // wait for the refill itself before it uses the next stage.
+  int i = 0;
+  for (; i + 2 * kDepth <= nkb; i += kDepth) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-      if (kb + d < kb1) {
-        multiply(st[d]);
-        if (kb + d + kDepth < kb1) fetch(st[d], kb + d + kDepth);
+      multiply(st[d], i + d);
+      __builtin_amdgcn_sched_barrier(0);
+      fetch(st[d], i + d + kDepth);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  for (; i < nkb; i += kDepth) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      if (i + d < nkb) {
+        multiply(st[d], i + d);
+        if (i + d + kDepth < nkb) fetch(st[d], i + d + kDepth);
       }
     }
   }
 
+  // The eight waves' sums, added in a fixed order: wave w + 4's to wave w's,
+  // then those four.
+  if (w >= kDecodeWaves / 2) {
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) red[w][r * NT + n][l] = acc[r][n];
+      for (int n = 0; n < NT; ++n) red[w - kDecodeWaves / 2][r * NT + n][l] = acc[r][n];
+  }
+  __syncthreads();
+  if (w < kDecodeWaves / 2) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) red[w][r * NT + n][l] += acc[r][n];
+  }
   __syncthreads();
   for (int j = int(threadIdx.x); j < RT * NT * kWave; j += kDecodeWaves * kWave) {
     const int tile = j / kWave, ln = j % kWave;
     f32x4 v = red[0][tile][ln];
 #pragma unroll
-    for (int q = 1; q < kDecodeWaves; ++q) v += red[q][tile][ln];
-    const int t = (tile % NT) * 16 + (ln & 15), o = o0 + (tile / NT) * 16 + (ln >> 4) * 4;
-    if (t < a.M && o < a.O)
-      store_out4(static_cast<YE*>(a.y) + size_t(t) * a.O + o, v, a.O - o, a.wide && o + 4 <= a.O);
+    for (int q = 1; q < kDecodeWaves / 2; ++q) v += red[q][tile][ln];
+    const int t = (tile % NT) * 16 + (ln & 15), o = (tile / NT) * 16 + (ln >> 4) * 4;
+    if (t < a.M && o < rows)
+      store_out4(static_cast<YE*>(a.y) + size_t(t) * a.O + o0 + o, v, rows - o, a.wide && o + 4 <= rows);
   }
 }
 
@@ -353,29 +480,66 @@ __global__ __launch_bounds__(kGemmThreads) void fp8_join_kernel(GemmArgs a) {
   }
 }
 
-template <int SC, int NT, int RT, typename XE, typename YE>
+template <int SC, int NT, int RT, int XM, typename XE, typename YE>
 hipError_t decode_go(const DecodeArgs& a, hipStream_t stream) {
-  const dim3 grid(unsigned((a.O + 16 * RT - 1) / (16 * RT)));
-  hipLaunchKernelGGL((fp8_decode_kernel<SC, NT, RT, XE, YE>), grid, dim3(kDecodeWaves * kWave), 0, stream, a);
+  const dim3 grid(unsigned((a.O + a.rows - 1) / a.rows));
+  hipLaunchKernelGGL((fp8_decode_kernel<SC, NT, RT, XM, XE, YE>), grid, dim3(kDecodeWaves * kWave), 0, stream, a);
   return hipGetLastError();
 }
 
-template <int SC, typename XE, typename YE>
-hipError_t decode_typed(const DecodeArgs& a, hipStream_t stream) {
-  if (a.M <= 16) return decode_go<SC, 1, 1, XE, YE>(a, stream);
-  if constexpr (sizeof(XE) == 1) {
-    if (a.M <= 32) return decode_go<SC, 2, 1, XE, YE>(a, stream);
-    return decode_go<SC, 4, 1, XE, YE>(a, stream);
-  }
+template <int SC, int NT, typename YE>
+hipError_t decode_given(const DecodeArgs& a, hipStream_t stream) {
+  const int rt = (a.rows + 15) / 16;
+  if (rt == 1) return decode_go<SC, NT, 1, kXGiven, uint8_t, YE>(a, stream);
+  if (rt == 2) return decode_go<SC, NT, 2, kXGiven, uint8_t, YE>(a, stream);
+  if (rt == 3) return decode_go<SC, NT, 3, kXGiven, uint8_t, YE>(a, stream);
+  if constexpr (NT <= 2)
+    if (rt == 4) return decode_go<SC, NT, 4, kXGiven, uint8_t, YE>(a, stream);
+  if constexpr (NT == 1)
+    if (rt <= 6) return decode_go<SC, NT, 6, kXGiven, uint8_t, YE>(a, stream);
   return hipErrorInvalidValue;
+}
+
+// Up to 16 tokens, quantised in the kernel (decode_fused).
+template <int SC, typename XE, typename YE>
+hipError_t decode_quantising(const DecodeArgs& a, hipStream_t stream) {
+  const int rt = (a.rows + 15) / 16;
+  if (rt == 1) return decode_go<SC, 1, 1, kXInLds, XE, YE>(a, stream);
+  if (rt == 2) return decode_go<SC, 1, 2, kXInLds, XE, YE>(a, stream);
+  if (rt == 3) return decode_go<SC, 1, 3, kXInRegs, XE, YE>(a, stream);
+  if (rt == 4) return decode_go<SC, 1, 4, kXInRegs, XE, YE>(a, stream);
+  if (rt <= 6) return decode_go<SC, 1, 6, kXInRegs, XE, YE>(a, stream);
+  return hipErrorInvalidValue;
+}
+
+// Output rows of a workgroup: equal shares of the weight for every compute
+// unit (a unit with twice the rows of another would finish last: a compute
+// unit takes at most ~22 GB/s from HBM here), in as few workgroups per unit as
+// the widest kernel for these tokens allows.
+int decode_rows(int64_t m, int64_t out_dim, int cus) {
+  const int most = m <= 16 ? 96 : m <= 32 ? 64 : 48;
+  const int64_t k = (out_dim + int64_t(cus) * most - 1) / (int64_t(cus) * most);
+  const int64_t rows = (out_dim + cus * k - 1) / (cus * k);
+  return int(m <= 16 ? rows : (rows + 3) / 4 * 4);
+}
+
+// Whether the kernel quantises x itself: always where it can do so while the
+// weights stream (more than 32 rows a workgroup; 16 x 21504 x 5376: 26.9 us
+// against 25.0 and a launch of about 3), and else where Q(x) fits its LDS
+// (1 x 5376 x 21504: 28.3 us against 28.0 and a launch).  Where neither holds
+// the work per workgroup is mostly that quantisation (8 x 1152 x 6912 in fp32:
+// 13.1 us against 7.3 and a launch).
+bool decode_fused(int64_t m, int64_t out_dim, int64_t in_dim, int cus) {
+  return m <= kFp8FusedTokens &&
+         (decode_rows(m, out_dim, cus) > 32 || m * fp8_blocks(in_dim) * kBlock <= kDecodeLdsX);
 }
 
 template <int SC, typename YE>
 hipError_t decode_x(tb_dtype x_dtype, const DecodeArgs& a, hipStream_t stream) {
-  if (x_dtype == TB_E4M3) return decode_typed<SC, uint8_t, YE>(a, stream);
-  // Quantised in the kernel: y has x's type or either.
-  if (x_dtype == TB_BF16) return decode_typed<SC, bf16_t, YE>(a, stream);
-  return decode_typed<SC, float, YE>(a, stream);
+  if (x_dtype == TB_BF16) return decode_quantising<SC, bf16_t, YE>(a, stream);
+  if (x_dtype == TB_F32) return decode_quantising<SC, float, YE>(a, stream);
+  if (a.M <= 16) return decode_given<SC, 1, YE>(a, stream);
+  return a.M <= 32 ? decode_given<SC, 2, YE>(a, stream) : decode_given<SC, 4, YE>(a, stream);
 }
 
 template <int SC, typename YE>
@@ -396,7 +560,8 @@ Fp8Plan plan_fp8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, tb_
   Fp8Plan p{};
   const int64_t KB = fp8_blocks(in_dim);
   p.decode = m <= kDecodeMaxTokens;
-  p.fused = !quantised && m <= kFp8FusedTokens;
+  p.rows = p.decode ? decode_rows(m, out_dim, cus) : 0;
+  p.fused = p.decode && !quantised && decode_fused(m, out_dim, in_dim, cus);
   p.S = 1;
   size_t at = 0;
   if (!quantised && !p.fused) {
@@ -445,7 +610,8 @@ hipError_t launch_fp8_product(const Fp8Plan& p, tb_dtype x_dtype, tb_dtype y_dty
   const int wide = out_dim % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & (4 * ys - 1)) == 0;
   const int KB = int(fp8_blocks(in_dim));
   if (p.decode) {
-    const DecodeArgs a{x, xs, static_cast<const uint8_t*>(w), ws, y, int(m), int(out_dim), int(in_dim), KB, wide};
+    const DecodeArgs a{x, xs, static_cast<const uint8_t*>(w), ws, y, int(m), int(out_dim), int(in_dim), KB,
+                       wide && p.rows % 4 == 0, p.rows};
     if (y_dtype == TB_BF16)
       return e8 ? decode_x<TB_SCALE_E8M0, bf16_t>(x_dtype, a, stream) : decode_x<TB_SCALE_F32, bf16_t>(x_dtype, a, stream);
     return e8 ? decode_x<TB_SCALE_E8M0, float>(x_dtype, a, stream) : decode_x<TB_SCALE_F32, float>(x_dtype, a, stream);

@@ -207,6 +207,7 @@ hipError_t launch_fp8_tiles(const Fp8TilePlan& p, tb_scale scale_type, const voi
 struct Fp8Plan {
   int decode;              // 1: the few-token kernel (m <= kDecodeMaxTokens)
   int fused;               // x is quantised inside it
+  int rows;                // output rows of its workgroups
   int big;                 // 1: the 256 x 256 tiles of `tile`; 0: 128 x 128 tiles
   Fp8TilePlan tile;
   int tiles_m, tiles_n, S; // 128 x 128 tiles and slices of in_dim

@@ -186,7 +186,10 @@ def check_product(y, xq, xs, wq, ws, cols=None):
 
 SIZES = [(1, 1, 16), (1, 16, 128), (1, 130, 1152), (2, 17, 144), (7, 1536, 1152), (16, 256, 6912), (15, 33, 272),
          (17, 100, 400), (32, 128, 1024), (33, 130, 1040), (61, 6912, 1152), (64, 48, 2064), (65, 1, 16), (65, 130, 144),
-         (128, 128, 128), (129, 257, 1168), (200, 1000, 640), (300, 520, 5376), (777, 1152, 1024), (260, 260, 16)]
+         (128, 128, 128), (129, 257, 1168), (200, 1000, 640), (300, 520, 5376), (777, 1152, 1024), (260, 260, 16),
+         # Shares of 33 to 96 rows a workgroup in the few-token kernel, and more than one workgroup a compute unit.
+         (5, 12000, 400), (16, 16001, 272), (3, 21504, 144), (20, 12003, 272), (30, 16000, 144), (40, 12010, 144),
+         (60, 30000, 144), (9, 30001, 1168)]
 
 
 @pytest.mark.parametrize("kind", SCALES)
@@ -209,9 +212,10 @@ def test_product(m, out, n, kind):
 
 
 @pytest.mark.parametrize("kind", SCALES)
-@pytest.mark.parametrize("m", [3, 16, 40, 64, 100, 513])
-def test_product_of_fp32_activations(m, kind):
-    x, wq, ws = operands(m, 390, 1296, kind, dtype=F32)
+@pytest.mark.parametrize("m,out,n", [(3, 390, 1296), (16, 390, 1296), (40, 390, 1296), (64, 390, 1296), (100, 390, 1296),
+                                     (513, 390, 1296), (7, 9000, 272), (16, 16500, 144), (12, 24000, 144), (2, 21, 6912)])
+def test_product_of_fp32_activations(m, out, n, kind):
+    x, wq, ws = operands(m, out, n, kind, dtype=F32)
     xq, xs = tb.quantize_activations(x, SCALES[kind])
     y = tb.dense_forward_fp8(x, wq, ws)
     assert y.dtype == F32
