@@ -9,6 +9,7 @@ library is missing or fails to load, the import raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -144,13 +145,15 @@ def _need_device(*ts):
     """Every tensor lives on the current GPU (the device the library launches on)."""
     dev = None
     for t in ts:
-        if t is not None:
-            if not t.is_cuda:
+        if t is None:
+            continue
+        d = t.get_device()   # -1 on the CPU
+        if dev is None and d >= 0:
+            dev = torch.cuda.current_device()
+        if d != dev or d < 0:
+            if d < 0:
                 raise TBError(TB_ERR_INVALID_ARGUMENT, "tensors must live on the GPU")
-            if dev is None:
-                dev = torch.cuda.current_device()
-            if t.get_device() != dev:
-                raise TBError(TB_ERR_INVALID_ARGUMENT, f"tensor on {t.device}, but the current device is cuda:{dev}")
+            raise TBError(TB_ERR_INVALID_ARGUMENT, f"tensor on {t.device}, but the current device is cuda:{dev}")
 
 
 def _need_cuda(*ts):
@@ -159,6 +162,17 @@ def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_contiguous():
             raise TBError(TB_ERR_UNSUPPORTED, "tensors must be contiguous")
+
+
+def _here(ts: list) -> int:
+    """The device of tensors that are contiguous and live on the current GPU (else _need_cuda says what is wrong)."""
+    dev = ts[0].get_device()
+    fine = dev >= 0 and dev == torch.cuda.current_device()
+    for t in ts:
+        fine = fine and t.get_device() == dev and t.is_contiguous()
+    if not fine:
+        _need_cuda(*ts)
+    return dev
 
 
 # Shape and dtype checks run before the device checks and before anything
@@ -181,7 +195,7 @@ def _expect_out(out: torch.Tensor | None, shape, dtype: torch.dtype | None = Non
 def _output(out: torch.Tensor | None, shape, dtype: torch.dtype, like: torch.Tensor) -> torch.Tensor:
     """A new output of this shape and dtype on like's device, or the caller's `out` after checking it."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     _expect("out", out, shape, dtype)
     if out.device != like.device:
         raise TBError(TB_ERR_INVALID_ARGUMENT, f"out is on {out.device}, the inputs on {like.device}")
@@ -475,30 +489,71 @@ def quantize_activations(x: torch.Tensor, scale_dtype: torch.dtype = torch.float
     code, sc = _dtype_code(x.dtype), _scale_code(scale_dtype)
     m, in_dim = x.shape
     _need_cuda(x)
-    q = torch.empty((m, in_dim), dtype=E4M3, device=x.device)
-    scale = torch.empty((m, _fp8_blocks(in_dim)), dtype=scale_dtype, device=x.device)
+    q = x.new_empty((m, in_dim), dtype=E4M3)
+    scale = x.new_empty((m, _fp8_blocks(in_dim)), dtype=scale_dtype)
     _check(lib.tb_quantize_activations(_ptr(x), _ptr(q), _ptr(scale), m, in_dim, code, sc, _stream()))
     return q, scale
+
+
+# The checks below look at shapes and dtypes only, and a serving loop repeats its shapes: their results are kept by
+# those (a refusal is raised, not kept).
+
+
+def _kind(t: torch.Tensor | None):
+    return None if t is None else (t.shape, t.dtype)
+
+
+def _expect_kind(name: str, kind, shape, dtype: torch.dtype | None = None) -> None:
+    if kind[0] != shape:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, f"{name} must be {list(shape)}, got {list(kind[0])}")
+    if dtype is not None and kind[1] != dtype:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, f"{name} must be {dtype}, got {kind[1]}")
+
+
+@functools.lru_cache(maxsize=4096)
+def _rebuild_fp8_dims(s, W0, U, V, q, scale, scale_dtype):
+    """(out_dim, in_dim, rank, dtype code, scale code, scale shape) of reconstruct_weight_fp8's operands by kind."""
+    shape, dtype = W0
+    if len(shape) != 2:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "W0 must be [out, in]")
+    code = _dtype_code(dtype)
+    out_dim, in_dim = shape
+    if s is not None:
+        _expect_kind("s", s, (out_dim,), dtype)
+    if (U is None) != (V is None):
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "U and V are given together or not at all")
+    rank = 0
+    if U is not None:
+        if len(U[0]) != 2:
+            raise TBError(TB_ERR_INVALID_ARGUMENT, "U must be [out, rank]")
+        rank = U[0][1]
+        _expect_kind("U", U, (out_dim, rank), dtype)
+        _expect_kind("V", V, (in_dim, rank), dtype)
+    sc = _scale_code(scale_dtype)
+    blocks = _fp8_blocks(out_dim), _fp8_blocks(in_dim)
+    if q is not None:
+        _expect_kind("out", q, (out_dim, in_dim), E4M3)
+        _expect_kind("out", scale, blocks, scale_dtype)
+    return out_dim, in_dim, rank, code, sc, blocks
 
 
 def reconstruct_weight_fp8(s: torch.Tensor | None, W0: torch.Tensor, U: torch.Tensor | None, V: torch.Tensor | None,
                            scale_dtype: torch.dtype = torch.float32, out=None) -> tuple:
     """diag(s) @ W0 + U @ V.T as (e4m3 [out, in], scales [ceil(out / 128), ceil(in / 128)]) without forming it wide,
     via tb_reconstruct_weight_fp8 (s None: unit scale; into the pair `out` when given, whose scale dtype wins)."""
-    out_dim, in_dim, rank, U, V = _bundle_dims(s, W0, U, V)
     q = scale = None
     if out is not None:
         q, scale = out
         scale_dtype = scale.dtype
-    sc = _scale_code(scale_dtype)
-    shapes = (out_dim, in_dim), (_fp8_blocks(out_dim), _fp8_blocks(in_dim))
-    _expect_out(q, shapes[0], E4M3)
-    _expect_out(scale, shapes[1], scale_dtype)
-    _need_cuda(s, W0, U, V, q, scale)
-    q = _output(q, shapes[0], E4M3, W0)
-    scale = _output(scale, shapes[1], scale_dtype, W0)
-    _check(lib.tb_reconstruct_weight_fp8(_ptr(s), _ptr(W0), _ptr(U), _ptr(V), _ptr(q), _ptr(scale), out_dim, in_dim,
-                                         rank, _dtype_code(W0.dtype), sc, _stream()))
+    out_dim, in_dim, rank, code, sc, blocks = _rebuild_fp8_dims(_kind(s), _kind(W0), _kind(U), _kind(V), _kind(q),
+                                                                _kind(scale), scale_dtype)
+    dev = _here([t for t in (W0, s, U, V, q, scale) if t is not None])
+    if q is None:
+        q = W0.new_empty((out_dim, in_dim), dtype=E4M3)
+        scale = W0.new_empty(blocks, dtype=scale_dtype)
+    _check(lib.tb_reconstruct_weight_fp8(_ptr(s), W0.data_ptr(), _ptr(U) if rank else None, _ptr(V) if rank else None,
+                                         q.data_ptr(), scale.data_ptr(), out_dim, in_dim, rank, code, sc,
+                                         torch._C._cuda_getCurrentRawStream(dev)))
     return q, scale
 
 
@@ -507,13 +562,45 @@ def quantize_weight(W: torch.Tensor, scale_dtype: torch.dtype = torch.float32, o
     return reconstruct_weight_fp8(None, W, None, None, scale_dtype, out)
 
 
+@functools.lru_cache(maxsize=4096)
+def _fp8_workspace_size(device: int, m: int, out_dim: int, in_dim: int, x_code: int, y_code: int, scale: int) -> int:
+    """By sizes and types (and the device, whose compute units the plan counts): a serving loop asks once per shape."""
+    out = ctypes.c_size_t(0)
+    _check(lib.tb_dense_forward_fp8_workspace_size(m, out_dim, in_dim, x_code, y_code, scale, ctypes.byref(out)))
+    return out.value
+
+
 def dense_forward_fp8_workspace_size(m: int, out_dim: int, in_dim: int, x_dtype: torch.dtype, out_dtype: torch.dtype,
                                      scale_dtype: torch.dtype) -> int:
-    out = ctypes.c_size_t(0)
+    """Bytes of workspace that dense_forward_fp8 takes on the current device for these sizes."""
     code = TB_E4M3 if x_dtype == E4M3 else _dtype_code(x_dtype)
-    _check(lib.tb_dense_forward_fp8_workspace_size(m, out_dim, in_dim, code, _dtype_code(out_dtype),
-                                                   _scale_code(scale_dtype), ctypes.byref(out)))
-    return out.value
+    return _fp8_workspace_size(torch.cuda.current_device(), m, out_dim, in_dim, code, _dtype_code(out_dtype),
+                               _scale_code(scale_dtype))
+
+
+@functools.lru_cache(maxsize=4096)
+def _dense_fp8_dims(x, Wq, w_scale, x_scale, out, out_dtype):
+    """(m, out_dim, in_dim, x code, y code, scale code, y dtype) of dense_forward_fp8's operands by kind."""
+    (x_shape, x_dtype), (w_shape, _) = x, Wq
+    if len(x_shape) != 2 or len(w_shape) != 2:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [m, in] and Wq [out, in]")
+    quantised = x_dtype == E4M3
+    x_code = TB_E4M3 if quantised else _dtype_code(x_dtype)
+    m, in_dim = x_shape
+    out_dim = w_shape[0]
+    _expect_kind("Wq", Wq, (out_dim, in_dim), E4M3)
+    sc = _scale_code(w_scale[1])
+    _expect_kind("w_scale", w_scale, (_fp8_blocks(out_dim), _fp8_blocks(in_dim)))
+    if quantised != (x_scale is not None):
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "x_scale goes with an x in float8_e4m3fn, and only with one")
+    if quantised:
+        _expect_kind("x_scale", x_scale, (m, _fp8_blocks(in_dim)), w_scale[1])
+    if out_dtype is None:
+        out_dtype = out[1] if out is not None else torch.bfloat16 if quantised else x_dtype
+    y_code = _dtype_code(out_dtype)
+    if out is not None:
+        _expect_kind("out", out, (m, out_dim), out_dtype)
+    return m, out_dim, in_dim, x_code, y_code, sc, out_dtype
 
 
 def dense_forward_fp8(x: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, x_scale: torch.Tensor | None = None,
@@ -523,40 +610,21 @@ def dense_forward_fp8(x: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, 
 
     x [m, in] in bfloat16 or float32 is quantised within the call (scales of w_scale's dtype); in float8_e4m3fn it
     comes with x_scale (quantize_activations).  y has out's dtype, out_dtype, x's dtype, or bfloat16 for an e4m3 x."""
-    if x.dim() != 2 or Wq.dim() != 2:
-        raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [m, in] and Wq [out, in]")
-    quantised = x.dtype == E4M3
-    x_code = TB_E4M3 if quantised else _dtype_code(x.dtype)
-    m, in_dim = x.shape
-    out_dim = Wq.shape[0]
-    _expect("Wq", Wq, (out_dim, in_dim), E4M3)
-    sc = _scale_code(w_scale.dtype)
-    _expect("w_scale", w_scale, (_fp8_blocks(out_dim), _fp8_blocks(in_dim)))
-    if quantised != (x_scale is not None):
-        raise TBError(TB_ERR_INVALID_ARGUMENT, "x_scale goes with an x in float8_e4m3fn, and only with one")
-    if quantised:
-        _expect("x_scale", x_scale, (m, _fp8_blocks(in_dim)), w_scale.dtype)
-    if out is not None:
-        out_dtype = out.dtype if out_dtype is None else out_dtype
-    elif out_dtype is None:
-        out_dtype = torch.bfloat16 if quantised else x.dtype
-    y_code = _dtype_code(out_dtype)
-    _expect_out(out, (m, out_dim), out_dtype)
-    _need_cuda(x, Wq, w_scale, x_scale, out)
-    out = _output(out, (m, out_dim), out_dtype, x)
-    ws = workspace
-    if ws is None:
-        size = ctypes.c_size_t(0)
-        _check(lib.tb_dense_forward_fp8_workspace_size(m, out_dim, in_dim, x_code, y_code, sc, ctypes.byref(size)))
-        need = size.value
+    m, out_dim, in_dim, x_code, y_code, sc, y_dtype = _dense_fp8_dims(_kind(x), _kind(Wq), _kind(w_scale),
+                                                                      _kind(x_scale), _kind(out), out_dtype)
+    dev = _here([t for t in (x, Wq, w_scale, x_scale, out, workspace) if t is not None])
+    if out is None:
+        out = x.new_empty((m, out_dim), dtype=y_dtype)
+    if workspace is None:
+        nbytes = _fp8_workspace_size(dev, m, out_dim, in_dim, x_code, y_code, sc)
         # From torch's allocator, per call: it follows the stream and, under graph capture, the graph's own pool,
         # so no two graphs share it.
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-        nbytes = need
+        workspace = x.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
     else:
-        nbytes = _workspace_bytes(ws)
-    _check(lib.tb_dense_forward_fp8(_ptr(x), _ptr(x_scale), _ptr(Wq), _ptr(w_scale), _ptr(out), m, out_dim, in_dim,
-                                    x_code, y_code, sc, _ptr(ws), nbytes, _stream()))
+        nbytes = workspace.numel() * workspace.element_size()
+    _check(lib.tb_dense_forward_fp8(x.data_ptr(), _ptr(x_scale), Wq.data_ptr(), w_scale.data_ptr(), out.data_ptr(), m,
+                                    out_dim, in_dim, x_code, y_code, sc, _ptr(workspace), nbytes,
+                                    torch._C._cuda_getCurrentRawStream(dev)))
     return out
 
 
@@ -566,19 +634,42 @@ def dense_forward_fp8(x: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, 
 
 
 def _rotated_dims(positions, freqs, tokens: int, dim: int) -> int:
-    """rot_dim after checking positions [tokens] and freqs [rot_dim / 2] (both None: 0) against heads of dim."""
+    """rot_dim after checking the kinds of positions [tokens] and freqs [rot_dim / 2] (both None: 0) against heads of
+    dim."""
     if (positions is None) != (freqs is None):
         raise TBError(TB_ERR_INVALID_ARGUMENT, "positions and freqs are given together or not at all")
     if freqs is None:
         return 0
-    if freqs.dim() != 1:
+    if len(freqs[0]) != 1:
         raise TBError(TB_ERR_INVALID_ARGUMENT, "freqs must be [rot_dim / 2]")
-    rot = 2 * freqs.shape[0]
+    rot = 2 * freqs[0][0]
     if rot > dim:
         raise TBError(TB_ERR_INVALID_ARGUMENT, f"{rot} rotated dimensions, but heads of {dim}")
-    _expect("freqs", freqs, (rot // 2,), torch.float64)
-    _expect("positions", positions, (tokens,), torch.int64)
+    _expect_kind("freqs", freqs, (rot // 2,), torch.float64)
+    _expect_kind("positions", positions, (tokens,), torch.int64)
     return rot
+
+
+@functools.lru_cache(maxsize=4096)
+def _heads_dims(parts, positions, freqs, outs):
+    """(tokens, head_dim, rot_dim, dtype code) of head_norm_rotate's operands by kind."""
+    if not 1 <= len(parts) <= MAX_GROUP:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, f"a call takes 1..{MAX_GROUP} parts")
+    if outs is not None and len(outs) != len(parts):
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "one output per part")
+    for (shape, _), _ in parts:
+        if len(shape) != 3:
+            raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [tokens, heads, head_dim]")
+    (tokens, _, dim), dtype = parts[0][0]
+    code = _dtype_code(dtype)
+    rot = _rotated_dims(positions, freqs, tokens, dim)
+    for j, (x, w) in enumerate(parts):
+        _expect_kind(f"part {j}", x, (tokens, x[0][1], dim), dtype)
+        if w is not None:
+            _expect_kind("weight", w, (dim,), dtype)
+        if outs is not None:
+            _expect_kind("out", outs[j], x[0], dtype)
+    return tokens, dim, rot, code
 
 
 def head_norm_rotate(parts, positions: torch.Tensor | None, freqs: torch.Tensor | None, eps: float = 1e-6,
@@ -589,45 +680,40 @@ def head_norm_rotate(parts, positions: torch.Tensor | None, freqs: torch.Tensor 
     be strided (a view of packed rows) with adjacent elements.  positions int64 [tokens], freqs float64 [rot_dim / 2]
     (radians per position; both None: no rotation).  Returns new tensors, or writes `outs` (x itself for in place, or
     a view of a cache)."""
-    if not 1 <= len(parts) <= MAX_GROUP:
-        raise TBError(TB_ERR_INVALID_ARGUMENT, f"a call takes 1..{MAX_GROUP} parts")
-    if outs is not None and len(outs) != len(parts):
-        raise TBError(TB_ERR_INVALID_ARGUMENT, "one output per part")
-    x0 = parts[0][0]
-    if x0.dim() != 3:
-        raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [tokens, heads, head_dim]")
-    code = _dtype_code(x0.dtype)
-    tokens, _, dim = x0.shape
-    rot = _rotated_dims(positions, freqs, tokens, dim)
-    dtype, weight_shape = x0.dtype, (dim,)
-    for j, (x, w) in enumerate(parts):
-        if x.dim() != 3:
-            raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [tokens, heads, head_dim]")
-        if j:
-            _expect(f"part {j}", x, (tokens, x.shape[1], dim), dtype)
-        if w is not None:
-            _expect("weight", w, weight_shape, dtype)
-        if outs is not None:
-            _expect("out", outs[j], x.shape, dtype)
-    _need_cuda(positions, freqs, *(w for _, w in parts))
-    _need_device(*(x for x, _ in parts), *(outs or ()))
+    tokens, dim, rot, code = _heads_dims(tuple([(_kind(x), _kind(w)) for x, w in parts]), _kind(positions),
+                                         _kind(freqs), None if outs is None else tuple([_kind(y) for y in outs]))
+    dev = parts[0][0].get_device()
+    fine = dev >= 0 and dev == torch.cuda.current_device()
     ys, fields = [], []
     for j, (x, w) in enumerate(parts):
+        heads = x.shape[1]
         xt, xh, xe = x.stride()
-        if outs is None:
-            y = torch.empty(x.shape, dtype=dtype, device=x.device)
-            yt, yh, ye = x.shape[1] * dim, dim, 1
-        else:
+        fine = fine and x.get_device() == dev
+        if outs is not None:
             y = outs[j]
             yt, yh, ye = y.stride()
+            fine = fine and y.get_device() == dev
+        else:
+            y = x.new_empty((tokens, heads, dim)) if fine else x
+            yt, yh, ye = heads * dim, dim, 1
         if (xe != 1 or ye != 1) and dim > 1:
             raise TBError(TB_ERR_UNSUPPORTED, "the elements of a head must be adjacent")
+        wp = 0
+        if w is not None:
+            wp = w.data_ptr()
+            fine = fine and w.get_device() == dev and w.is_contiguous()
         # tb_head_part, every field eight bytes
-        fields += (x.data_ptr(), y.data_ptr(), 0 if w is None else w.data_ptr(), x.shape[1], xt, xh, yt, yh)
+        fields += (x.data_ptr(), y.data_ptr(), wp, heads, xt, xh, yt, yh)
         ys.append(y)
-    _check(lib.tb_head_norm_rotate(len(parts), (ctypes.c_int64 * len(fields))(*fields), tokens, dim, rot,
-                                   int(interleaved), _ptr(positions), _ptr(freqs), eps, weight_offset, code,
-                                   _stream()))
+    if rot:
+        fine = (fine and positions.get_device() == dev and freqs.get_device() == dev and positions.is_contiguous()
+                and freqs.is_contiguous())
+    if not fine:
+        _need_device(*[x for x, _ in parts], *ys)
+        _need_cuda(positions, freqs, *[w for _, w in parts])
+    _check(lib.tb_head_norm_rotate(len(parts), (ctypes.c_int64 * len(fields))(*fields), tokens, dim, rot, interleaved,
+                                   _ptr(positions), _ptr(freqs), eps, weight_offset, code,
+                                   torch._C._cuda_getCurrentRawStream(dev)))
     return ys
 
 
@@ -645,7 +731,7 @@ def qkv_forward(x: torch.Tensor, q, k, v, head_dim: int, positions: torch.Tensor
     for name, p in zip("qkv", (q, k, v)):
         if head_dim < 1 or p[at].dim() != 2 or p[at].shape[0] % head_dim:
             raise TBError(TB_ERR_INVALID_ARGUMENT, f"{name}: {list(p[at].shape)} is not rows of heads of {head_dim}")
-    _rotated_dims(positions, freqs, x.shape[0], head_dim)
+    _rotated_dims(_kind(positions), _kind(freqs), x.shape[0], head_dim)
     for w in (q_weight, k_weight):
         if w is not None:
             _expect("head weight", w, (head_dim,), x.dtype)

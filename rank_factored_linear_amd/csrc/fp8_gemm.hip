@@ -385,8 +385,8 @@ __device__ __forceinline__ void store_tile(const Args& a, int m0, int n0, const 
       for (int i = 0; i < 4; ++i) {
         const f32x4& v = acc[4 * h + i][j];
         *reinterpret_cast<lds_u32x2*>(wr + i * 32) =
-            u32x2{f32_to_bf16(v[0]) | (uint32_t(f32_to_bf16(v[1])) << 16),
-                  f32_to_bf16(v[2]) | (uint32_t(f32_to_bf16(v[3])) << 16)};
+            u32x2{pack_bf16(v[0], v[1]),
+                  pack_bf16(v[2], v[3])};
       }
       // A wave reads back what it wrote itself, and its LDS operations complete in order.
       asm volatile("" ::: "memory");
@@ -467,8 +467,8 @@ __global__ __launch_bounds__(kThreads) void fp8_tiles_join_kernel(Args a) {
     if (t >= a.M || o >= a.O) continue;
     bf16_t* dst = a.y + size_t(t) * a.O + o;
     if (a.wide) {
-      *reinterpret_cast<u32x2*>(dst) = u32x2{f32_to_bf16(sum[j][0]) | (uint32_t(f32_to_bf16(sum[j][1])) << 16),
-                                             f32_to_bf16(sum[j][2]) | (uint32_t(f32_to_bf16(sum[j][3])) << 16)};
+      *reinterpret_cast<u32x2*>(dst) = u32x2{pack_bf16(sum[j][0], sum[j][1]),
+                                             pack_bf16(sum[j][2], sum[j][3])};
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)

@@ -21,8 +21,8 @@ template <typename YE>
 __device__ __forceinline__ void store_out4(YE* y, const f32x4& v, int n, bool wide) {
   if constexpr (sizeof(YE) == 2) {
     if (wide) {
-      *reinterpret_cast<u32x2*>(y) = u32x2{f32_to_bf16(v[0]) | (uint32_t(f32_to_bf16(v[1])) << 16),
-                                           f32_to_bf16(v[2]) | (uint32_t(f32_to_bf16(v[3])) << 16)};
+      *reinterpret_cast<u32x2*>(y) = u32x2{pack_bf16(v[0], v[1]),
+                                           pack_bf16(v[2], v[3])};
       return;
     }
   } else if (wide) {

@@ -27,7 +27,7 @@ constexpr int kThreads = 256;
 struct HeadArgs {
   int n;
   tb_head_part part[kMaxProjections];
-  int first[kMaxProjections + 1];   // part j owns heads first[j] .. first[j+1] - 1 of a token
+  int first[kMaxProjections + 1];   // part j owns head groups first[j] .. first[j+1] - 1 of a token
   int64_t T;
   int D, half;      // head size, rotated pairs
   int G;            // lanes per head (a power of two)
@@ -37,59 +37,75 @@ struct HeadArgs {
   float eps, offset, inv_d;
 };
 
+// V consecutive elements as they are in memory.
+template <typename E, int V> struct Raw { uint4 v; };
+template <typename E> struct Raw<E, 1> { E v; };
+template <> struct Raw<bf16_t, 2> { uint32_t v; };
+template <> struct Raw<float, 2> { float2 v; };
+
 template <typename E, int V>
-__device__ __forceinline__ void load_chunk(const E* p, float (&f)[V]) {
-  if constexpr (V * sizeof(E) == 16) {
+__device__ __forceinline__ Raw<E, V> load_raw(const E* p) {
+  Raw<E, V> r;
+  r.v = *reinterpret_cast<const decltype(r.v)*>(p);
+  return r;
+}
+template <typename E, int V> __device__ __forceinline__ Raw<E, V> zero_raw() {
+  if constexpr (V == 1) return Raw<E, 1>{from_f32<E>(0.f)};
+  else if constexpr (V > 2) return Raw<E, V>{make_uint4(0, 0, 0, 0)};
+  else return Raw<E, V>{};
+}
+
+template <typename E, int V>
+__device__ __forceinline__ void widen(const Raw<E, V>& r, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = to_f32<E>(r.v);
+  } else if constexpr (V == 2) {
     if constexpr (sizeof(E) == 2) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+      f[0] = __uint_as_float(r.v << 16);
+      f[1] = __uint_as_float(r.v & 0xffff0000u);
     } else {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(p);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = v[e];
+      f[0] = r.v.x;
+      f[1] = r.v.y;
     }
   } else {
+    const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
 #pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = to_f32<E>(p[e]);
+    for (int e = 0; e < V; ++e) {
+      if constexpr (sizeof(E) == 2) f[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+      else f[e] = __uint_as_float(w[e]);
+    }
   }
 }
 
 template <typename E, int V>
 __device__ __forceinline__ void store_chunk(E* p, const float (&f)[V]) {
-  if constexpr (V * sizeof(E) == 16) {
-    if constexpr (sizeof(E) == 2) {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = f32_to_bf16(f[2 * e]) | (uint32_t(f32_to_bf16(f[2 * e + 1])) << 16);
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      *reinterpret_cast<f32x4*>(p) = f32x4{f[0], f[1], f[2], f[3]};
-    }
+  if constexpr (V == 1) {
+    *p = from_f32<E>(f[0]);
+  } else if constexpr (V == 2) {
+    if constexpr (sizeof(E) == 2) *reinterpret_cast<uint32_t*>(p) = pack_bf16(f[0], f[1]);
+    else *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+  } else if constexpr (sizeof(E) == 2) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                                              pack_bf16(f[6], f[7]));
   } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) p[e] = from_f32<E>(f[e]);
+    *reinterpret_cast<f32x4*>(p) = f32x4{f[0], f[1], f[2], f[3]};
   }
 }
 
-// V: elements of a chunk (16 bytes, or 1 for any size and alignment); UPL:
+// V: elements of a chunk (16 bytes, 2, or 1 for any size and alignment); UPL:
 // units (pairs of chunks) per lane; INTER: interleaved pairs.
 template <typename E, int V, int UPL, bool INTER>
 __global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs a) {
   const int l = int(threadIdx.x) & 63;
-  const int64_t t = int64_t(blockIdx.x) * (kThreads / kWave) + (threadIdx.x >> 6);
+  const int64_t t = int64_t(blockIdx.x) * (kThreads / kWave) + __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
   if (t >= a.T) return;
   const int lane = l & (a.G - 1), slot = l / a.G, slots = kWave / a.G;
-  const int heads = a.first[a.n];
-  const int h0 = int(blockIdx.y) * a.iters * slots;
+  const int g0 = int(blockIdx.y) * a.iters, g1 = min(g0 + a.iters, a.first[a.n]);
 
   // Unit u's chunks: interleaved, 2V consecutive elements from 2V u.  Else the
   // rotated units take V elements from V u and their partners R/2 further on,
   // and the units after them 2V consecutive elements of the rest.
   int ea[UPL], eb[UPL];
-  float cs[UPL][V], sn[UPL][V];
-  const double where = a.half > 0 ? double(a.pos[t]) : 0.;
 #pragma unroll
   for (int k = 0; k < UPL; ++k) {
     const int u = lane + k * a.G;
@@ -103,9 +119,34 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs a) {
       ea[k] = 2 * a.half + 2 * (u * V - a.half);
       eb[k] = ea[k] + V;
     }
+  }
+
+  // The part that owns group g (uniform), and this lane's head of the group.
+  int j = 0;
+  while (g0 >= a.first[j + 1]) ++j;
+  Raw<E, V> ra[UPL], rb[UPL];
+  auto fetch = [&](int g, int pj) {
+    const tb_head_part& pt = a.part[pj];
+    const int h = (g - a.first[pj]) * slots + slot;
+    const E* x = static_cast<const E*>(pt.x) + t * pt.x_token_stride + h * pt.x_head_stride;
+#pragma unroll
+    for (int k = 0; k < UPL; ++k) {
+      ra[k] = rb[k] = zero_raw<E, V>();
+      if (h < int(pt.heads)) {
+        if (ea[k] < a.D) ra[k] = load_raw<E, V>(x + ea[k]);
+        if (eb[k] < a.D) rb[k] = load_raw<E, V>(x + eb[k]);
+      }
+    }
+  };
+  fetch(g0, j);   // under way while the angles are computed
+
+  float cs[UPL][V], sn[UPL][V];
+  const double where = a.half > 0 ? double(a.pos[t]) : 0.;
+#pragma unroll
+  for (int k = 0; k < UPL; ++k)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const int p = u * V + e;   // the pair's frequency
+      const int p = (lane + k * a.G) * V + e;   // the pair's frequency
       cs[k][e] = 1.f;
       sn[k][e] = 0.f;
       if (p < a.half) {
@@ -113,50 +154,54 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs a) {
         sincospif(2.f * float(turns - rint(turns)), &sn[k][e], &cs[k][e]);
       }
     }
-  }
 
-  for (int it = 0; it < a.iters; ++it) {
-    const int h = h0 + it * slots + slot;
-    const bool live = h < heads;
-    int j = 0;
-    while (live && j + 1 < a.n && h >= a.first[j + 1]) ++j;
+  float wa[UPL][V], wb[UPL][V];
+  int have = -1;   // the part whose weights are in wa, wb
+  for (int g = g0; g < g1; ++g) {
     const tb_head_part& pt = a.part[j];
-    const int hh = live ? h - a.first[j] : 0;
-    const E* x = static_cast<const E*>(pt.x) + t * pt.x_token_stride + hh * pt.x_head_stride;
+    const int h = (g - a.first[j]) * slots + slot;
+    if (j != have) {
+      have = j;
+      const E* wt = static_cast<const E*>(pt.weight);
+#pragma unroll
+      for (int k = 0; k < UPL; ++k) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) wa[k][e] = wb[k][e] = 1.f;
+        if (wt) {
+          if (ea[k] < a.D) widen<E, V>(load_raw<E, V>(wt + ea[k]), wa[k]);
+          if (eb[k] < a.D) widen<E, V>(load_raw<E, V>(wt + eb[k]), wb[k]);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            wa[k][e] += a.offset;
+            wb[k][e] += a.offset;
+          }
+        }
+      }
+    }
     float fa[UPL][V], fb[UPL][V];
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < UPL; ++k) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) fa[k][e] = fb[k][e] = 0.f;
-      if (live && ea[k] < a.D) load_chunk<E, V>(x + ea[k], fa[k]);
-      if (live && eb[k] < a.D) load_chunk<E, V>(x + eb[k], fb[k]);
+      widen<E, V>(ra[k], fa[k]);
+      widen<E, V>(rb[k], fb[k]);
 #pragma unroll
       for (int e = 0; e < V; ++e) sum += fa[k][e] * fa[k][e] + fb[k][e] * fb[k][e];
     }
+    const int jn = j;
+    if (g + 1 < g1) {   // the next group loads while this one is finished
+      while (g + 1 >= a.first[j + 1]) ++j;
+      fetch(g + 1, j);
+    }
     for (int d = 1; d < a.G; d *= 2) sum += __shfl_xor(sum, d);
     const float r = 1.f / sqrtf(sum * a.inv_d + a.eps);
-    if (!live) continue;
-    const E* wt = static_cast<const E*>(pt.weight);
-    E* y = static_cast<E*>(pt.y) + t * pt.y_token_stride + hh * pt.y_head_stride;
+    E* y = static_cast<E*>(a.part[jn].y) + t * a.part[jn].y_token_stride + h * a.part[jn].y_head_stride;
+    const bool live = h < int(a.part[jn].heads);
 #pragma unroll
     for (int k = 0; k < UPL; ++k) {
-      float wa[V], wb[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) wa[e] = wb[e] = 1.f;
-      if (wt) {
-        if (ea[k] < a.D) load_chunk<E, V>(wt + ea[k], wa);
-        if (eb[k] < a.D) load_chunk<E, V>(wt + eb[k], wb);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          wa[e] += a.offset;
-          wb[e] += a.offset;
-        }
-      }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        fa[k][e] *= r * wa[e];
-        fb[k][e] *= r * wb[e];
+        fa[k][e] *= r * wa[k][e];
+        fb[k][e] *= r * wb[k][e];
       }
       if constexpr (INTER && V > 1) {
         // The unit's 2V elements are V pairs: the first V/2 in chunk a, the rest in chunk b.
@@ -177,8 +222,8 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs a) {
           fb[k][e] = x1 * cs[k][e] + x0 * sn[k][e];
         }
       }
-      if (ea[k] < a.D) store_chunk<E, V>(y + ea[k], fa[k]);
-      if (eb[k] < a.D) store_chunk<E, V>(y + eb[k], fb[k]);
+      if (live && ea[k] < a.D) store_chunk<E, V>(y + ea[k], fa[k]);
+      if (live && eb[k] < a.D) store_chunk<E, V>(y + eb[k], fb[k]);
     }
   }
 }
@@ -189,36 +234,49 @@ hipError_t heads_typed(HeadArgs& a, bool interleaved, hipStream_t stream) {
   a.G = 1;
   while (a.G < kWave && a.G < units) a.G *= 2;
   const int upl = (units + a.G - 1) / a.G, slots = kWave / a.G;
-  const int groups = (a.first[a.n] + slots - 1) / slots;
-  // A wave walks all of a token's heads (its angles are then computed once)
-  // unless there are too few tokens to fill the chip.
-  a.iters = a.T >= 4096 ? groups : std::max(1, int(groups * a.T / 4096));
+  for (int j = 0; j < a.n; ++j) a.first[j + 1] = a.first[j] + int((a.part[j].heads + slots - 1) / slots);
+  const int groups = a.first[a.n];
+  // A wave walks all of a token's heads, computing its angles once (4096 tokens
+  // of 32 + 8 heads of 256: 34 us, against 40 in two waves and 56 in ten),
+  // unless that leaves too few waves for the chip.
+  a.iters = std::max(1, int(std::min<int64_t>(groups, groups * a.T / 4096)));
   const dim3 grid(unsigned((a.T + kThreads / kWave - 1) / (kThreads / kWave)), unsigned((groups + a.iters - 1) / a.iters));
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);
     return hipGetLastError();
   };
   if (upl == 1) return interleaved ? go(heads_kernel<E, V, 1, true>) : go(heads_kernel<E, V, 1, false>);
-  if (upl == 2) return interleaved ? go(heads_kernel<E, V, 2, true>) : go(heads_kernel<E, V, 2, false>);
-  if constexpr (V == 1) {
+  if constexpr (V <= 4)
+    if (upl == 2) return interleaved ? go(heads_kernel<E, V, 2, true>) : go(heads_kernel<E, V, 2, false>);
+  if constexpr (V <= 2)
     if (upl <= 4) return interleaved ? go(heads_kernel<E, V, 4, true>) : go(heads_kernel<E, V, 4, false>);
+  if constexpr (V == 1)
     if (upl <= 8) return interleaved ? go(heads_kernel<E, V, 8, true>) : go(heads_kernel<E, V, 8, false>);
-  }
   return hipErrorInvalidValue;
+}
+
+// Whether every part can be taken in chunks of V elements: sizes, strides and
+// addresses are multiples of one.
+template <typename E>
+bool chunks_fit(const HeadArgs& a, bool interleaved, int V) {
+  if (a.D % V != 0 || (!interleaved && a.half % V != 0)) return false;
+  for (int j = 0; j < a.n; ++j) {
+    const tb_head_part& p = a.part[j];
+    if (p.heads > 0 &&
+        ((p.x_token_stride | p.x_head_stride | p.y_token_stride | p.y_head_stride) % V != 0 ||
+         ((reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.y) | reinterpret_cast<uintptr_t>(p.weight)) &
+          (V * sizeof(E) - 1)) != 0))
+      return false;
+  }
+  return true;
 }
 
 template <typename E>
 hipError_t heads_vec(HeadArgs& a, bool interleaved, hipStream_t stream) {
   constexpr int V = 16 / sizeof(E);
-  // 16-byte chunks need sizes, strides and addresses that are multiples of 16 bytes.
-  bool vec = a.D % V == 0 && (interleaved || a.half % V == 0);
-  for (int j = 0; j < a.n && vec; ++j) {
-    const tb_head_part& p = a.part[j];
-    vec = (p.x_token_stride | p.x_head_stride | p.y_token_stride | p.y_head_stride) % V == 0 &&
-          ((reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.y) | reinterpret_cast<uintptr_t>(p.weight)) &
-           15u) == 0;
-  }
-  return vec ? heads_typed<E, V>(a, interleaved, stream) : heads_typed<E, 1>(a, interleaved, stream);
+  if (chunks_fit<E>(a, interleaved, V)) return heads_typed<E, V>(a, interleaved, stream);
+  return chunks_fit<E>(a, interleaved, 2) ? heads_typed<E, 2>(a, interleaved, stream)
+                                          : heads_typed<E, 1>(a, interleaved, stream);
 }
 
 }  // namespace
@@ -230,7 +288,6 @@ hipError_t launch_heads(tb_dtype dtype, int n, const tb_head_part* parts, int64_
   a.n = n;
   for (int j = 0; j < n; ++j) {
     a.part[j] = parts[j];
-    a.first[j + 1] = a.first[j] + int(parts[j].heads);
   }
   a.T = tokens;
   a.D = head_dim;
