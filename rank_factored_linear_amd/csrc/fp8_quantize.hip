@@ -162,6 +162,195 @@ __global__ __launch_bounds__(kThreads, 2) void rebuild_blocks_kernel(const EI* _
   }
 }
 
+// ---- bf16 bundles with rank % 8 == 0, up to 256 ------------------------------
+//
+// The same block per workgroup, with U and V coming in k-tiles of 32 straight
+// into a ring of LDS slots (kRingSlots of 16 KB), kRingSlots - 1 k-tiles ahead,
+// and the product passing through LDS in two halves, so that three workgroups
+// fit a compute unit and hide each other's waits.
+namespace ring {
+
+constexpr int BK = 32, kRingSlots = 3;
+constexpr int kOpBytes = kBlock * BK * 2;      // one operand's k-tile: 128 rows of 64 bytes
+constexpr int kSlotBytes = 2 * kOpBytes;
+constexpr int kLds = kRingSlots * kSlotBytes;
+constexpr unsigned kRsrcFlags = 0x00020000u;   // buffer descriptor word 3: 32-bit data format
+constexpr int kPast = int(0x80000000u);        // lane offset past every buffer: zeros
+static_assert(kLds >= 64 * kPitch * 4, "half a tile of fp32 fits the ring's room");
+
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+typedef rebuild::t128::f32x16 f32x16;
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// Two direct-to-LDS loads: load j fills 1 KB at dst + j KB, lane l at + 16 l.
+__device__ __forceinline__ void dma2(unsigned dst, __amdgpu_buffer_rsrc_t r, int v0, int v1, int soff) {
+  asm volatile(
+      "s_mov_b32 m0, %[d0]\n\ts_nop 0\n\t"
+      "buffer_load_dwordx4 %[v0], %[r], %[so] offen lds\n\t"
+      "s_mov_b32 m0, %[d1]\n\ts_nop 0\n\t"
+      "buffer_load_dwordx4 %[v1], %[r], %[so] offen lds"
+      :
+      : [d0] "s"(dst), [d1] "s"(dst + 1024u), [v0] "v"(v0), [v1] "v"(v1), [r] "s"(r), [so] "s"(soff)
+      : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// KT: k-tiles of the rank (those past it load zeros).
+template <int SC, int KT>
+__global__ __launch_bounds__(kThreads, 3) void rebuild_ring_kernel(const bf16_t* __restrict__ s,
+                                                                   const bf16_t* __restrict__ w0,
+                                                                   const bf16_t* __restrict__ u,
+                                                                   const bf16_t* __restrict__ v,
+                                                                   uint8_t* __restrict__ q,
+                                                                   scale_t<SC>* __restrict__ scale, int O, int I,
+                                                                   int R, int KB) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+  __shared__ uint32_t wave_max[kThreads / kWave];
+  lds_byte* const base = (lds_byte*)lds;
+  const int tid = int(threadIdx.x), w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+  const int ob = int(blockIdx.x) / KB, kb = int(blockIdx.x) % KB;
+  const int o0 = ob * kBlock, i0 = kb * kBlock;
+  const int c = (tid & 15) * 8, r0 = tid >> 4;   // epilogue: columns c..c+7 of rows r0 + 16 p
+
+  // A wave fills rows 32 w + 16 j + l / 4 of a k-tile; chunk c of row r sits at
+  // c ^ ((r >> 2) & 3), so that fragment reads of 16 rows meet all banks.
+  const unsigned dst = unsigned(uintptr_t(base)) + unsigned(w) * 2048u;
+  const int drow = w * 32 + (l >> 2), dc = (l & 3) ^ ((l >> 4) & 3);
+  const int orows = min(O - o0, kBlock), irows = min(I - i0, kBlock);
+  const __amdgpu_buffer_rsrc_t ru =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<bf16_t*>(u + size_t(o0) * R), 0, orows * R * 2, kRsrcFlags);
+  const __amdgpu_buffer_rsrc_t rv =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<bf16_t*>(v + size_t(i0) * R), 0, irows * R * 2, kRsrcFlags);
+  auto issue = [&](int slot, int kt) {
+    const bool ok = dc * 8 < R - kt * BK;
+    const int a0 = drow * R * 2 + dc * 16, a1 = a0 + 32 * R;
+    dma2(dst + slot * kSlotBytes, ru, ok ? a0 : kPast, ok ? a1 : kPast, kt * BK * 2);
+    dma2(dst + slot * kSlotBytes + kOpBytes, rv, ok ? a0 : kPast, ok ? a1 : kPast, kt * BK * 2);
+  };
+
+  // W0 first: it arrives under the product.
+  Frag8<bf16_t> f[8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int o = o0 + r0 + 16 * p;
+    f[p] = load_frag_if<bf16_t>(w0 + size_t(o) * I + i0 + c, o < O && i0 + c < I);   // I % 8 == 0
+  }
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int e = 0; e < kRingSlots - 1; ++e)
+    if (e < KT) issue(e, e);
+
+  const int wi = w & 1, wo = w >> 1, h = l >> 5, lr = l & 31;
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
+
+#pragma unroll
+  for (int st = 0; st < KT; ++st) {
+    // Loads land in order: k-tile st has when at most those after it are out.
+    if constexpr (kRingSlots == 3) {
+      if (st + 1 < KT) wait_vm<4>();
+      else wait_vm<0>();
+    } else {
+      wait_vm<0>();
+    }
+    __builtin_amdgcn_s_barrier();   // published; and every wave has left the slot filled next
+    if (st + kRingSlots - 1 < KT) issue((st + kRingSlots - 1) % kRingSlots, st + kRingSlots - 1);
+    __builtin_amdgcn_sched_barrier(0);
+    const int off = (st % kRingSlots) * kSlotBytes;
+    u32x4 fv[2][2], fu[2][2];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb) {
+        const int pos = ((ks * 2 + h) ^ ((lr >> 2) & 3)) << 4;
+        fv[rb][ks] = *reinterpret_cast<const lds_u32x4*>(base + off + kOpBytes + (wi * 64 + rb * 32 + lr) * 64 + pos);
+        fu[rb][ks] = *reinterpret_cast<const lds_u32x4*>(base + off + (wo * 64 + rb * 32 + lr) * 64 + pos);
+      }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+        for (int cb = 0; cb < 2; ++cb)
+          acc[rb][cb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fv[rb][ks]),
+                                                                __builtin_bit_cast(bf16x8, fu[cb][ks]), acc[rb][cb], 0,
+                                                                0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    mfma_operand_guard();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // The product through LDS, 64 rows at a time: waves 2 half, 2 half + 1 hold
+  // them (columns in fours per lane), every thread then takes eight columns of
+  // its rows.
+  float val[8][8];
+  uint32_t a = 0;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    __syncthreads();
+    if (wo == half) {
+#pragma unroll
+      for (int cb = 0; cb < 2; ++cb)
+#pragma unroll
+        for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const f32x16& m = acc[rb][cb];
+            *reinterpret_cast<lds_f32x4*>(base + ((cb * 32 + lr) * kPitch + wi * 64 + rb * 32 + 8 * b + 4 * h) * 4) =
+                f32x4{m[4 * b], m[4 * b + 1], m[4 * b + 2], m[4 * b + 3]};
+          }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int pp = 0; pp < 4; ++pp) {
+      const int p = half * 4 + pp, o = o0 + r0 + 16 * p;
+      const f32x4 lo = *reinterpret_cast<const lds_f32x4*>(base + ((r0 + 16 * pp) * kPitch + c) * 4);
+      const f32x4 hi = *reinterpret_cast<const lds_f32x4*>(base + ((r0 + 16 * pp) * kPitch + c + 4) * 4);
+      unpack8(f[p], val[p]);
+      const float so = s != nullptr && o < O ? to_f32<bf16_t>(s[o]) : 1.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        val[p][e] = so * val[p][e] + (e < 4 ? lo[e & 3] : hi[e & 3]);
+        a = max(a, abs_bits(val[p][e]));
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) a = max(a, uint32_t(__shfl_xor(int(a), d)));
+  if (l == 0) wave_max[w] = a;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kThreads / kWave; ++j) a = max(a, wave_max[j]);
+  scale_t<SC> st;
+  float by;
+  block_scale<SC>(a, st, by);
+  if (tid == 0) scale[size_t(ob) * KB + kb] = st;
+  if (i0 + c >= I) return;
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int o = o0 + r0 + 16 * p;
+    if (o >= O) continue;
+    const float(&t)[8] = val[p];
+    *reinterpret_cast<u32x2*>(q + size_t(o) * I + i0 + c) =
+        u32x2{pack4(t[0] * by, t[1] * by, t[2] * by, t[3] * by), pack4(t[4] * by, t[5] * by, t[6] * by, t[7] * by)};
+  }
+}
+
+}  // namespace ring
+
 template <typename E, int SC>
 hipError_t rows_typed(const void* x, void* q, void* scale, int64_t m, int64_t in_dim, hipStream_t stream) {
   const int KB = int(fp8_blocks(in_dim));
@@ -183,8 +372,12 @@ hipError_t blocks_typed(const void* s, const void* w0, const void* u, const void
     return hipGetLastError();
   };
   if (rank == 0) return go(rebuild_blocks_kernel<EI, SC, kNone>);
-  if constexpr (sizeof(EI) == 2)
+  if constexpr (sizeof(EI) == 2) {
+    if (rank % 8 == 0 && rank <= 64) return go(ring::rebuild_ring_kernel<SC, 2>);
+    if (rank % 8 == 0 && rank <= 128) return go(ring::rebuild_ring_kernel<SC, 4>);
+    if (rank % 8 == 0 && rank <= 256) return go(ring::rebuild_ring_kernel<SC, 8>);
     if (rank % 8 == 0) return go(rebuild_blocks_kernel<EI, SC, kMfma>);
+  }
   return go(rebuild_blocks_kernel<EI, SC, kAny>);
 }
 
