@@ -336,16 +336,27 @@ __global__ __launch_bounds__(kDecodeWaves* kWave) void fp8_decode_kernel(DecodeA
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: 128 outputs x 128 tokens per workgroup, four waves of 64 x 64,
-// one block of 128 columns per step.  Both operands' blocks are staged in LDS
-// (two buffers; rows of 128 bytes with their 16-byte pieces XOR-swizzled by
-// row, so that the fragment reads of 16 rows meet all banks) through
-// registers, so the next block's loads fly while this one multiplies.
-// With few tiles the reduction is cut into S slices over blockIdx.y; each
-// slice writes its fp32 sums and a second launch adds them in slice order, so
-// the result does not depend on timing.
+// More tokens (the 256 x 256 tiles of fp8_gemm.hip aside): 64 tokens x 128
+// outputs per workgroup, four waves of 64 outputs x 32 tokens, one block of
+// 128 columns per step.  Both operands' blocks and the tokens' scales come
+// straight into a ring of three LDS slots, two blocks ahead, so that a step
+// waits for a block asked for two steps before (staged through registers, one
+// block ahead took 27 us at 777 x 1152 x 6912 in fp32, and two blocks ahead
+// did not fit the registers).  Rows of 128 bytes keep their 16-byte pieces
+// XOR-swizzled by (row >> 1) & 7, so that the fragment reads of 16 rows meet
+// all banks.
+// With few tiles the reduction is cut into S slices; each slice writes its
+// fp32 sums and a second launch adds them in slice order, so the result does
+// not depend on timing.
+//
+// Bound by the rate at which blocks reach LDS from the memory-side cache (24 KB
+// per block and tile) and, for fp32 results, by the bf16 matrix rate: 777 x
+// 1152 x 6912 takes 21.3 us in fp32 (four slices, and 4.4 us to join them) and
+// 16.7 us in bf16; 2000 x 8192 x 5376 in fp32 216 us (0.81 PFLOP/s). 128 tokens
+// per workgroup (eight waves) were no faster: 22.3, 16.4 and 232 us.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 128, kGemmThreads = 256;
+constexpr int kTile = 128, TM = 64, kSlots = 3;   // outputs and tokens of a tile; LDS slots
+constexpr int kGemmThreads = 4 * TM;
 
 struct GemmArgs {
   const uint8_t* x;
@@ -353,128 +364,180 @@ struct GemmArgs {
   const uint8_t* w;
   const void* ws;
   void* y;
-  float* part;   // [S][tiles][64][256] pieces of four, or NULL with one slice
+  float* part;   // [S][tiles][8][4 TM] pieces of four, or NULL with one slice
   int M, O, I, KB;
   int tiles_m, tiles_n, S;
   int wide;
 };
 
-__device__ __forceinline__ int swz(int row, int piece) { return row * 128 + ((piece ^ ((row >> 1) & 7)) << 4); }
+// Tile u's first token and output: groups of eight token tiles walked column
+// by column, so that workgroups that run together share rows in L2.
+__device__ __forceinline__ void tile_at(const GemmArgs& a, int u, int& m0, int& n0) {
+  const int per_group = 8 * a.tiles_n, first = u / per_group * 8, gs = min(a.tiles_m - first, 8), r = u % per_group;
+  m0 = (first + r % gs) * TM;
+  n0 = r / gs * kTile;
+}
+
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) uint32_t lds_u32;
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// One direct-to-LDS load: 16 bytes per lane, 1 KB at dst.  M0 takes one wait
+// state before a load reads it.
+__device__ __forceinline__ void dma16(unsigned dst, __amdgpu_buffer_rsrc_t r, int v, int soff) {
+  asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
+               [v] "v"(v), [r] "s"(r), [s] "s"(soff)
+               : "memory", "m0");
+}
+// A scale per lane, four bytes apart in LDS (a byte is widened).
+template <int SC>
+__device__ __forceinline__ void dma_scale(unsigned dst, __amdgpu_buffer_rsrc_t r, int v, int soff) {
+  if constexpr (SC == TB_SCALE_E8M0)
+    asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_ubyte %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
+                 [v] "v"(v), [r] "s"(r), [s] "s"(soff)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_dword %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
+                 [v] "v"(v), [r] "s"(r), [s] "s"(soff)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// At most N of this wave's loads are still out, and its LDS reads are done.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
 
 template <int SC, typename YE>
 __global__ __launch_bounds__(kGemmThreads, 2) void fp8_gemm_kernel(GemmArgs a) {
   constexpr bool kExact = sizeof(YE) == 4;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][kTile * 128];  // [buffer][W or x]
-  const int tid = int(threadIdx.x), w = tid / kWave, l = tid % kWave;
+  constexpr int kWaves = TM / 16, kW = 16 / kWaves;   // kW, 2: loads of W and x per wave and block
+  constexpr int kX = kTile * 128, kScales = kX + TM * 128, kSlot = kScales + kWaves * 256;
+  constexpr int kLoads = kW + 2 + 1;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kSlots * kSlot];
+  lds_byte* const base = (lds_byte*)ring;
+  const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave), l = int(threadIdx.x) % kWave;
   const int lr = l & 15, q = l >> 4, wo = w & 1, wt = w >> 1;
-  // Tiles in groups of eight token tiles, so that workgroups that run together
-  // share rows of both operands in L2.
-  const int per_group = 8 * a.tiles_n, first = int(blockIdx.x) / per_group * 8, gs = min(a.tiles_m - first, 8);
-  const int tm = first + (int(blockIdx.x) % per_group) % gs, tn = (int(blockIdx.x) % per_group) / gs;
-  const int m0 = tm * kTile, n0 = tn * kTile;
-  const int slice = int(blockIdx.y);
+  // Workgroup g runs on XCD g % 8: each XCD takes a run of the tiles of few
+  // slices, so that what it reads again fits its own L2.
+  const int tiles = a.tiles_m * a.tiles_n, total = tiles * a.S, xcd = int(blockIdx.x) % 8;
+  const int at = xcd * (total / 8) + min(xcd, total % 8) + int(blockIdx.x) / 8;
+  const int slice = at / tiles, tile = at % tiles;
+  int m0, n0;
+  tile_at(a, tile, m0, n0);
   const int kb0 = int(int64_t(slice) * a.KB / a.S), kb1 = int(int64_t(slice + 1) * a.KB / a.S);
 
-  const int sr = tid >> 3, sp = tid & 7;   // staging: piece sp of rows sr + 32 j
-  const scale_t<SC>* ws = static_cast<const scale_t<SC>*>(a.ws) + size_t(tn) * a.KB;
-  const scale_t<SC>* xs[4];
+  const int rows_w = min(a.O - n0, kTile), rows_x = min(a.M - m0, TM);
+  const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + size_t(n0) * a.I, int64_t(rows_w) * a.I);
+  const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x + size_t(m0) * a.I, int64_t(rows_x) * a.I);
+  const __amdgpu_buffer_rsrc_t rs =
+      rows_rsrc(static_cast<const scale_t<SC>*>(a.xs) + size_t(m0) * a.KB, int64_t(rows_x) * a.KB * int(sizeof(scale_t<SC>)));
+  const scale_t<SC>* ws = static_cast<const scale_t<SC>*>(a.ws) + size_t(n0 / kBlock) * a.KB;
+  // Load j of an operand: row 8 (w loads + j) + l / 8, the piece that the
+  // swizzle keeps at position l % 8; eight rows further on the swizzle differs
+  // in its upper bit only.
+  const int dr = l >> 3, pe = (l & 7) ^ (dr >> 1), po = pe ^ 4;
+  const unsigned b0 = unsigned(uintptr_t(base));
+  const int soff_scale = (wt * 32 + (l & 31)) * a.KB * int(sizeof(scale_t<SC>));
+  auto issue = [&](int slot, int kb) {
+    const int left = kb < kb1 ? a.I - kb * kBlock : 0, k = min(kb, kb1 - 1) * kBlock;
+    const int ve = pe * 16 < left ? dr * a.I + pe * 16 : kPast, vo = po * 16 < left ? dr * a.I + po * 16 : kPast;
+    const unsigned d = b0 + unsigned(slot * kSlot);
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    xs[j] = static_cast<const scale_t<SC>*>(a.xs) + size_t(min(m0 + wt * 64 + j * 16 + lr, a.M - 1)) * a.KB;
+    for (int j = 0; j < kW; ++j) {
+      const int row8 = w * kW + j;
+      dma16(d + row8 * 1024, rw, (row8 & 1) ? vo : ve, k + row8 * 8 * a.I);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) dma16(d + kX + (w * 2 + j) * 1024, rx, j ? vo : ve, k + (w * 2 + j) * 8 * a.I);
+    dma_scale<SC>(d + kScales + w * 256, rs, soff_scale, min(kb, kb1 - 1) * int(sizeof(scale_t<SC>)));
+  };
 
-  f32x4 acc[4][4];
+  f32x4 acc[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  u32x4 rw[4], rx[4];
-  scale_t<SC> nws{}, nxs[4]{};
-  auto fetch = [&](int kb) {
-    const int k = kb * kBlock + sp * 16;
+  const int sw = (lr >> 1) & 7, p0 = (q ^ sw) << 4, p1 = ((q + 4) ^ sw) << 4;
+  auto step = [&](auto which, int kb) {
+    constexpr int slot = decltype(which)::value;
+    wait_loads<kLoads>();             // block kb has landed; kb + 1 may be out
+    __builtin_amdgcn_s_barrier();     // published; and every wave has left the slot filled next
+    issue((slot + 2) % kSlots, kb + 2);
+    const lds_byte* const s = base + slot * kSlot;
+    const float wsc = scale_value(ws[kb]);
+    Operand<kExact> fx[2];
+    float sc[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int o = n0 + sr + 32 * j, t = m0 + sr + 32 * j;
-      rw[j] = o < a.O && k < a.I ? *reinterpret_cast<const u32x4*>(a.w + size_t(o) * a.I + k) : u32x4{0, 0, 0, 0};
-      rx[j] = t < a.M && k < a.I ? *reinterpret_cast<const u32x4*>(a.x + size_t(t) * a.I + k) : u32x4{0, 0, 0, 0};
-      nxs[j] = xs[j][kb];
-    }
-    nws = ws[kb];
-  };
-  auto stage = [&](int buf) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      *reinterpret_cast<u32x4*>(&lds[buf][0][swz(sr + 32 * j, sp)]) = rw[j];
-      *reinterpret_cast<u32x4*>(&lds[buf][1][swz(sr + 32 * j, sp)]) = rx[j];
-    }
-  };
-  if (kb0 < kb1) {
-    fetch(kb0);
-    stage(0);
-  }
-  for (int kb = kb0; kb < kb1; ++kb) {
-    const int buf = (kb - kb0) & 1;
-    float sc[4];
-    const float wsc = scale_value(nws);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sc[j] = scale_value(nxs[j]) * wsc;
-    __syncthreads();   // this block is staged, and every wave has left the other buffer
-    if (kb + 1 < kb1) fetch(kb + 1);
-    Operand<kExact> fx[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = wt * 64 + j * 16 + lr;
-      fx[j] = operand<kExact>(join(*reinterpret_cast<const u32x4*>(&lds[buf][1][swz(row, q)]),
-                                   *reinterpret_cast<const u32x4*>(&lds[buf][1][swz(row, q + 4)])));
+    for (int j = 0; j < 2; ++j) {
+      const lds_byte* r = s + kX + (wt * 32 + j * 16 + lr) * 128;
+      fx[j] = operand<kExact>(join(*reinterpret_cast<const lds_u32x4*>(r + p0), *reinterpret_cast<const lds_u32x4*>(r + p1)));
+      const uint32_t raw = *reinterpret_cast<const lds_u32*>(s + kScales + w * 256 + (j * 16 + lr) * 4);
+      if constexpr (SC == TB_SCALE_E8M0) sc[j] = scale_value(uint8_t(raw)) * wsc;
+      else sc[j] = __uint_as_float(raw) * wsc;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = wo * 64 + i * 16 + lr;
-      const Operand<kExact> fw = operand<kExact>(join(*reinterpret_cast<const u32x4*>(&lds[buf][0][swz(row, q)]),
-                                                      *reinterpret_cast<const u32x4*>(&lds[buf][0][swz(row, q + 4)])));
+      const lds_byte* r = s + (wo * 64 + i * 16 + lr) * 128;
+      const Operand<kExact> fw =
+          operand<kExact>(join(*reinterpret_cast<const lds_u32x4*>(r + p0), *reinterpret_cast<const lds_u32x4*>(r + p1)));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] += mma(fw, fx[j]) * sc[j];
+      for (int j = 0; j < 2; ++j) acc[i][j] += mma(fw, fx[j]) * sc[j];
     }
-    if (kb + 1 < kb1) stage(buf ^ 1);
+  };
+  issue(0, kb0);
+  issue(1, kb0 + 1);
+  int kb = kb0;
+  for (; kb + 2 < kb1; kb += 3) {
+    step(std::integral_constant<int, 0>{}, kb);
+    step(std::integral_constant<int, 1>{}, kb + 1);
+    step(std::integral_constant<int, 2>{}, kb + 2);
   }
+  if (kb < kb1) step(std::integral_constant<int, 0>{}, kb);
+  if (kb + 1 < kb1) step(std::integral_constant<int, 1>{}, kb + 1);
+  wait_loads<0>();   // nothing lands in LDS after the workgroup has ended
 
   if (a.S > 1) {
     f32x4* p = reinterpret_cast<f32x4*>(a.part) +
-               (size_t(slice) * a.tiles_m * a.tiles_n + blockIdx.x) * 16 * kGemmThreads + tid;
+               (size_t(slice) * tiles + tile) * 8 * kGemmThreads + threadIdx.x;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[(i * 4 + j) * kGemmThreads] = acc[i][j];
+      for (int j = 0; j < 2; ++j) p[(i * 2 + j) * kGemmThreads] = acc[i][j];
     return;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = m0 + wt * 64 + j * 16 + lr, o = n0 + wo * 64 + i * 16 + q * 4;
+    for (int j = 0; j < 2; ++j) {
+      const int t = m0 + wt * 32 + j * 16 + lr, o = n0 + wo * 64 + i * 16 + q * 4;
       if (t < a.M && o < a.O)
         store_out4(static_cast<YE*>(a.y) + size_t(t) * a.O + o, acc[i][j], a.O - o, a.wide && o + 4 <= a.O);
     }
 }
 
 // The slices' sums of a split product, added in slice order: one workgroup for
-// four of a tile's sixteen pieces.
+// the pieces of 16 outputs of each of a tile's waves.
 template <typename YE>
 __global__ __launch_bounds__(kGemmThreads) void fp8_join_kernel(GemmArgs a) {
-  const int tid = int(threadIdx.x), w = tid / kWave, l = tid % kWave, lr = l & 15, q = l >> 4, wo = w & 1, wt = w >> 1;
+  const int w = int(threadIdx.x) / kWave, l = int(threadIdx.x) % kWave, lr = l & 15, q = l >> 4, wo = w & 1, wt = w >> 1;
   const int tile = int(blockIdx.x) >> 2, tiles = a.tiles_m * a.tiles_n, i = int(blockIdx.x) & 3;
-  const int per_group = 8 * a.tiles_n, first = tile / per_group * 8, gs = min(a.tiles_m - first, 8);
-  const int m0 = (first + (tile % per_group) % gs) * kTile, n0 = (tile % per_group) / gs * kTile;
-  const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + (size_t(tile) * 16 + i * 4) * kGemmThreads + tid;
-  f32x4 sum[4];
+  int m0, n0;
+  tile_at(a, tile, m0, n0);
+  const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + (size_t(tile) * 4 + i) * 2 * kGemmThreads + threadIdx.x;
+  f32x4 sum[2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) sum[j] = p[j * kGemmThreads];
+  for (int j = 0; j < 2; ++j) sum[j] = p[j * kGemmThreads];
   for (int s = 1; s < a.S; ++s)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sum[j] += p[(size_t(s) * tiles * 16 + j) * kGemmThreads];
+    for (int j = 0; j < 2; ++j) sum[j] += p[(size_t(s) * tiles * 8 + j) * kGemmThreads];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int t = m0 + wt * 64 + j * 16 + lr, o = n0 + wo * 64 + i * 16 + q * 4;
+  for (int j = 0; j < 2; ++j) {
+    const int t = m0 + wt * 32 + j * 16 + lr, o = n0 + wo * 64 + i * 16 + q * 4;
     if (t < a.M && o < a.O)
       store_out4(static_cast<YE*>(a.y) + size_t(t) * a.O + o, sum[j], a.O - o, a.wide && o + 4 <= a.O);
   }
@@ -544,8 +607,8 @@ hipError_t decode_x(tb_dtype x_dtype, const DecodeArgs& a, hipStream_t stream) {
 
 template <int SC, typename YE>
 hipError_t gemm_go(const GemmArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((fp8_gemm_kernel<SC, YE>), dim3(unsigned(a.tiles_m * a.tiles_n), unsigned(a.S)),
-                     dim3(kGemmThreads), 0, stream, a);
+  hipLaunchKernelGGL((fp8_gemm_kernel<SC, YE>), dim3(unsigned(a.tiles_m * a.tiles_n * a.S)), dim3(kGemmThreads), 0,
+                     stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.S == 1) return e;
   hipLaunchKernelGGL((fp8_join_kernel<YE>), dim3(unsigned(a.tiles_m * a.tiles_n * 4)), dim3(kGemmThreads), 0, stream,
@@ -579,14 +642,17 @@ Fp8Plan plan_fp8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, tb_
     p.off_part = at;
     at += p.tile.part_bytes;
   } else if (!p.decode) {
-    p.tiles_m = int((m + kTile - 1) / kTile);
     p.tiles_n = int((out_dim + kTile - 1) / kTile);
+    p.tiles_m = int((m + TM - 1) / TM);
+    // Slices for the two workgroups that a compute unit holds, of at least four
+    // blocks, where that saves more than the second launch costs (as much as
+    // about 12 blocks).
     const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
-    // Two workgroups fit a compute unit; a slice keeps at least four blocks.
-    if (tiles < cus) p.S = int(std::max<int64_t>(1, std::min<int64_t>(2 * cus / tiles, KB / 4)));
+    const int64_t s = std::min<int64_t>(2 * cus / tiles, KB / 4);
+    if (s > 1 && KB - KB / s >= 12) p.S = int(s);
     if (p.S > 1) {
       p.off_part = at;
-      at += size_t(p.S) * tiles * kTile * kTile * 4;
+      at += size_t(p.S) * tiles * kTile * TM * 4;
     }
   }
   p.bytes = at;

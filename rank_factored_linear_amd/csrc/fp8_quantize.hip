@@ -200,7 +200,7 @@ __device__ __forceinline__ void dma2(unsigned dst, __amdgpu_buffer_rsrc_t r, int
 
 template <int N>
 __device__ __forceinline__ void wait_vm() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");   // and this wave's LDS reads are done
 }
 
 // KT: k-tiles of the rank (those past it load zeros).

@@ -208,9 +208,9 @@ struct Fp8Plan {
   int decode;              // 1: the few-token kernel (m <= kDecodeMaxTokens)
   int fused;               // x is quantised inside it
   int rows;                // output rows of its workgroups
-  int big;                 // 1: the 256 x 256 tiles of `tile`; 0: 128 x 128 tiles
+  int big;                 // 1: the 256 x 256 tiles of `tile`; 0: tiles of 64 tokens x 128 outputs
   Fp8TilePlan tile;
-  int tiles_m, tiles_n, S; // 128 x 128 tiles and slices of in_dim
+  int tiles_m, tiles_n, S;   // those tiles and their slices of in_dim
   size_t off_xq, off_xs, off_part, bytes;   // Q(x), its scales and the slices' sums in the workspace
 };
 // quantised: x comes in e4m3 with its scales.
