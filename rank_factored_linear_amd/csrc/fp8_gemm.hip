@@ -32,17 +32,19 @@ constexpr int kWaves = 8, kThreads = kWaves * kWave;
 constexpr int kOpBytes = BT * kBlock;         // one operand's block in LDS
 constexpr int kBOffset = 2 * kOpBytes;        // ring [W0][W1][x0][x1]
 constexpr int kRingBytes = 4 * kOpBytes;
+constexpr int kScaleBytes = 2 * kWaves * 256; // each wave's 64 activation scales of two blocks
 constexpr unsigned kRsrcFlags = 0x00020000u;  // buffer descriptor word 3: 32-bit data format
 constexpr int kPast = int(0x80000000u);       // lane offset past every buffer: the load returns zeros
 // Finished tiles leave through LDS, 16 tokens x 64 outputs of bf16 at a time
 // per wave, rows 144 bytes apart, beside the ring.
 constexpr int kStagePitch = 144, kStageBytes = 16 * kStagePitch;
-static_assert(kRingBytes + kWaves * kStageBytes <= 160 * 1024, "ring and staging fit the LDS");
+static_assert(kRingBytes + kScaleBytes + kWaves * kStageBytes <= 160 * 1024, "ring, scales and staging fit the LDS");
 constexpr int kPieces = 32;                   // pieces of four results per lane and tile
 
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+typedef __attribute__((address_space(3))) uint32_t lds_u32;
 
 struct Args {
   const uint8_t* x;
@@ -89,60 +91,75 @@ __device__ __forceinline__ lds_byte* opaque(lds_byte* p) {
 }
 
 struct Lanes {
-  unsigned dma_w, dma_x;   // this wave's 4 KB of each operand in buffer 0
-  int row, ce, co;         // load j: row + 8 j, piece ce (even j) or co (odd j)
-  lds_byte* w_rd[2];       // the fragment's pieces q and q + 4 of W row wo * 128 + lane % 16
-  lds_byte* x_rd[2];       // and of x row wt * 64 + lane % 16
-  int xs_off;              // bytes from the tile's first activation scale to those of that row
+  unsigned dma_w, dma_x, dma_s;  // where this wave's loads land in buffer 0
+  int row_w, row_x, tok;         // first row of its loads in the tile; its first token
+  int ce, co;                    // lane offsets' pieces (bytes) in loads of even and of odd groups of eight rows
+  int dr;                        // row of the lane in a load
+  lds_byte* w_rd[2];             // the fragment's pieces q and q + 4 of W row wo * 128 + lane % 16
+  lds_byte* x_rd[2];             // and of x row wt * 64 + lane % 16
+  lds_byte* s_rd;                // the scale of that x row
 };
 
-__device__ __forceinline__ Lanes make_lanes(uint8_t* ring, int scale_row_bytes) {
+__device__ __forceinline__ Lanes make_lanes(uint8_t* ring, uint8_t* scales) {
   lds_byte* base = (lds_byte*)ring;
   const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave), l = int(threadIdx.x) % kWave;
   const int lr = l & 15, q = l >> 4, wo = w & 1, wt = w >> 1;
   Lanes ln;
+  // W rows: 16 of the fragments 0..3 of one half of the outputs, and 64 rows on
+  // the same of fragments 4..7.  x rows: 32.
+  ln.row_w = (w >> 2) * 128 + (w & 3) * 16;
+  ln.row_x = w * 32;
+  ln.tok = wt * 64;
   const unsigned b0 = unsigned(uintptr_t(base));
-  ln.dma_w = __builtin_amdgcn_readfirstlane(b0 + unsigned(w) * 4096u);
-  ln.dma_x = __builtin_amdgcn_readfirstlane(b0 + unsigned(kBOffset) + unsigned(w) * 4096u);
-  ln.xs_off = (wt * 64 + lr) * scale_row_bytes;
-  ln.row = w * 32 + (l >> 3);
-  ln.ce = (l & 7) ^ ((ln.row >> 1) & 7);
-  ln.co = (l & 7) ^ (((ln.row + 8) >> 1) & 7);
-  // Fragment rows are 16 apart: the swizzle of row r + 16 i is that of r.
+  ln.dma_w = __builtin_amdgcn_readfirstlane(b0 + unsigned(ln.row_w) * kBlock);
+  ln.dma_x = __builtin_amdgcn_readfirstlane(b0 + unsigned(kBOffset) + unsigned(ln.row_x) * kBlock);
+  ln.dma_s = __builtin_amdgcn_readfirstlane(unsigned(uintptr_t((lds_byte*)scales)) + unsigned(w) * 256u);
+  // Groups of eight rows start at multiples of eight: their swizzle is the
+  // row's half, with the upper bit flipped in every second group.
+  ln.dr = l >> 3;
+  ln.ce = ((l & 7) ^ (ln.dr >> 1)) << 4;
+  ln.co = ln.ce ^ 64;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int piece = ((q + 4 * h) ^ ((lr >> 1) & 7)) << 4;
     ln.w_rd[h] = opaque(base + (wo * 128 + lr) * kBlock + piece);
     ln.x_rd[h] = opaque(base + kBOffset + (wt * 64 + lr) * kBlock + piece);
   }
+  ln.s_rd = opaque((lds_byte*)scales + w * 256 + lr * 4);
   return ln;
 }
 
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-// Four direct-to-LDS loads of a wave: load j fills 1 KB at dst + j KB from the
-// rows at soff + j * step.  M0 takes one wait state before a load reads it.
-// Written as assembly so that the compiler does not drain them before each LDS
-// read; wait_dma is the wait.
-__device__ __forceinline__ void dma4(unsigned dst, __amdgpu_buffer_rsrc_t r, int ve, int vo, int soff, int step) {
-  asm volatile(
-      "s_mov_b32 m0, %[d0]\n\ts_nop 0\n\t"
-      "buffer_load_dwordx4 %[ve], %[r], %[s0] offen lds\n\t"
-      "s_mov_b32 m0, %[d1]\n\ts_nop 0\n\t"
-      "buffer_load_dwordx4 %[vo], %[r], %[s1] offen lds\n\t"
-      "s_mov_b32 m0, %[d2]\n\ts_nop 0\n\t"
-      "buffer_load_dwordx4 %[ve], %[r], %[s2] offen lds\n\t"
-      "s_mov_b32 m0, %[d3]\n\ts_nop 0\n\t"
-      "buffer_load_dwordx4 %[vo], %[r], %[s3] offen lds"
-      :
-      : [d0] "s"(dst), [d1] "s"(dst + 1024u), [d2] "s"(dst + 2048u), [d3] "s"(dst + 3072u), [ve] "v"(ve), [vo] "v"(vo),
-        [r] "s"(r), [s0] "s"(soff), [s1] "s"(soff + step), [s2] "s"(soff + 2 * step), [s3] "s"(soff + 3 * step)
-      : "memory", "m0");
+// One direct-to-LDS load of a wave: eight rows of 128 bytes, 1 KB at dst.  M0
+// takes one wait state before a load reads it.  Written as assembly so that the
+// compiler does not drain it before each LDS read; wait_loads is the wait.
+__device__ __forceinline__ void dma(unsigned dst, __amdgpu_buffer_rsrc_t r, int v, int soff) {
+  asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
+               [v] "v"(v), [r] "s"(r), [s] "s"(soff)
+               : "memory", "m0");
+}
+// One scale per lane, four bytes apart in LDS (a byte is widened).
+template <int SC>
+__device__ __forceinline__ void dma_scale(unsigned dst, __amdgpu_buffer_rsrc_t r, int v, int soff) {
+  if constexpr (SC == TB_SCALE_E8M0)
+    asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_ubyte %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
+                 [v] "v"(v), [r] "s"(r), [s] "s"(soff)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_dword %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
+                 [v] "v"(v), [r] "s"(r), [s] "s"(soff)
+                 : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
-// Every load of this wave has landed.
-__device__ __forceinline__ void wait_dma() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// At most N of this wave's loads are still out, and its LDS reads are done.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
@@ -176,22 +193,49 @@ __device__ __forceinline__ Source<SC> source_of(const Args& a, const Item& it) {
   return s;
 }
 
-// Block kb of both operands into LDS buffer BUF; pieces past the reduction, and
-// every piece of a block at or past kb1, are fetched from past the buffers and
-// so land as zeros without memory traffic.  There is no branch: one here would
-// let the compiler move products of a step into the block behind it.
-template <int BUF, int SC>
-__device__ __forceinline__ void issue(const Args& a, const Source<SC>& s, const Lanes& ln, int kb, int kb1) {
-  const int left = kb < kb1 ? a.I - kb * kBlock : 0;
-  const int ve = ln.ce * 16 < left ? ln.row * a.I + (ln.ce << 4) : kPast;
-  const int vo = ln.co * 16 < left ? ln.row * a.I + (ln.co << 4) : kPast;
-  const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(uniform_ptr(s.w)), 0, __builtin_amdgcn_readfirstlane(s.wbytes), kRsrcFlags);
-  const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(uniform_ptr(s.x)), 0, __builtin_amdgcn_readfirstlane(s.xbytes), kRsrcFlags);
-  const int soff = __builtin_amdgcn_readfirstlane(min(kb, kb1 - 1) * kBlock), step = 8 * a.I;
-  dma4(ln.dma_w + BUF * kOpBytes, rw, ve, vo, soff, step);
-  dma4(ln.dma_x + BUF * kOpBytes, rx, ve, vo, soff, step);
+// The loads of a block: 0..3 its x rows, 4 and 5 the W rows of fragments 0..3,
+// 6 and 7 those of fragments 4..7, 8 its activation scales.  Pieces past the
+// reduction, rows past the matrix and every piece of a block at or past kb1 are
+// fetched from past the buffers and so land as zeros without memory traffic.
+// There is no branch: one here would let the compiler move products of a step
+// into the block behind it, and the waits count loads.
+template <int SC>
+struct Issue {
+  __amdgpu_buffer_rsrc_t rw, rx, rs;
+  int ve, vo, vs;      // lane offsets of even and of odd groups of eight rows; of the scales
+  int x, w, s;         // offsets of the wave's first rows and of the scales
+  int step;            // bytes of eight rows
+};
+
+template <int SC>
+__device__ __forceinline__ Issue<SC> issue_of(const Args& a, const Source<SC>& s, const Lanes& ln, int kb, int kb1) {
+  Issue<SC> i;
+  const int left = kb < kb1 ? a.I - kb * kBlock : 0, k = min(kb, kb1 - 1) * kBlock, n = int(sizeof(scale_t<SC>));
+  i.ve = ln.ce < left ? ln.dr * a.I + ln.ce : kPast;
+  i.vo = ln.co < left ? ln.dr * a.I + ln.co : kPast;
+  i.vs = (ln.tok + int(threadIdx.x) % kWave) * a.KB * n;
+  i.rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(uniform_ptr(s.w)), 0,
+                                           __builtin_amdgcn_readfirstlane(s.wbytes), kRsrcFlags);
+  i.rx = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(uniform_ptr(s.x)), 0,
+                                           __builtin_amdgcn_readfirstlane(s.xbytes), kRsrcFlags);
+  i.rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(uniform_ptr(s.xs)), 0,
+                                           __builtin_amdgcn_readfirstlane(s.xsbytes), kRsrcFlags);
+  i.x = __builtin_amdgcn_readfirstlane(ln.row_x * a.I + k);
+  i.w = __builtin_amdgcn_readfirstlane(ln.row_w * a.I + k);
+  i.s = __builtin_amdgcn_readfirstlane(min(kb, kb1 - 1) * n);
+  i.step = 8 * a.I;
+  return i;
+}
+
+template <int BUF, int J, int SC>
+__device__ __forceinline__ void load(const Lanes& ln, const Issue<SC>& i) {
+  if constexpr (J < 4)
+    dma(ln.dma_x + unsigned(BUF * kOpBytes + J * 1024), i.rx, J & 1 ? i.vo : i.ve, i.x + J * i.step);
+  else if constexpr (J < 8) {
+    constexpr int g = J < 6 ? J - 4 : J - 6 + 8;   // group of eight rows: 0, 1, 8, 9
+    dma(ln.dma_w + unsigned(BUF * kOpBytes + g * 1024), i.rw, J & 1 ? i.vo : i.ve, i.w + g * i.step);
+  } else
+    dma_scale<SC>(ln.dma_s + unsigned(BUF * kWaves * 256), i.rs, i.vs, i.s);
 }
 
 template <int BUF>
@@ -211,35 +255,18 @@ template <int SC> struct Scales;
 template <> struct Scales<TB_SCALE_E8M0> { int w, x[4]; };
 template <> struct Scales<TB_SCALE_F32> { float x[4]; };
 
-template <int SC>
-struct RawScales {
-  scale_t<SC> w, x[4];
-};
-
-// xs_off: this lane's token of x fragment 0 in the tile, times KB scales.
-// Tokens past the last read a zero scale.
-template <int SC>
-__device__ __forceinline__ RawScales<SC> load_scales(const Args& a, const Source<SC>& s, int xs_off, int kb) {
-  RawScales<SC> r;
-  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(uniform_ptr(s.xs)), 0, __builtin_amdgcn_readfirstlane(s.xsbytes), kRsrcFlags);
-  r.w = s.ws[kb];
+template <int BUF, int SC>
+__device__ __forceinline__ Scales<SC> read_scales(const Source<SC>& s, const Lanes& ln, int kb) {
+  Scales<SC> r;
+  const scale_t<SC> w = s.ws[kb];
+  if constexpr (SC == TB_SCALE_E8M0) r.w = int(w);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int soff = __builtin_amdgcn_readfirstlane((j * 16 * a.KB + kb) * int(sizeof(scale_t<SC>)));
-    if constexpr (SC == TB_SCALE_E8M0)
-      r.x[j] = __builtin_amdgcn_raw_buffer_load_b8(rs, xs_off, soff, 0);
-    else
-      r.x[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, xs_off, soff, 0));
+    const uint32_t raw = *reinterpret_cast<const lds_u32*>(ln.s_rd + BUF * (kWaves * 256) + j * 64);
+    if constexpr (SC == TB_SCALE_E8M0) r.x[j] = int(raw);
+    else r.x[j] = __uint_as_float(raw) * w;
   }
   return r;
-}
-
-__device__ __forceinline__ Scales<TB_SCALE_E8M0> use_scales(const RawScales<TB_SCALE_E8M0>& r) {
-  return {int(r.w), {int(r.x[0]), int(r.x[1]), int(r.x[2]), int(r.x[3])}};
-}
-__device__ __forceinline__ Scales<TB_SCALE_F32> use_scales(const RawScales<TB_SCALE_F32>& r) {
-  return {{r.x[0] * r.w, r.x[1] * r.w, r.x[2] * r.w, r.x[3] * r.w}};
 }
 
 // The product of W fragment i (f) and x fragment j into acc[i][j].  With fp32
@@ -263,111 +290,148 @@ __device__ __forceinline__ void finish_block(const Scales<TB_SCALE_F32>& sc, f32
   acc[7][3] += pend * sc.x[3];
 }
 
-// W fragments 2 S and 2 S + 1 with the four x fragments.
-template <int S, int SC>
-__device__ __forceinline__ void mma_pair(const i32x8 (&fa)[2], const i32x8 (&fb)[4], const Scales<SC>& sc,
-                                         f32x4 (&acc)[8][4], f32x4& pend) {
-  product<2 * S, 0, 2 * S - 1, 3>(fa[0], fb[0], sc, acc, pend);
-  product<2 * S, 1, 2 * S, 0>(fa[0], fb[1], sc, acc, pend);
-  product<2 * S, 2, 2 * S, 1>(fa[0], fb[2], sc, acc, pend);
-  product<2 * S, 3, 2 * S, 2>(fa[0], fb[3], sc, acc, pend);
-  product<2 * S + 1, 0, 2 * S, 3>(fa[1], fb[0], sc, acc, pend);
-  product<2 * S + 1, 1, 2 * S + 1, 0>(fa[1], fb[1], sc, acc, pend);
-  product<2 * S + 1, 2, 2 * S + 1, 1>(fa[1], fb[2], sc, acc, pend);
-  product<2 * S + 1, 3, 2 * S + 1, 2>(fa[1], fb[3], sc, acc, pend);
-}
-
 // One block in software-pipelined form.  On entry block kb sits in buffer BUF,
-// its x fragments in fb and W fragments 0, 1 in fa0, its scales in sc; the
-// loads of block kb + 1 into the other buffer and of its scales (raw) are in
-// flight.  The barrier falls before the last quarter of the products, once
-// block kb + 1 has landed and every wave holds its last fragments of BUF;
-// block kb + 2 is then issued into BUF.  The last quarter goes x fragment by x
-// fragment, so that each one's registers take the next block's as soon as its
-// two products are under way.
+// its x fragments in fb, its W fragments 0, 1 in fa0 and its scales in sc; the
+// loads of block kb + 1 into the other buffer are out.
+//   - Once every wave holds its x fragments and W fragments 0..3 (the barrier
+//     after the first quarter of the products), block kb + 2's x and the W rows
+//     of fragments 0..3 are asked for into the same buffer.
+//   - Before the last quarter block kb + 1 must have landed (all but the six
+//     loads just named) and every wave holds its last fragments: the rest of
+//     block kb + 2 is asked for, and the first fragments of kb + 1 are read
+//     under that quarter.
+// The loads go out one by one between products: issued together behind a
+// barrier they keep every wave from its products until the address units have
+// taken them (4096 x 4096 x 8192 with powers of two: 134 us with nine at a
+// time, where the products alone take 90 and the loads alone 85).
+// The last quarter goes x fragment by x fragment, so that each one's registers
+// take the next block's as soon as its two products are under way.
+#define TB_FENCE __builtin_amdgcn_sched_barrier(0)
+#define TB_LOAD(J)              \
+  TB_FENCE;                     \
+  load<BUF, J, SC>(ln, next);   \
+  TB_FENCE
 template <int BUF, int SC>
 __device__ __forceinline__ void k_step(const Args& a, const Source<SC>& s, const Lanes& ln, int kb, int kb1,
                                        i32x8 (&fa0)[2], i32x8 (&fa1)[2], i32x8 (&fb)[4], Scales<SC>& sc,
-                                       RawScales<SC>& raw, f32x4 (&acc)[8][4]) {
+                                       f32x4 (&acc)[8][4]) {
   f32x4 pend;
-#define TB_FENCE __builtin_amdgcn_sched_barrier(0)
+  const Issue<SC> next = issue_of<SC>(a, s, ln, kb + 2, kb1);
   fa1[0] = read_w<BUF>(ln, 2);
   fa1[1] = read_w<BUF>(ln, 3);
   TB_FENCE;
-  mma_pair<0>(fa0, fb, sc, acc, pend);
+  product<0, 0, -1, 3>(fa0[0], fb[0], sc, acc, pend);
+  product<0, 1, 0, 0>(fa0[0], fb[1], sc, acc, pend);
+  product<0, 2, 0, 1>(fa0[0], fb[2], sc, acc, pend);
+  product<0, 3, 0, 2>(fa0[0], fb[3], sc, acc, pend);
+  product<1, 0, 0, 3>(fa0[1], fb[0], sc, acc, pend);
+  product<1, 1, 1, 0>(fa0[1], fb[1], sc, acc, pend);
+  product<1, 2, 1, 1>(fa0[1], fb[2], sc, acc, pend);
+  product<1, 3, 1, 2>(fa0[1], fb[3], sc, acc, pend);
   TB_FENCE;
+  wait_lds();
+  __builtin_amdgcn_s_barrier();
   fa0[0] = read_w<BUF>(ln, 4);
   fa0[1] = read_w<BUF>(ln, 5);
   TB_FENCE;
-  mma_pair<1>(fa1, fb, sc, acc, pend);
+  product<2, 0, 1, 3>(fa1[0], fb[0], sc, acc, pend);
+  product<2, 1, 2, 0>(fa1[0], fb[1], sc, acc, pend);
+  TB_LOAD(0);
+  product<2, 2, 2, 1>(fa1[0], fb[2], sc, acc, pend);
+  product<2, 3, 2, 2>(fa1[0], fb[3], sc, acc, pend);
+  TB_LOAD(1);
+  product<3, 0, 2, 3>(fa1[1], fb[0], sc, acc, pend);
+  product<3, 1, 3, 0>(fa1[1], fb[1], sc, acc, pend);
+  TB_LOAD(2);
+  product<3, 2, 3, 1>(fa1[1], fb[2], sc, acc, pend);
+  product<3, 3, 3, 2>(fa1[1], fb[3], sc, acc, pend);
   TB_FENCE;
   fa1[0] = read_w<BUF>(ln, 6);
   fa1[1] = read_w<BUF>(ln, 7);
+  TB_LOAD(3);
+  product<4, 0, 3, 3>(fa0[0], fb[0], sc, acc, pend);
+  product<4, 1, 4, 0>(fa0[0], fb[1], sc, acc, pend);
+  TB_LOAD(4);
+  product<4, 2, 4, 1>(fa0[0], fb[2], sc, acc, pend);
+  product<4, 3, 4, 2>(fa0[0], fb[3], sc, acc, pend);
+  TB_LOAD(5);
+  product<5, 0, 4, 3>(fa0[1], fb[0], sc, acc, pend);
+  product<5, 1, 5, 0>(fa0[1], fb[1], sc, acc, pend);
+  product<5, 2, 5, 1>(fa0[1], fb[2], sc, acc, pend);
+  product<5, 3, 5, 2>(fa0[1], fb[3], sc, acc, pend);
   TB_FENCE;
-  mma_pair<2>(fa0, fb, sc, acc, pend);
-  TB_FENCE;
-  wait_dma();
-  __syncthreads();
+  wait_loads<6>();
+  __builtin_amdgcn_s_barrier();
   const Scales<SC> now = sc;
-  sc = use_scales(raw);
+  sc = read_scales<1 - BUF, SC>(s, ln, min(kb + 1, kb1 - 1));
   fa0[0] = read_w<1 - BUF>(ln, 0);
   fa0[1] = read_w<1 - BUF>(ln, 1);
-  TB_FENCE;
-  raw = load_scales<SC>(a, s, ln.xs_off, min(kb + 2, kb1 - 1));
-  issue<BUF, SC>(a, s, ln, kb + 2, kb1);
   TB_FENCE;
   product<6, 0, 5, 3>(fa1[0], fb[0], now, acc, pend);
   product<7, 0, 6, 0>(fa1[1], fb[0], now, acc, pend);
   TB_FENCE;
   fb[0] = read_x<1 - BUF>(ln, 0);
-  TB_FENCE;
+  TB_LOAD(6);
   product<6, 1, 7, 0>(fa1[0], fb[1], now, acc, pend);
   product<7, 1, 6, 1>(fa1[1], fb[1], now, acc, pend);
   TB_FENCE;
   fb[1] = read_x<1 - BUF>(ln, 1);
-  TB_FENCE;
+  TB_LOAD(7);
   product<6, 2, 7, 1>(fa1[0], fb[2], now, acc, pend);
   product<7, 2, 6, 2>(fa1[1], fb[2], now, acc, pend);
   TB_FENCE;
   fb[2] = read_x<1 - BUF>(ln, 2);
-  TB_FENCE;
+  TB_LOAD(8);
   product<6, 3, 7, 2>(fa1[0], fb[3], now, acc, pend);
   product<7, 3, 6, 3>(fa1[1], fb[3], now, acc, pend);
   TB_FENCE;
   fb[3] = read_x<1 - BUF>(ln, 3);
   finish_block(now, acc, pend);
   TB_FENCE;
-#undef TB_FENCE
 }
+#undef TB_LOAD
+#undef TB_FENCE
 
 template <int SC>
 __device__ __forceinline__ void k_run(const Args& a, const Source<SC>& s, const Lanes& ln, int kb0, int kb1,
-                                      RawScales<SC> first, RawScales<SC> raw, f32x4 (&acc)[8][4]) {
+                                      f32x4 (&acc)[8][4]) {
   i32x8 fa0[2], fa1[2], fb[4];
-  wait_dma();
+  wait_loads<0>();
   __syncthreads();
-  Scales<SC> sc = use_scales(first);
+  Scales<SC> sc = read_scales<0, SC>(s, ln, kb0);
 #pragma unroll
   for (int j = 0; j < 4; ++j) fb[j] = read_x<0>(ln, j);
   fa0[0] = read_w<0>(ln, 0);
   fa0[1] = read_w<0>(ln, 1);
   int kb = kb0;
   for (; kb + 1 < kb1; kb += 2) {
-    k_step<0, SC>(a, s, ln, kb, kb1, fa0, fa1, fb, sc, raw, acc);
-    k_step<1, SC>(a, s, ln, kb + 1, kb1, fa0, fa1, fb, sc, raw, acc);
+    k_step<0, SC>(a, s, ln, kb, kb1, fa0, fa1, fb, sc, acc);
+    k_step<1, SC>(a, s, ln, kb + 1, kb1, fa0, fa1, fb, sc, acc);
   }
-  if (kb < kb1) k_step<0, SC>(a, s, ln, kb, kb1, fa0, fa1, fb, sc, raw, acc);
-  wait_dma();
+  if (kb < kb1) k_step<0, SC>(a, s, ln, kb, kb1, fa0, fa1, fb, sc, acc);
+  wait_loads<0>();
   __syncthreads();   // the ring is free
 }
 
+template <int BUF, int SC>
+__device__ __forceinline__ void load_block(const Args& a, const Source<SC>& s, const Lanes& ln, int kb, int kb1) {
+  const Issue<SC> i = issue_of<SC>(a, s, ln, kb, kb1);
+  load<BUF, 0, SC>(ln, i);
+  load<BUF, 1, SC>(ln, i);
+  load<BUF, 2, SC>(ln, i);
+  load<BUF, 3, SC>(ln, i);
+  load<BUF, 4, SC>(ln, i);
+  load<BUF, 5, SC>(ln, i);
+  load<BUF, 6, SC>(ln, i);
+  load<BUF, 7, SC>(ln, i);
+  load<BUF, 8, SC>(ln, i);
+}
+
+// The first two blocks of an item (the ring must be free).
 template <int SC>
-__device__ __forceinline__ void prefetch(const Args& a, const Source<SC>& s, const Lanes& ln, const Item& it,
-                                         RawScales<SC>& first, RawScales<SC>& raw) {
-  first = load_scales<SC>(a, s, ln.xs_off, it.kb0);
-  raw = load_scales<SC>(a, s, ln.xs_off, min(it.kb0 + 1, a.KB - 1));
-  issue<0, SC>(a, s, ln, it.kb0, it.kb1);
-  issue<1, SC>(a, s, ln, it.kb0 + 1, it.kb1);
+__device__ __forceinline__ void prefetch(const Args& a, const Source<SC>& s, const Lanes& ln, const Item& it) {
+  load_block<0, SC>(a, s, ln, it.kb0, it.kb1);
+  load_block<1, SC>(a, s, ln, it.kb0 + 1, it.kb1);
 }
 
 // The wave's 128 outputs x 64 tokens as bf16: 16 tokens x 64 outputs at a time
@@ -411,28 +475,28 @@ __device__ __forceinline__ void store_tile(const Args& a, int m0, int n0, const 
 template <int SC>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) void fp8_tiles_kernel(Args a) {
   __shared__ __attribute__((aligned(16))) uint8_t ring[kRingBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t scales[kScaleBytes];
   __shared__ __attribute__((aligned(16))) uint8_t stage[kWaves * kStageBytes];
   const int g = int(blockIdx.x), G = int(gridDim.x);
   const int pos = a.xcd_major ? (g % 8) * (G / 8) + g / 8 : g;
   const int total = a.split_tiles * a.S + (a.tiles_m * a.tiles_n - a.split_tiles);
   if (pos >= total) return;
-  const Lanes ln = make_lanes(ring, a.KB * int(sizeof(scale_t<SC>)));
+  const Lanes ln = make_lanes(ring, scales);
   Item it = item_at(a, pos);
   Source<SC> src = source_of<SC>(a, it);
-  RawScales<SC> first, raw;
-  prefetch<SC>(a, src, ln, it, first, raw);
+  prefetch<SC>(a, src, ln, it);
   for (int v = pos; v < total; v += G) {
     f32x4 acc[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    k_run<SC>(a, src, ln, it.kb0, it.kb1, first, raw, acc);
+    k_run<SC>(a, src, ln, it.kb0, it.kb1, acc);
     const Item cur = it;
     if (v + G < total) {   // the next item's first blocks load while this one is stored
       it = item_at(a, v + G);
       src = source_of<SC>(a, it);
-      prefetch<SC>(a, src, ln, it, first, raw);
+      prefetch<SC>(a, src, ln, it);
     }
     if (cur.slice < 0) {
       store_tile(a, cur.m0, cur.n0, acc, (lds_byte*)stage);
