@@ -92,7 +92,7 @@ __device__ __forceinline__ lds_byte* opaque(lds_byte* p) {
 
 struct Lanes {
   unsigned dma_w, dma_x, dma_s;  // where this wave's loads land in buffer 0
-  int row_w, row_x, tok;         // first row of its loads in the tile; its first token
+  int row, tok;         // first row of its loads in the tile; its first token
   int ce, co;                    // lane offsets' pieces (bytes) in loads of even and of odd groups of eight rows
   int dr;                        // row of the lane in a load
   lds_byte* w_rd[2];             // the fragment's pieces q and q + 4 of W row wo * 128 + lane % 16
@@ -105,14 +105,11 @@ __device__ __forceinline__ Lanes make_lanes(uint8_t* ring, uint8_t* scales) {
   const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave), l = int(threadIdx.x) % kWave;
   const int lr = l & 15, q = l >> 4, wo = w & 1, wt = w >> 1;
   Lanes ln;
-  // W rows: 16 of the fragments 0..3 of one half of the outputs, and 64 rows on
-  // the same of fragments 4..7.  x rows: 32.
-  ln.row_w = (w >> 2) * 128 + (w & 3) * 16;
-  ln.row_x = w * 32;
+  ln.row = w * 32;
   ln.tok = wt * 64;
   const unsigned b0 = unsigned(uintptr_t(base));
-  ln.dma_w = __builtin_amdgcn_readfirstlane(b0 + unsigned(ln.row_w) * kBlock);
-  ln.dma_x = __builtin_amdgcn_readfirstlane(b0 + unsigned(kBOffset) + unsigned(ln.row_x) * kBlock);
+  ln.dma_w = __builtin_amdgcn_readfirstlane(b0 + unsigned(ln.row) * kBlock);
+  ln.dma_x = __builtin_amdgcn_readfirstlane(b0 + unsigned(kBOffset) + unsigned(ln.row) * kBlock);
   ln.dma_s = __builtin_amdgcn_readfirstlane(unsigned(uintptr_t((lds_byte*)scales)) + unsigned(w) * 256u);
   // Groups of eight rows start at multiples of eight: their swizzle is the
   // row's half, with the upper bit flipped in every second group.
@@ -193,12 +190,14 @@ __device__ __forceinline__ Source<SC> source_of(const Args& a, const Item& it) {
   return s;
 }
 
-// The loads of a block: 0..3 its x rows, 4 and 5 the W rows of fragments 0..3,
-// 6 and 7 those of fragments 4..7, 8 its activation scales.  Pieces past the
+// The loads of a block: 0..3 its x rows, 4..7 its W rows, 8 its activation
+// scales.  Pieces past the
 // reduction, rows past the matrix and every piece of a block at or past kb1 are
 // fetched from past the buffers and so land as zeros without memory traffic.
 // There is no branch: one here would let the compiler move products of a step
 // into the block behind it, and the waits count loads.
+constexpr int kBlockLoads = 9;
+
 template <int SC>
 struct Issue {
   __amdgpu_buffer_rsrc_t rw, rx, rs;
@@ -220,8 +219,8 @@ __device__ __forceinline__ Issue<SC> issue_of(const Args& a, const Source<SC>& s
                                            __builtin_amdgcn_readfirstlane(s.xbytes), kRsrcFlags);
   i.rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(uniform_ptr(s.xs)), 0,
                                            __builtin_amdgcn_readfirstlane(s.xsbytes), kRsrcFlags);
-  i.x = __builtin_amdgcn_readfirstlane(ln.row_x * a.I + k);
-  i.w = __builtin_amdgcn_readfirstlane(ln.row_w * a.I + k);
+  i.x = __builtin_amdgcn_readfirstlane(ln.row * a.I + k);
+  i.w = __builtin_amdgcn_readfirstlane(ln.row * a.I + k);
   i.s = __builtin_amdgcn_readfirstlane(min(kb, kb1 - 1) * n);
   i.step = 8 * a.I;
   return i;
@@ -232,8 +231,7 @@ __device__ __forceinline__ void load(const Lanes& ln, const Issue<SC>& i) {
   if constexpr (J < 4)
     dma(ln.dma_x + unsigned(BUF * kOpBytes + J * 1024), i.rx, J & 1 ? i.vo : i.ve, i.x + J * i.step);
   else if constexpr (J < 8) {
-    constexpr int g = J < 6 ? J - 4 : J - 6 + 8;   // group of eight rows: 0, 1, 8, 9
-    dma(ln.dma_w + unsigned(BUF * kOpBytes + g * 1024), i.rw, J & 1 ? i.vo : i.ve, i.w + g * i.step);
+    dma(ln.dma_w + unsigned(BUF * kOpBytes + (J - 4) * 1024), i.rw, J & 1 ? i.vo : i.ve, i.w + (J - 4) * i.step);
   } else
     dma_scale<SC>(ln.dma_s + unsigned(BUF * kWaves * 256), i.rs, i.vs, i.s);
 }
@@ -249,63 +247,47 @@ __device__ __forceinline__ i32x8 read_x(const Lanes& ln, int j) {
               *reinterpret_cast<const lds_u32x4*>(ln.x_rd[1] + BUF * kOpBytes + j * 16 * kBlock));
 }
 
-// The scales of a block as the products take them: bytes for the matrix
-// instruction, or xs * ws.
-template <int SC> struct Scales;
-template <> struct Scales<TB_SCALE_E8M0> { int w, x[4]; };
-template <> struct Scales<TB_SCALE_F32> { float x[4]; };
+// xs * ws of the lane's token in each x fragment.
+struct Scales { float x[4]; };
 
 template <int BUF, int SC>
-__device__ __forceinline__ Scales<SC> read_scales(const Source<SC>& s, const Lanes& ln, int kb) {
-  Scales<SC> r;
-  const scale_t<SC> w = s.ws[kb];
-  if constexpr (SC == TB_SCALE_E8M0) r.w = int(w);
+__device__ __forceinline__ Scales read_scales(const Source<SC>& s, const Lanes& ln, int kb) {
+  Scales r;
+  const float w = scale_value(s.ws[kb]);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t raw = *reinterpret_cast<const lds_u32*>(ln.s_rd + BUF * (kWaves * 256) + j * 64);
-    if constexpr (SC == TB_SCALE_E8M0) r.x[j] = int(raw);
-    else r.x[j] = __uint_as_float(raw) * w;
+    r.x[j] = (SC == TB_SCALE_E8M0 ? scale_value(uint8_t(raw)) : __uint_as_float(raw)) * w;
   }
   return r;
 }
 
-// The product of W fragment i (f) and x fragment j into acc[i][j].  With fp32
-// scales its results stay in `pend` and are added, to where PI, PJ say, under
-// the product that follows (PI < 0: nothing is pending).
+// The product of W fragment I (f) and x fragment J for acc[I][J].  Its results
+// stay in `pend` and are scaled and added, to where PI, PJ say, under the
+// product that follows (PI < 0: nothing is pending).
 template <int I, int J, int PI, int PJ>
-__device__ __forceinline__ void product(const i32x8& f, const i32x8& fx, const Scales<TB_SCALE_E8M0>& sc,
-                                        f32x4 (&acc)[8][4], f32x4&) {
-  acc[I][J] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f, fx, acc[I][J], 0, 0, 0, sc.w, 0, sc.x[J]);
-}
-template <int I, int J, int PI, int PJ>
-__device__ __forceinline__ void product(const i32x8& f, const i32x8& fx, const Scales<TB_SCALE_F32>& sc,
-                                        f32x4 (&acc)[8][4], f32x4& pend) {
+__device__ __forceinline__ void product(const i32x8& f, const i32x8& fx, const Scales& sc, f32x4 (&acc)[8][4],
+                                        f32x4& pend) {
   const f32x4 p =
       __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f, fx, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
   if constexpr (PI >= 0) acc[PI][PJ] += pend * sc.x[PJ];
   pend = p;
 }
-__device__ __forceinline__ void finish_block(const Scales<TB_SCALE_E8M0>&, f32x4 (&)[8][4], f32x4&) {}
-__device__ __forceinline__ void finish_block(const Scales<TB_SCALE_F32>& sc, f32x4 (&acc)[8][4], f32x4& pend) {
-  acc[7][3] += pend * sc.x[3];
-}
 
 // One block in software-pipelined form.  On entry block kb sits in buffer BUF,
-// its x fragments in fb, its W fragments 0, 1 in fa0 and its scales in sc; the
-// loads of block kb + 1 into the other buffer are out.
-//   - Once every wave holds its x fragments and W fragments 0..3 (the barrier
-//     after the first quarter of the products), block kb + 2's x and the W rows
-//     of fragments 0..3 are asked for into the same buffer.
-//   - Before the last quarter block kb + 1 must have landed (all but the six
-//     loads just named) and every wave holds its last fragments: the rest of
-//     block kb + 2 is asked for, and the first fragments of kb + 1 are read
-//     under that quarter.
+// its x fragments in fb, its W fragments 0..3 in fa0 and fa1 and its scales in
+// sc; the loads of block kb + 1 into the other buffer are out.
+//   - The first half of the products (W fragments 0..3) frees fa0 and fa1 for
+//     fragments 4..7, the last that are read from BUF.
+//   - A few products into the second half, one barrier: every wave holds all of
+//     block kb, and block kb + 1 has landed.  From there on block kb + 2 is
+//     asked for into BUF, and each x fragment's registers take the next block's
+//     as soon as their last products are under way, then fa0 and fa1.  So the
+//     reads of a block are spread over half a step (packed into its last
+//     quarter they outlast the products there).
 // The loads go out one by one between products: issued together behind a
 // barrier they keep every wave from its products until the address units have
-// taken them (4096 x 4096 x 8192 with powers of two: 134 us with nine at a
-// time, where the products alone take 90 and the loads alone 85).
-// The last quarter goes x fragment by x fragment, so that each one's registers
-// take the next block's as soon as its two products are under way.
+// taken them.
 #define TB_FENCE __builtin_amdgcn_sched_barrier(0)
 #define TB_LOAD(J)              \
   TB_FENCE;                     \
@@ -313,13 +295,10 @@ __device__ __forceinline__ void finish_block(const Scales<TB_SCALE_F32>& sc, f32
   TB_FENCE
 template <int BUF, int SC>
 __device__ __forceinline__ void k_step(const Args& a, const Source<SC>& s, const Lanes& ln, int kb, int kb1,
-                                       i32x8 (&fa0)[2], i32x8 (&fa1)[2], i32x8 (&fb)[4], Scales<SC>& sc,
+                                       i32x8 (&fa0)[2], i32x8 (&fa1)[2], i32x8 (&fb)[4], Scales& sc,
                                        f32x4 (&acc)[8][4]) {
   f32x4 pend;
   const Issue<SC> next = issue_of<SC>(a, s, ln, kb + 2, kb1);
-  fa1[0] = read_w<BUF>(ln, 2);
-  fa1[1] = read_w<BUF>(ln, 3);
-  TB_FENCE;
   product<0, 0, -1, 3>(fa0[0], fb[0], sc, acc, pend);
   product<0, 1, 0, 0>(fa0[0], fb[1], sc, acc, pend);
   product<0, 2, 0, 1>(fa0[0], fb[2], sc, acc, pend);
@@ -329,64 +308,68 @@ __device__ __forceinline__ void k_step(const Args& a, const Source<SC>& s, const
   product<1, 2, 1, 1>(fa0[1], fb[2], sc, acc, pend);
   product<1, 3, 1, 2>(fa0[1], fb[3], sc, acc, pend);
   TB_FENCE;
-  wait_lds();
-  __builtin_amdgcn_s_barrier();
   fa0[0] = read_w<BUF>(ln, 4);
   fa0[1] = read_w<BUF>(ln, 5);
   TB_FENCE;
   product<2, 0, 1, 3>(fa1[0], fb[0], sc, acc, pend);
   product<2, 1, 2, 0>(fa1[0], fb[1], sc, acc, pend);
-  TB_LOAD(0);
   product<2, 2, 2, 1>(fa1[0], fb[2], sc, acc, pend);
   product<2, 3, 2, 2>(fa1[0], fb[3], sc, acc, pend);
-  TB_LOAD(1);
+  TB_FENCE;
+  fa1[0] = read_w<BUF>(ln, 6);
+  TB_FENCE;
   product<3, 0, 2, 3>(fa1[1], fb[0], sc, acc, pend);
   product<3, 1, 3, 0>(fa1[1], fb[1], sc, acc, pend);
-  TB_LOAD(2);
   product<3, 2, 3, 1>(fa1[1], fb[2], sc, acc, pend);
   product<3, 3, 3, 2>(fa1[1], fb[3], sc, acc, pend);
   TB_FENCE;
-  fa1[0] = read_w<BUF>(ln, 6);
   fa1[1] = read_w<BUF>(ln, 7);
-  TB_LOAD(3);
+  TB_FENCE;
   product<4, 0, 3, 3>(fa0[0], fb[0], sc, acc, pend);
-  product<4, 1, 4, 0>(fa0[0], fb[1], sc, acc, pend);
-  TB_LOAD(4);
-  product<4, 2, 4, 1>(fa0[0], fb[2], sc, acc, pend);
-  product<4, 3, 4, 2>(fa0[0], fb[3], sc, acc, pend);
-  TB_LOAD(5);
-  product<5, 0, 4, 3>(fa0[1], fb[0], sc, acc, pend);
-  product<5, 1, 5, 0>(fa0[1], fb[1], sc, acc, pend);
-  product<5, 2, 5, 1>(fa0[1], fb[2], sc, acc, pend);
-  product<5, 3, 5, 2>(fa0[1], fb[3], sc, acc, pend);
+  product<5, 0, 4, 0>(fa0[1], fb[0], sc, acc, pend);
+  product<4, 1, 5, 0>(fa0[0], fb[1], sc, acc, pend);
+  product<5, 1, 4, 1>(fa0[1], fb[1], sc, acc, pend);
   TB_FENCE;
-  wait_loads<6>();
+  wait_loads<0>();
   __builtin_amdgcn_s_barrier();
-  const Scales<SC> now = sc;
+  const Scales now = sc;
   sc = read_scales<1 - BUF, SC>(s, ln, min(kb + 1, kb1 - 1));
-  fa0[0] = read_w<1 - BUF>(ln, 0);
-  fa0[1] = read_w<1 - BUF>(ln, 1);
   TB_FENCE;
-  product<6, 0, 5, 3>(fa1[0], fb[0], now, acc, pend);
+  product<6, 0, 5, 1>(fa1[0], fb[0], now, acc, pend);
+  TB_LOAD(0);
   product<7, 0, 6, 0>(fa1[1], fb[0], now, acc, pend);
   TB_FENCE;
   fb[0] = read_x<1 - BUF>(ln, 0);
-  TB_LOAD(6);
+  TB_LOAD(1);
   product<6, 1, 7, 0>(fa1[0], fb[1], now, acc, pend);
+  TB_LOAD(2);
   product<7, 1, 6, 1>(fa1[1], fb[1], now, acc, pend);
   TB_FENCE;
   fb[1] = read_x<1 - BUF>(ln, 1);
-  TB_LOAD(7);
-  product<6, 2, 7, 1>(fa1[0], fb[2], now, acc, pend);
+  TB_LOAD(3);
+  product<4, 2, 7, 1>(fa0[0], fb[2], now, acc, pend);
+  TB_LOAD(4);
+  product<5, 2, 4, 2>(fa0[1], fb[2], now, acc, pend);
+  TB_LOAD(5);
+  product<6, 2, 5, 2>(fa1[0], fb[2], now, acc, pend);
+  TB_LOAD(6);
   product<7, 2, 6, 2>(fa1[1], fb[2], now, acc, pend);
   TB_FENCE;
   fb[2] = read_x<1 - BUF>(ln, 2);
+  TB_LOAD(7);
+  product<4, 3, 7, 2>(fa0[0], fb[3], now, acc, pend);
+  product<5, 3, 4, 3>(fa0[1], fb[3], now, acc, pend);
+  TB_FENCE;
+  fa0[0] = read_w<1 - BUF>(ln, 0);
+  fa0[1] = read_w<1 - BUF>(ln, 1);
   TB_LOAD(8);
-  product<6, 3, 7, 2>(fa1[0], fb[3], now, acc, pend);
+  product<6, 3, 5, 3>(fa1[0], fb[3], now, acc, pend);
   product<7, 3, 6, 3>(fa1[1], fb[3], now, acc, pend);
   TB_FENCE;
   fb[3] = read_x<1 - BUF>(ln, 3);
-  finish_block(now, acc, pend);
+  fa1[0] = read_w<1 - BUF>(ln, 2);
+  fa1[1] = read_w<1 - BUF>(ln, 3);
+  acc[7][3] += pend * now.x[3];
   TB_FENCE;
 }
 #undef TB_LOAD
@@ -396,13 +379,16 @@ template <int SC>
 __device__ __forceinline__ void k_run(const Args& a, const Source<SC>& s, const Lanes& ln, int kb0, int kb1,
                                       f32x4 (&acc)[8][4]) {
   i32x8 fa0[2], fa1[2], fb[4];
-  wait_loads<0>();
+  // Block kb0 has landed (the nine loads of the next one may be out).
+  wait_loads<kBlockLoads>();
   __syncthreads();
-  Scales<SC> sc = read_scales<0, SC>(s, ln, kb0);
+  Scales sc = read_scales<0, SC>(s, ln, kb0);
 #pragma unroll
   for (int j = 0; j < 4; ++j) fb[j] = read_x<0>(ln, j);
   fa0[0] = read_w<0>(ln, 0);
   fa0[1] = read_w<0>(ln, 1);
+  fa1[0] = read_w<0>(ln, 2);
+  fa1[1] = read_w<0>(ln, 3);
   int kb = kb0;
   for (; kb + 1 < kb1; kb += 2) {
     k_step<0, SC>(a, s, ln, kb, kb1, fa0, fa1, fb, sc, acc);
