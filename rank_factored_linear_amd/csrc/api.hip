@@ -706,7 +706,8 @@ tb_status tb_quantize_activations(const void* x, void* q, void* scale, int64_t m
   if (!aligned16(x) || !aligned16(q)) return fail(TB_ERR_UNSUPPORTED, "x and q must be 16-byte aligned");
   if (!aligned_to(scale, scale_bytes(scale_type)))
     return fail(TB_ERR_UNSUPPORTED, "scale must be aligned to its element size");
-  hipError_t e = launch_quantize_rows(dtype, scale_type, x, q, scale, m, in_dim, static_cast<hipStream_t>(stream));
+  hipError_t e = launch_quantize_rows(dtype, scale_type, x, q, scale, ScaleStrides{fp8_blocks(in_dim), 1}, m, in_dim,
+                                      static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "launching the activation quantiser");
   return ok();
 }

@@ -58,6 +58,7 @@ struct Args {
   int split_tiles, S;   // the first split_tiles tiles are cut into S slices
   int xcd_major;        // workgroup g takes position (g % 8) * (grid / 8) + g / 8
   int wide;             // y 16-byte aligned and O a multiple of 8
+  int64_t xs_t, xs_k;   // strides of xs (ScaleStrides)
 };
 
 // Tile u of the processing order: groups of eight token tiles walked column by
@@ -169,7 +170,7 @@ template <int SC>
 struct Source {
   const uint8_t* w;
   const uint8_t* x;
-  const uint8_t* xs;
+  const scale_t<SC>* xs;
   int wbytes, xbytes, xsbytes;
   const scale_t<SC>* ws;
 };
@@ -182,8 +183,8 @@ __device__ __forceinline__ Source<SC> source_of(const Args& a, const Item& it) {
   s.x = a.x + size_t(it.m0) * a.I;
   s.wbytes = rows_w * a.I;
   s.xbytes = rows_x * a.I;
-  s.xs = static_cast<const uint8_t*>(a.xs) + size_t(it.m0) * a.KB * sizeof(scale_t<SC>);
-  s.xsbytes = rows_x * a.KB * int(sizeof(scale_t<SC>));
+  s.xs = static_cast<const scale_t<SC>*>(a.xs) + it.m0 * a.xs_t;
+  s.xsbytes = int(((rows_x - 1) * a.xs_t + 1) * int64_t(sizeof(scale_t<SC>)));
   // The wave's 128 outputs are one weight block (a block past the last: any will do).
   const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave), blocks = (a.O + kBlock - 1) / kBlock;
   s.ws = static_cast<const scale_t<SC>*>(a.ws) + size_t(min(it.n0 / kBlock + (w & 1), blocks - 1)) * a.KB;
@@ -202,7 +203,7 @@ template <int SC>
 struct Issue {
   __amdgpu_buffer_rsrc_t rw, rx, rs;
   int ve, vo, vs;      // lane offsets of even and of odd groups of eight rows; of the scales
-  int x, w, s;         // offsets of the wave's first rows and of the scales
+  int x, w;            // offsets of the wave's first rows
   int step;            // bytes of eight rows
 };
 
@@ -212,16 +213,15 @@ __device__ __forceinline__ Issue<SC> issue_of(const Args& a, const Source<SC>& s
   const int left = kb < kb1 ? a.I - kb * kBlock : 0, k = min(kb, kb1 - 1) * kBlock, n = int(sizeof(scale_t<SC>));
   i.ve = ln.ce < left ? ln.dr * a.I + ln.ce : kPast;
   i.vo = ln.co < left ? ln.dr * a.I + ln.co : kPast;
-  i.vs = (ln.tok + int(threadIdx.x) % kWave) * a.KB * n;
+  i.vs = (ln.tok + int(threadIdx.x) % kWave) * int(a.xs_t) * n;
   i.rw = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(uniform_ptr(s.w)), 0,
                                            __builtin_amdgcn_readfirstlane(s.wbytes), kRsrcFlags);
   i.rx = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(uniform_ptr(s.x)), 0,
                                            __builtin_amdgcn_readfirstlane(s.xbytes), kRsrcFlags);
-  i.rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(uniform_ptr(s.xs)), 0,
+  i.rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(uniform_ptr(reinterpret_cast<const uint8_t*>(s.xs + min(kb, kb1 - 1) * a.xs_k))), 0,
                                            __builtin_amdgcn_readfirstlane(s.xsbytes), kRsrcFlags);
   i.x = __builtin_amdgcn_readfirstlane(ln.row * a.I + k);
   i.w = __builtin_amdgcn_readfirstlane(ln.row * a.I + k);
-  i.s = __builtin_amdgcn_readfirstlane(min(kb, kb1 - 1) * n);
   i.step = 8 * a.I;
   return i;
 }
@@ -233,7 +233,7 @@ __device__ __forceinline__ void load(const Lanes& ln, const Issue<SC>& i) {
   else if constexpr (J < 8) {
     dma(ln.dma_w + unsigned(BUF * kOpBytes + (J - 4) * 1024), i.rw, J & 1 ? i.vo : i.ve, i.w + (J - 4) * i.step);
   } else
-    dma_scale<SC>(ln.dma_s + unsigned(BUF * kWaves * 256), i.rs, i.vs, i.s);
+    dma_scale<SC>(ln.dma_s + unsigned(BUF * kWaves * 256), i.rs, i.vs, 0);
 }
 
 template <int BUF>
@@ -497,32 +497,36 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
   }
 }
 
-// The slices of the cut tiles, added in slice order: one workgroup for four
-// outputs' pieces (i) of a tile, all its tokens.
+// The slices of the cut tiles, added in slice order: one workgroup for 16 of
+// each wave's tokens (x fragment j) and 64 of its outputs (W fragments 4 h ..
+// + 3), so that a token's outputs leave as a whole line.
 __global__ __launch_bounds__(kThreads) void fp8_tiles_join_kernel(Args a) {
-  const int u = int(blockIdx.x) >> 3, i = int(blockIdx.x) & 7;
+  const int u = int(blockIdx.x) >> 3, j = int(blockIdx.x) & 3, h = (int(blockIdx.x) >> 2) & 1;
   const int w = int(threadIdx.x) / kWave, l = int(threadIdx.x) % kWave, lr = l & 15, q = l >> 4;
   int m0, n0;
   tile_at(a, u, m0, n0);
-  const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + (size_t(u) * kPieces + i * 4) * kThreads + threadIdx.x;
+  const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + (size_t(u) * kPieces + h * 16 + j) * kThreads + threadIdx.x;
+  const size_t next = size_t(a.split_tiles) * kPieces * kThreads;
   f32x4 sum[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) sum[j] = p[j * kThreads];
+  for (int i = 0; i < 4; ++i) sum[i] = __builtin_nontemporal_load(p + i * 4 * kThreads);
+#pragma unroll 4
   for (int s = 1; s < a.S; ++s)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sum[j] += p[(size_t(s) * a.split_tiles * kPieces + j) * kThreads];
+    for (int i = 0; i < 4; ++i) sum[i] += __builtin_nontemporal_load(p + s * next + i * 4 * kThreads);
+  const int t = m0 + (w >> 1) * 64 + j * 16 + lr;
+  if (t >= a.M) return;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int t = m0 + (w >> 1) * 64 + j * 16 + lr, o = n0 + (w & 1) * 128 + i * 16 + q * 4;
-    if (t >= a.M || o >= a.O) continue;
+  for (int i = 0; i < 4; ++i) {
+    const int o = n0 + (w & 1) * 128 + h * 64 + i * 16 + q * 4;
+    if (o >= a.O) continue;
     bf16_t* dst = a.y + size_t(t) * a.O + o;
     if (a.wide) {
-      *reinterpret_cast<u32x2*>(dst) = u32x2{pack_bf16(sum[j][0], sum[j][1]),
-                                             pack_bf16(sum[j][2], sum[j][3])};
+      *reinterpret_cast<u32x2*>(dst) = u32x2{pack_bf16(sum[i][0], sum[i][1]), pack_bf16(sum[i][2], sum[i][3])};
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (o + e < a.O) dst[e] = bf16_t{f32_to_bf16(sum[j][e])};
+        if (o + e < a.O) dst[e] = bf16_t{f32_to_bf16(sum[i][e])};
     }
   }
 }
@@ -553,13 +557,13 @@ Fp8TilePlan plan_fp8_tiles(int64_t m, int64_t out_dim, int64_t in_dim, int cus) 
   return p;
 }
 
-hipError_t launch_fp8_tiles(const Fp8TilePlan& p, tb_scale scale_type, const void* x, const void* xs, const void* w,
-                            const void* ws, void* y, float* part, int64_t m, int64_t out_dim, int64_t in_dim,
+hipError_t launch_fp8_tiles(const Fp8TilePlan& p, tb_scale scale_type, const void* x, const void* xs, ScaleStrides ss,
+                            const void* w, const void* ws, void* y, float* part, int64_t m, int64_t out_dim, int64_t in_dim,
                             hipStream_t stream) {
   const int wide = out_dim % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15u) == 0;
   const Args a{static_cast<const uint8_t*>(x), xs, static_cast<const uint8_t*>(w), ws, static_cast<bf16_t*>(y), part,
                int(m), int(out_dim), int(in_dim), int(fp8_blocks(in_dim)), p.tiles_m, p.tiles_n, p.split_tiles, p.S,
-               p.xcd_major, wide};
+               p.xcd_major, wide, ss.token, ss.block};
   const dim3 grid(unsigned(p.grid)), block(kThreads);
   if (scale_type == TB_SCALE_E8M0)
     hipLaunchKernelGGL(fp8_tiles_kernel<TB_SCALE_E8M0>, grid, block, 0, stream, a);

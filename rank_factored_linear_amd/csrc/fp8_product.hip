@@ -65,6 +65,7 @@ struct DecodeArgs {
   int M, O, I, KB;
   int wide;  // y rows can be written four outputs at a time
   int rows;  // output rows of a workgroup
+  int xs_t, xs_k;   // strides of xs (ScaleStrides)
 };
 
 constexpr unsigned kRsrcFlags = 0x00020000u;  // buffer descriptor word 3: 32-bit data format
@@ -197,7 +198,7 @@ __global__ __launch_bounds__(kDecodeWaves* kWave) void fp8_decode_kernel(DecodeA
 
   const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + size_t(o0) * a.I, int64_t(rows) * a.I);
   const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x, int64_t(a.M) * a.I * int(sizeof(XE)));
-  const __amdgpu_buffer_rsrc_t rxs = rows_rsrc(a.xs, int64_t(a.M) * a.KB * int(sizeof(scale_t<SC>)));
+  const __amdgpu_buffer_rsrc_t rxs = rows_rsrc(a.xs, (int64_t(a.M - 1) * a.xs_t + int64_t(a.KB - 1) * a.xs_k + 1) * int(sizeof(scale_t<SC>)));
   // The rows lie in one weight block or, from row `edge` on, in the next one too.
   const int edge = kBlock - o0 % kBlock;
   const bool two = edge < rows;
@@ -235,7 +236,7 @@ __global__ __launch_bounds__(kDecodeWaves* kWave) void fp8_decode_kernel(DecodeA
     }
     if constexpr (XM == kXGiven) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) s.xs[n] = load_scale<SC>(rxs, lr * a.KB, kb + n * 16 * a.KB);
+      for (int n = 0; n < NT; ++n) s.xs[n] = load_scale<SC>(rxs, (lr + n * 16) * a.xs_t, kb * a.xs_k);
     }
     s.ws[0] = load_scale<SC>(rws, 0, kb);
     s.ws[1] = load_scale<SC>(rws, 0, kb + a.KB);   // (past the descriptor where there is one block: zero)
@@ -368,6 +369,7 @@ struct GemmArgs {
   int M, O, I, KB;
   int tiles_m, tiles_n, S;
   int wide;
+  int64_t xs_t, xs_k;   // strides of xs (ScaleStrides)
 };
 
 // Tile u's first token and output: groups of eight token tiles walked column
@@ -433,15 +435,15 @@ __global__ __launch_bounds__(kGemmThreads, 2) void fp8_gemm_kernel(GemmArgs a) {
   const int rows_w = min(a.O - n0, kTile), rows_x = min(a.M - m0, TM);
   const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + size_t(n0) * a.I, int64_t(rows_w) * a.I);
   const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x + size_t(m0) * a.I, int64_t(rows_x) * a.I);
-  const __amdgpu_buffer_rsrc_t rs =
-      rows_rsrc(static_cast<const scale_t<SC>*>(a.xs) + size_t(m0) * a.KB, int64_t(rows_x) * a.KB * int(sizeof(scale_t<SC>)));
   const scale_t<SC>* ws = static_cast<const scale_t<SC>*>(a.ws) + size_t(n0 / kBlock) * a.KB;
   // Load j of an operand: row 8 (w loads + j) + l / 8, the piece that the
   // swizzle keeps at position l % 8; eight rows further on the swizzle differs
   // in its upper bit only.
   const int dr = l >> 3, pe = (l & 7) ^ (dr >> 1), po = pe ^ 4;
   const unsigned b0 = unsigned(uintptr_t(base));
-  const int soff_scale = (wt * 32 + (l & 31)) * a.KB * int(sizeof(scale_t<SC>));
+  const scale_t<SC>* xs = static_cast<const scale_t<SC>*>(a.xs) + int64_t(m0) * a.xs_t;
+  const int64_t xs_bytes = (int64_t(rows_x - 1) * a.xs_t + 1) * int(sizeof(scale_t<SC>));
+  const int xs_off = (wt * 32 + (l & 31)) * int(a.xs_t) * int(sizeof(scale_t<SC>));
   auto issue = [&](int slot, int kb) {
     const int left = kb < kb1 ? a.I - kb * kBlock : 0, k = min(kb, kb1 - 1) * kBlock;
     const int ve = pe * 16 < left ? dr * a.I + pe * 16 : kPast, vo = po * 16 < left ? dr * a.I + po * 16 : kPast;
@@ -453,7 +455,7 @@ __global__ __launch_bounds__(kGemmThreads, 2) void fp8_gemm_kernel(GemmArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) dma16(d + kX + (w * 2 + j) * 1024, rx, j ? vo : ve, k + (w * 2 + j) * 8 * a.I);
-    dma_scale<SC>(d + kScales + w * 256, rs, soff_scale, min(kb, kb1 - 1) * int(sizeof(scale_t<SC>)));
+    dma_scale<SC>(d + kScales + w * 256, rows_rsrc(xs + min(kb, kb1 - 1) * a.xs_k, xs_bytes), xs_off, 0);
   };
 
   f32x4 acc[4][2];
@@ -663,10 +665,12 @@ hipError_t launch_fp8_product(const Fp8Plan& p, tb_dtype x_dtype, tb_dtype y_dty
                               const void* xs, const void* w, const void* ws, void* y, int64_t m, int64_t out_dim,
                               int64_t in_dim, char* data, hipStream_t stream) {
   const bool e8 = scale_type == TB_SCALE_E8M0;
+  ScaleStrides ss{fp8_blocks(in_dim), 1};
   if (x_dtype != TB_E4M3 && !p.fused) {
     void* xq = data + p.off_xq;
     void* sq = data + p.off_xs;
-    hipError_t e = launch_quantize_rows(x_dtype, scale_type, x, xq, sq, m, in_dim, stream);
+    ss = ScaleStrides{1, m};
+    hipError_t e = launch_quantize_rows(x_dtype, scale_type, x, xq, sq, ss, m, in_dim, stream);
     if (e != hipSuccess) return e;
     x = xq;
     xs = sq;
@@ -677,17 +681,17 @@ hipError_t launch_fp8_product(const Fp8Plan& p, tb_dtype x_dtype, tb_dtype y_dty
   const int KB = int(fp8_blocks(in_dim));
   if (p.decode) {
     const DecodeArgs a{x, xs, static_cast<const uint8_t*>(w), ws, y, int(m), int(out_dim), int(in_dim), KB,
-                       wide && p.rows % 4 == 0, p.rows};
+                       wide && p.rows % 4 == 0, p.rows, int(ss.token), int(ss.block)};
     if (y_dtype == TB_BF16)
       return e8 ? decode_x<TB_SCALE_E8M0, bf16_t>(x_dtype, a, stream) : decode_x<TB_SCALE_F32, bf16_t>(x_dtype, a, stream);
     return e8 ? decode_x<TB_SCALE_E8M0, float>(x_dtype, a, stream) : decode_x<TB_SCALE_F32, float>(x_dtype, a, stream);
   }
   if (p.big)
-    return launch_fp8_tiles(p.tile, scale_type, x, xs, w, ws, y, reinterpret_cast<float*>(data + p.off_part), m,
+    return launch_fp8_tiles(p.tile, scale_type, x, xs, ss, w, ws, y, reinterpret_cast<float*>(data + p.off_part), m,
                             out_dim, in_dim, stream);
   const GemmArgs a{static_cast<const uint8_t*>(x), xs, static_cast<const uint8_t*>(w), ws, y,
                    reinterpret_cast<float*>(data + p.off_part), int(m), int(out_dim), int(in_dim), KB, p.tiles_m,
-                   p.tiles_n, p.S, wide};
+                   p.tiles_n, p.S, wide, ss.token, ss.block};
   if (y_dtype == TB_BF16) return e8 ? gemm_go<TB_SCALE_E8M0, bf16_t>(a, stream) : gemm_go<TB_SCALE_F32, bf16_t>(a, stream);
   return e8 ? gemm_go<TB_SCALE_E8M0, float>(a, stream) : gemm_go<TB_SCALE_F32, float>(a, stream);
 }

@@ -22,8 +22,8 @@ constexpr int kSeg = 8;
 
 template <typename E, int SC>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const E* __restrict__ x, uint8_t* __restrict__ q,
-                                                                 scale_t<SC>* __restrict__ scale, int64_t M, int I,
-                                                                 int KB) {
+                                                                 scale_t<SC>* __restrict__ scale, ScaleStrides ss,
+                                                                 int64_t M, int I, int KB) {
   const int l = int(threadIdx.x) & 63;
   const int64_t row = int64_t(blockIdx.x) * (kThreads / kWave) + (threadIdx.x >> 6);
   if (row >= M) return;
@@ -51,7 +51,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const E* __rest
     if (c < I)
       *reinterpret_cast<u32x2*>(qr + c) = u32x2{pack4(t[0] * by, t[1] * by, t[2] * by, t[3] * by),
                                                 pack4(t[4] * by, t[5] * by, t[6] * by, t[7] * by)};
-    if ((l & 15) == 0 && kb < KB) scale[row * KB + kb] = st;
+    if ((l & 15) == 0 && kb < KB) scale[row * ss.token + kb * ss.block] = st;
   }
 }
 
@@ -352,11 +352,12 @@ __global__ __launch_bounds__(kThreads, 3) void rebuild_ring_kernel(const bf16_t*
 }  // namespace ring
 
 template <typename E, int SC>
-hipError_t rows_typed(const void* x, void* q, void* scale, int64_t m, int64_t in_dim, hipStream_t stream) {
+hipError_t rows_typed(const void* x, void* q, void* scale, ScaleStrides ss, int64_t m, int64_t in_dim,
+                      hipStream_t stream) {
   const int KB = int(fp8_blocks(in_dim));
   const dim3 grid(unsigned((m + kThreads / kWave - 1) / (kThreads / kWave)), unsigned((KB + kSeg - 1) / kSeg));
   hipLaunchKernelGGL((quantize_rows_kernel<E, SC>), grid, dim3(kThreads), 0, stream, static_cast<const E*>(x),
-                     static_cast<uint8_t*>(q), static_cast<scale_t<SC>*>(scale), m, int(in_dim), KB);
+                     static_cast<uint8_t*>(q), static_cast<scale_t<SC>*>(scale), ss, m, int(in_dim), KB);
   return hipGetLastError();
 }
 
@@ -383,14 +384,14 @@ hipError_t blocks_typed(const void* s, const void* w0, const void* u, const void
 
 }  // namespace
 
-hipError_t launch_quantize_rows(tb_dtype dtype, tb_scale scale_type, const void* x, void* q, void* scale, int64_t m,
-                                int64_t in_dim, hipStream_t stream) {
+hipError_t launch_quantize_rows(tb_dtype dtype, tb_scale scale_type, const void* x, void* q, void* scale,
+                                ScaleStrides ss, int64_t m, int64_t in_dim, hipStream_t stream) {
   const bool e8 = scale_type == TB_SCALE_E8M0;
   if (dtype == TB_BF16)
-    return e8 ? rows_typed<bf16_t, TB_SCALE_E8M0>(x, q, scale, m, in_dim, stream)
-              : rows_typed<bf16_t, TB_SCALE_F32>(x, q, scale, m, in_dim, stream);
-  return e8 ? rows_typed<float, TB_SCALE_E8M0>(x, q, scale, m, in_dim, stream)
-            : rows_typed<float, TB_SCALE_F32>(x, q, scale, m, in_dim, stream);
+    return e8 ? rows_typed<bf16_t, TB_SCALE_E8M0>(x, q, scale, ss, m, in_dim, stream)
+              : rows_typed<bf16_t, TB_SCALE_F32>(x, q, scale, ss, m, in_dim, stream);
+  return e8 ? rows_typed<float, TB_SCALE_E8M0>(x, q, scale, ss, m, in_dim, stream)
+            : rows_typed<float, TB_SCALE_F32>(x, q, scale, ss, m, in_dim, stream);
 }
 
 hipError_t launch_rebuild_blocks(tb_dtype dtype, tb_scale scale_type, const void* s, const void* w0, const void* u,

@@ -181,9 +181,17 @@ int launch_lowrank_factors(tb_dtype dtype, const void* const* weights, int n, co
 constexpr int kFp8Block = 128;
 inline int64_t fp8_blocks(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
 
+// Where an activation scale lies: of token t and block b at t * token + b * block
+// (elements).  The public layout is token-major; a product that quantises x
+// itself keeps its scales block-major in the workspace, so that the scales of
+// neighbouring tokens are one line (4096 x 4096 x 8192: 122 -> 118 us).
+struct ScaleStrides {
+  int64_t token, block;
+};
+
 // x [m, in_dim] -> e4m3 and one scale per row and 128 columns.
-hipError_t launch_quantize_rows(tb_dtype dtype, tb_scale scale_type, const void* x, void* q, void* scale, int64_t m,
-                                int64_t in_dim, hipStream_t stream);
+hipError_t launch_quantize_rows(tb_dtype dtype, tb_scale scale_type, const void* x, void* q, void* scale,
+                                ScaleStrides ss, int64_t m, int64_t in_dim, hipStream_t stream);
 // diag(s) . W0 + U . V^T (s NULL: unit scale) -> e4m3 and one scale per 128 x 128 block.
 hipError_t launch_rebuild_blocks(tb_dtype dtype, tb_scale scale_type, const void* s, const void* w0, const void* u,
                                  const void* v, void* q, void* scale, int64_t out_dim, int64_t in_dim, int64_t rank,
@@ -200,8 +208,8 @@ struct Fp8TilePlan {
   size_t part_bytes;
 };
 Fp8TilePlan plan_fp8_tiles(int64_t m, int64_t out_dim, int64_t in_dim, int cus);
-hipError_t launch_fp8_tiles(const Fp8TilePlan& p, tb_scale scale_type, const void* x, const void* xs, const void* w,
-                            const void* ws, void* y, float* part, int64_t m, int64_t out_dim, int64_t in_dim,
+hipError_t launch_fp8_tiles(const Fp8TilePlan& p, tb_scale scale_type, const void* x, const void* xs, ScaleStrides ss,
+                            const void* w, const void* ws, void* y, float* part, int64_t m, int64_t out_dim, int64_t in_dim,
                             hipStream_t stream);
 
 struct Fp8Plan {
