@@ -68,12 +68,14 @@ typedef enum tb_scale {
 /* Columns of an activation block; rows and columns of a weight block. */
 #define TB_FP8_BLOCK 128
 
-/* Largest in_dim of the 8-bit calls. */
+/* Largest in_dim and token count of the 8-bit calls. */
 #define TB_FP8_MAX_IN_DIM (1 << 22)
+#define TB_FP8_MAX_TOKENS (1 << 24)
 
-/* Largest head of tb_head_norm_rotate, and most heads of one token over all parts. */
+/* Largest head of tb_head_norm_rotate, most heads of one token over all parts, most tokens. */
 #define TB_MAX_HEAD_DIM 1024
 #define TB_MAX_HEADS 65535
+#define TB_MAX_HEAD_TOKENS (1 << 25)
 
 /* Most projections one tb_linear_forward_group call takes. */
 #define TB_MAX_GROUP 8
@@ -421,8 +423,8 @@ tb_status tb_refine_shared_block(const void *const *weights, const float *const 
  *                  a' = max(a, 2^-100), each operation rounded to fp32.
  * e4m3 rounds to nearest, ties to even.  A block that holds an infinity or NaN
  * gets a NaN scale and NaN entries.
- *   m >= 0 (0: nothing is enqueued), in_dim >= 8, % 8 == 0 and <=
- *   TB_FP8_MAX_IN_DIM.  x and q 16-byte aligned, scale element aligned.
+ *   0 <= m <= TB_FP8_MAX_TOKENS (0: nothing is enqueued), in_dim >= 8, % 8 == 0
+ *   and <= TB_FP8_MAX_IN_DIM.  x and q 16-byte aligned, scale element aligned.
  *   Errors: TB_ERR_INVALID_ARGUMENT, TB_ERR_UNSUPPORTED, TB_ERR_HIP.
  */
 tb_status tb_quantize_activations(const void *x, void *q, void *scale, int64_t m, int64_t in_dim, tb_dtype dtype,
@@ -461,8 +463,8 @@ tb_status tb_reconstruct_weight_fp8(const void *s, const void *w0, const void *u
  *   y  [m, out_dim] in y_dtype (TB_BF16 or TB_F32), must not alias inputs.
  *   Weights that share an input can be stacked along out_dim into one call
  *   where every one but the last has a multiple of 128 rows.
- *   m >= 0 (0: nothing is enqueued), out_dim >= 1, in_dim % 16 == 0 and <=
- *   TB_FP8_MAX_IN_DIM; x, wq 16-byte aligned.  The product xs * ws of two
+ *   0 <= m <= TB_FP8_MAX_TOKENS (0: nothing is enqueued), out_dim >= 1,
+ *   in_dim % 16 == 0 and <= TB_FP8_MAX_IN_DIM; x, wq 16-byte aligned.  The product xs * ws of two
  *   scales must be finite in fp32.
  *   workspace: at least tb_dense_forward_fp8_workspace_size() bytes, 256-byte
  *   aligned, no initial contents (NULL when 0).  Calls that may run at the same
@@ -483,7 +485,7 @@ tb_status tb_dense_forward_fp8(const void *x, const void *x_scale, const void *w
  */
 typedef struct tb_head_part {
   const void *x;
-  void *y;            /* x itself (same strides) or memory that overlaps no part's x */
+  void *y;            /* x itself (same strides), or memory that overlaps no part's x and no other y */
   const void *weight; /* [head_dim], or NULL: no weight (and no offset) */
   int64_t heads;
   int64_t x_token_stride, x_head_stride;
@@ -503,7 +505,7 @@ typedef struct tb_head_part {
  * other elements are y = z.  Sums and products in fp32, angles in fp64 (right
  * to fp32 for positions up to 2^30), one rounding to y.
  *   n: 1 .. TB_MAX_GROUP parts (host array) of one dtype (x, y and weight);
- *   tokens >= 0 (0: nothing is enqueued); 1 <= head_dim <= TB_MAX_HEAD_DIM;
+ *   0 <= tokens <= TB_MAX_HEAD_TOKENS (0: nothing is enqueued); 1 <= head_dim <= TB_MAX_HEAD_DIM;
  *   0 <= rot_dim <= head_dim, even; positions [tokens] int64 and freqs [r]
  *   double, device (may be NULL where rot_dim is 0); eps >= 0.  Heads add up
  *   to TB_MAX_HEADS at most; a part may have none.  Strides are >= 0 and the

@@ -23,8 +23,10 @@ TB_F32, TB_BF16, TB_E4M3 = 0, 1, 2
 TB_SCALE_F32, TB_SCALE_E8M0 = 0, 1
 FP8_BLOCK = 128
 FP8_MAX_IN_DIM = 1 << 22
+FP8_MAX_TOKENS = 1 << 24
 MAX_HEAD_DIM = 1024
 MAX_HEADS = 65535
+MAX_HEAD_TOKENS = 1 << 25
 MAX_GROUP = 8
 WORKSPACE_CONTROL_BYTES = MAX_GROUP * 65536
 FROBENIUS_WORKSPACE_BYTES = 65536
@@ -694,7 +696,7 @@ def head_norm_rotate(parts, positions: torch.Tensor | None, freqs: torch.Tensor 
             yt, yh, ye = y.stride()
             fine = fine and y.get_device() == dev
         else:
-            y = x.new_empty((tokens, heads, dim)) if fine else x
+            y = x if not fine else torch.empty_like(x) if x.is_contiguous() else x.new_empty((tokens, heads, dim))
             yt, yh, ye = heads * dim, dim, 1
         if (xe != 1 or ye != 1) and dim > 1:
             raise TBError(TB_ERR_UNSUPPORTED, "the elements of a head must be adjacent")

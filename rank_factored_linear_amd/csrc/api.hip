@@ -671,13 +671,15 @@ tb_status check_fp8_dims(int64_t m, int64_t out_dim, int64_t in_dim, int64_t ste
   if (m < 0 || out_dim < 1 || in_dim < 1)
     return fail(TB_ERR_INVALID_ARGUMENT, "need m >= 0, out_dim >= 1, in_dim >= 1 (got %lld, %lld, %lld)", (long long)m,
                 (long long)out_dim, (long long)in_dim);
-  if (m > kMaxDim || out_dim > kMaxDim) return fail(TB_ERR_UNSUPPORTED, "a dimension exceeds 2^30");
+  if (m > TB_FP8_MAX_TOKENS || out_dim > kMaxDim)
+    return fail(TB_ERR_UNSUPPORTED, "m exceeds %d or out_dim 2^30", TB_FP8_MAX_TOKENS);
   if (in_dim > TB_FP8_MAX_IN_DIM)
     return fail(TB_ERR_UNSUPPORTED, "in_dim %lld exceeds %d", (long long)in_dim, TB_FP8_MAX_IN_DIM);
   if (in_dim % step != 0)
     return fail(TB_ERR_UNSUPPORTED, "in_dim %lld is not a multiple of %lld", (long long)in_dim, (long long)step);
-  if (fp8_blocks(out_dim) * fp8_blocks(std::max(in_dim, m)) >= (int64_t(1) << 31) ||
-      fp8_blocks(m) * fp8_blocks(in_dim) >= (int64_t(1) << 31))
+  // One launch's workgroups of 256 threads stay below 2^32 threads.
+  if (fp8_blocks(out_dim) * fp8_blocks(in_dim) >= (int64_t(1) << 24) ||
+      2 * fp8_blocks(out_dim) * fp8_blocks(m) >= (int64_t(1) << 24))
     return fail(TB_ERR_UNSUPPORTED, "matrix too large");
   return TB_OK;
 }
@@ -792,8 +794,8 @@ tb_status tb_head_norm_rotate(int32_t n, const tb_head_part* parts, int64_t toke
     return fail(TB_ERR_INVALID_ARGUMENT, "need tokens >= 0, head_dim >= 1 and an even rot_dim in [0, head_dim] (got %lld, %lld, %lld)",
                 (long long)tokens, (long long)head_dim, (long long)rot_dim);
   if (!(eps >= 0.f)) return fail(TB_ERR_INVALID_ARGUMENT, "eps must be >= 0");
-  if (head_dim > TB_MAX_HEAD_DIM || tokens > kMaxDim)
-    return fail(TB_ERR_UNSUPPORTED, "head_dim exceeds %d or tokens 2^30", TB_MAX_HEAD_DIM);
+  if (head_dim > TB_MAX_HEAD_DIM || tokens > TB_MAX_HEAD_TOKENS)
+    return fail(TB_ERR_UNSUPPORTED, "head_dim exceeds %d or tokens %d", TB_MAX_HEAD_DIM, TB_MAX_HEAD_TOKENS);
   int64_t heads = 0;
   for (int j = 0; j < n; ++j) {
     const tb_head_part& p = parts[j];
@@ -805,8 +807,15 @@ tb_status tb_head_norm_rotate(int32_t n, const tb_head_part* parts, int64_t toke
     const int64_t strides[4] = {p.x_token_stride, p.x_head_stride, p.y_token_stride, p.y_head_stride};
     for (int64_t s : strides) {
       if (s < 0) return fail(TB_ERR_INVALID_ARGUMENT, "part %d: a stride is negative", j);
-      if (s > (int64_t(1) << 40)) return fail(TB_ERR_UNSUPPORTED, "part %d: a stride exceeds 2^40", j);
+      if (s > (int64_t(1) << 35)) return fail(TB_ERR_UNSUPPORTED, "part %d: a stride exceeds 2^35", j);
     }
+    // In place means element for element.
+    if (p.x == p.y && ((tokens > 1 && p.x_token_stride != p.y_token_stride) ||
+                       (p.heads > 1 && p.x_head_stride != p.y_head_stride)))
+      return fail(TB_ERR_INVALID_ARGUMENT, "part %d: y is x, with other strides", j);
+    for (int k = 0; k < j; ++k)
+      if (parts[k].heads > 0 && (parts[k].y == p.y || parts[k].y == p.x || parts[k].x == p.y))
+        return fail(TB_ERR_INVALID_ARGUMENT, "parts %d and %d: one writes what the other reads or writes", k, j);
     if (!rows_apart(tokens, p.heads, head_dim, p.y_token_stride, p.y_head_stride))
       return fail(TB_ERR_INVALID_ARGUMENT, "part %d: the rows of y overlap", j);
     if (!aligned_to(p.x, esize(dtype)) || !aligned_to(p.y, esize(dtype)) || !aligned_to(p.weight, esize(dtype)))

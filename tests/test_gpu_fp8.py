@@ -225,7 +225,9 @@ def test_product_of_fp32_activations(m, out, n, kind):
 
 @pytest.mark.parametrize("kind", SCALES)
 @pytest.mark.parametrize("m,out,n", [(600, 5376, 2048), (1030, 2304, 5376), (2048, 4352, 1152), (4096, 2048, 1024),
-                                     (2000, 8200, 400), (2100, 5004, 2064)])
+                                     (2000, 8200, 400), (2100, 5004, 2064),
+                                     # More tiles than compute units, the rest of them cut into slices; odd rows of y.
+                                     (2000, 8200, 2064), (2041, 8195, 2064)])
 def test_product_of_many_tokens(m, out, n, kind):
     print(m, out, n, kind, flush=True)
     x, wq, ws = operands(m, out, n, kind)

@@ -82,6 +82,17 @@ def test_head_norm_rotate_refuses(part, kw, status):
                                    0.0, a["dt"], None) == status
 
 
+def test_parts_that_write_into_each_other_are_refused():
+    call = lambda *parts: lib.tb_head_norm_rotate(len(parts), _parts(*parts), 3, 64, 64, 0, FAKE, FAKE, 1e-6,   # noqa: E731
+                                                  0.0, 1, None)
+    far = dict(x=FAKE << 1, y=FAKE << 2)
+    assert call(far, dict(x=FAKE << 3, y=FAKE << 2)) == INV      # one output for both
+    assert call(far, dict(x=FAKE << 2, y=FAKE << 3)) == INV      # the first writes what the second reads
+    assert call(far, dict(x=FAKE << 3, y=FAKE << 1)) == INV
+    assert call(dict(xt=256)) == INV                             # in place, but rows elsewhere
+    assert call(dict(xh=128, xt=256)) == INV
+
+
 def test_a_bad_second_part_is_refused():
     arr = _parts({}, dict(y=None))
     assert lib.tb_head_norm_rotate(2, arr, 3, 64, 64, 0, FAKE, FAKE, 1e-6, 0.0, 1, None) == INV
