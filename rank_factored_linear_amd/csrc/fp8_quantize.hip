@@ -63,7 +63,10 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const E* __rest
 // W0 loads are issued ahead of the product and arrive under it.  Each thread
 // keeps its 64 rebuilt values in registers between the block's maximum and
 // their rounding, so W is formed once, in fp32, and never written wide: bf16
-// bundles move 3 bytes per weight through HBM.
+// bundles move 3 bytes per weight through HBM.  This kernel serves fp32 bundles
+// and ranks that the ring kernel below does not take (4096 x 5376 at rank 64 in
+// fp32: 80 us, bound by the fp32 matrix rate) and dense weights, where there is
+// no product (8192 x 5376: 29 us in bf16, 37 us in fp32).
 constexpr int kPitch = 132;  // floats per row of the tile in LDS: 16-byte aligned, rows 4 banks apart
 
 enum Product { kNone, kMfma, kAny };
@@ -165,9 +168,16 @@ __global__ __launch_bounds__(kThreads, 2) void rebuild_blocks_kernel(const EI* _
 // ---- bf16 bundles with rank % 8 == 0, up to 256 ------------------------------
 //
 // The same block per workgroup, with U and V coming in k-tiles of 32 straight
-// into a ring of LDS slots (kRingSlots of 16 KB), kRingSlots - 1 k-tiles ahead,
-// and the product passing through LDS in two halves, so that three workgroups
-// fit a compute unit and hide each other's waits.
+// into a ring of three LDS slots of 16 KB, two k-tiles ahead, and the product
+// passing through LDS in two halves, so that three workgroups fit a compute
+// unit and hide each other's waits.
+//
+// 21504 x 5376 at rank 256: 126 us (2.8 TB/s of W0 read and e4m3 written;
+// staged through registers, two workgroups per compute unit: 154 us). The
+// 128 KB of U and V that each block draws from L2 through direct-to-LDS loads
+// bound it, not HBM (8192 x 5376 at rank 64, a quarter of them: 3.7 TB/s; rank
+// 0: 4.6 TB/s). Two persistent workgroups per compute unit that keep loading
+// across blocks were slower (153 us): three waves per SIMD count for more.
 namespace ring {
 
 constexpr int BK = 32, kRingSlots = 3;
@@ -259,13 +269,9 @@ __global__ __launch_bounds__(kThreads, 3) void rebuild_ring_kernel(const bf16_t*
 
 #pragma unroll
   for (int st = 0; st < KT; ++st) {
-    // Loads land in order: k-tile st has when at most those after it are out.
-    if constexpr (kRingSlots == 3) {
-      if (st + 1 < KT) wait_vm<4>();
-      else wait_vm<0>();
-    } else {
-      wait_vm<0>();
-    }
+    // Loads land in order: k-tile st has when at most the four of the next one are out.
+    if (st + 1 < KT) wait_vm<4>();
+    else wait_vm<0>();
     __builtin_amdgcn_s_barrier();   // published; and every wave has left the slot filled next
     if (st + kRingSlots - 1 < KT) issue((st + kRingSlots - 1) % kRingSlots, st + kRingSlots - 1);
     __builtin_amdgcn_sched_barrier(0);
