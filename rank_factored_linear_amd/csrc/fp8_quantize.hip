@@ -172,12 +172,13 @@ __global__ __launch_bounds__(kThreads, 2) void rebuild_blocks_kernel(const EI* _
 // passing through LDS in two halves, so that three workgroups fit a compute
 // unit and hide each other's waits.
 //
-// 21504 x 5376 at rank 256: 126 us (2.8 TB/s of W0 read and e4m3 written;
-// staged through registers, two workgroups per compute unit: 154 us). The
-// 128 KB of U and V that each block draws from L2 through direct-to-LDS loads
-// bound it, not HBM (8192 x 5376 at rank 64, a quarter of them: 3.7 TB/s; rank
-// 0: 4.6 TB/s). Two persistent workgroups per compute unit that keep loading
-// across blocks were slower (153 us): three waves per SIMD count for more.
+// 21504 x 5376 at rank 256: 124 us (2.8 TB/s of W0 read and e4m3 written;
+// staged through registers, two workgroups per compute unit: 154 us). HBM does
+// not bound it (8192 x 5376 at rank 64: 3.7 TB/s; rank 0: 4.6 TB/s): a block
+// takes about 9000 cycles of a compute unit, in which its products, its vector
+// work, its LDS traffic and its 176 KB through L1 take 2000 to 4000 each and
+// overlap in part. U and V through registers with three workgroups a unit took
+// 125 us, two persistent workgroups that keep loading across blocks 153.
 namespace ring {
 
 constexpr int BK = 32, kRingSlots = 3;
