@@ -63,13 +63,91 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const E* __rest
 // W0 loads are issued ahead of the product and arrive under it.  Each thread
 // keeps its 64 rebuilt values in registers between the block's maximum and
 // their rounding, so W is formed once, in fp32, and never written wide: bf16
-// bundles move 3 bytes per weight through HBM.  This kernel serves fp32 bundles
-// and ranks that the ring kernel below does not take (4096 x 5376 at rank 64 in
-// fp32: 80 us, bound by the fp32 matrix rate) and dense weights, where there is
-// no product (8192 x 5376: 29 us in bf16, 37 us in fp32).
+// bundles move 3 bytes per weight through HBM.  This kernel serves fp32 bundles,
+// ranks that the ring kernel below does not take, and dense weights, where there
+// is no product (8192 x 5376: 29 us in bf16, 37 us in fp32).
 constexpr int kPitch = 132;  // floats per row of the tile in LDS: 16-byte aligned, rows 4 banks apart
 
-enum Product { kNone, kMfma, kAny };
+// The fp32 product of a block with rank % 4 == 0: four waves of 64 x 64 in
+// v_mfma_f32_32x32x2_f32, k-tiles of 32 in two LDS buffers, the next one in
+// registers meanwhile.  A lane reads four consecutive k of a row for four
+// products, lanes 0..31 the first four of eight and lanes 32..63 the others:
+// U and V are paired alike, so only the order of the sum is another.  Rows are
+// 36 floats apart, so sixteen rows' pieces of four meet all 64 banks.
+//
+// Calls, beside four 64 x 64 products without prefetch (kAny, which other ranks
+// still take): 21504 x 5376 rank 256: 546 us (1166), 108 TFLOP/s against 138 of
+// a library product; 4096 x 5376 rank 64: 52 (79), 21469 x 432 rank 128: 44
+// (88). At rank 64 neither the matrix rate (20 us) nor HBM (22) is reached;
+// what holds it there was not measured.
+namespace f128 {
+
+constexpr int kStep = 32, kRow = 36, kOpFloats = kBlock * kRow;
+constexpr int kLdsBytes = 2 * 2 * kOpFloats * 4;   // [buffer][U, V]
+using f32x16 = rebuild::t128::f32x16;
+
+__device__ __forceinline__ void product(const float* u, const float* v, int O, int I, int R, int o0, int i0,
+                                        float* lds, f32x16 (&acc)[2][2]) {
+  const int tid = int(threadIdx.x), w = tid >> 6, l = tid & 63, h = l >> 5, lr = l & 31;
+  const int wi = w & 1, wo = w >> 1, row0 = tid >> 3, piece = (tid & 7) * 4;
+  f32x4 next[2][4];
+  auto load = [&](int k0) {
+    const int k = k0 + piece;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = row0 + 32 * j;
+      const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+      next[0][j] = o0 + row < O && k < R ? *reinterpret_cast<const f32x4*>(u + size_t(o0 + row) * R + k) : none;
+      next[1][j] = i0 + row < I && k < R ? *reinterpret_cast<const f32x4*>(v + size_t(i0 + row) * R + k) : none;
+    }
+  };
+  auto store = [&](int buf) {
+#pragma unroll
+    for (int op = 0; op < 2; ++op)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<f32x4*>(lds + (2 * buf + op) * kOpFloats + (row0 + 32 * j) * kRow + piece) = next[op][j];
+  };
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.f;
+  load(0);
+  store(0);
+  __syncthreads();
+  int buf = 0;
+  for (int k0 = 0; k0 < R; k0 += kStep, buf ^= 1) {
+    const bool more = k0 + kStep < R;
+    if (more) load(k0 + kStep);
+    const float* lu = lds + 2 * buf * kOpFloats + (wo * 64 + lr) * kRow + 4 * h;
+    const float* lv = lds + (2 * buf + 1) * kOpFloats + (wi * 64 + lr) * kRow + 4 * h;
+#pragma unroll
+    for (int kk = 0; kk < kStep; kk += 8) {
+      f32x4 fu[2], fv[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        fu[b] = *reinterpret_cast<const f32x4*>(lu + b * 32 * kRow + kk);
+        fv[b] = *reinterpret_cast<const f32x4*>(lv + b * 32 * kRow + kk);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int rb = 0; rb < 2; ++rb)
+#pragma unroll
+          for (int cb = 0; cb < 2; ++cb)
+            acc[rb][cb] = __builtin_amdgcn_mfma_f32_32x32x2f32(fv[rb][e], fu[cb][e], acc[rb][cb], 0, 0, 0);
+    }
+    // The other buffer's readers passed the barrier that ended the last step.
+    if (more) store(buf ^ 1);
+    __syncthreads();
+  }
+}
+
+}  // namespace f128
+
+enum Product { kNone, kMfma, kMfma32, kAny };
 
 template <typename EI, int SC, int PROD>
 __global__ __launch_bounds__(kThreads, 2) void rebuild_blocks_kernel(const EI* __restrict__ s,
@@ -79,7 +157,8 @@ __global__ __launch_bounds__(kThreads, 2) void rebuild_blocks_kernel(const EI* _
                                                                      uint8_t* __restrict__ q,
                                                                      scale_t<SC>* __restrict__ scale, int O, int I,
                                                                      int R, int KB) {
-  constexpr int kTile = PROD == kNone ? 16 : kBlock * kPitch * 4;
+  constexpr int kTile = PROD == kNone ? 16 : PROD == kMfma32 ? f128::kLdsBytes : kBlock * kPitch * 4;
+  static_assert(f128::kLdsBytes >= kBlock * kPitch * 4, "the tile fits the fp32 product's staging");
   static_assert(kTile == 16 || kTile >= rebuild::t128::kLdsBytes, "the product's staging fits the tile's room");
   __shared__ __attribute__((aligned(16))) unsigned char lds[kTile];
   __shared__ uint32_t wave_max[kThreads / kWave];
@@ -96,10 +175,13 @@ __global__ __launch_bounds__(kThreads, 2) void rebuild_blocks_kernel(const EI* _
   }
 
   float* tile = reinterpret_cast<float*>(lds);
-  if constexpr (PROD == kMfma) {
+  if constexpr (PROD == kMfma || PROD == kMfma32) {
     namespace t = rebuild::t128;
     t::f32x16 acc[2][2];
-    t::product(u, v, O, I, R, o0, i0, lds, acc);
+    if constexpr (PROD == kMfma32)
+      f128::product(u, v, O, I, R, o0, i0, tile, acc);
+    else
+      t::product(u, v, O, I, R, o0, i0, lds, acc);
     __syncthreads();   // every wave has read the last k-tile
     const int wi = w & 1, wo = w >> 1, h = l >> 5, lr = l & 31;
 #pragma unroll
@@ -174,11 +256,14 @@ __global__ __launch_bounds__(kThreads, 2) void rebuild_blocks_kernel(const EI* _
 //
 // 21504 x 5376 at rank 256: 124 us (2.8 TB/s of W0 read and e4m3 written;
 // staged through registers, two workgroups per compute unit: 154 us). HBM does
-// not bound it (8192 x 5376 at rank 64: 3.7 TB/s; rank 0: 4.6 TB/s): a block
-// takes about 9000 cycles of a compute unit, in which its products, its vector
-// work, its LDS traffic and its 176 KB through L1 take 2000 to 4000 each and
-// overlap in part. U and V through registers with three workgroups a unit took
-// 125 us, two persistent workgroups that keep loading across blocks 153.
+// not bound it (8192 x 5376 at rank 64: 3.7 TB/s; rank 0: 4.6 TB/s). Counters
+// at rank 256: 10300 cycles of a compute unit per block, matrix units busy 20 %
+// of them, vector instructions 26 %, LDS reads and writes of the waves 19 %
+// with no bank conflict; waves spend 45 % of their cycles in waits and 35 %
+// ready but not issued. No unit is full; which wait costs most was not
+// measured (direct-to-LDS writes and L1 are not in these counters). U and V
+// through registers with three workgroups a unit took 125 us, two persistent
+// workgroups that keep loading across blocks 153.
 namespace ring {
 
 constexpr int BK = 32, kRingSlots = 3;
@@ -385,6 +470,8 @@ hipError_t blocks_typed(const void* s, const void* w0, const void* u, const void
     if (rank % 8 == 0 && rank <= 128) return go(ring::rebuild_ring_kernel<SC, 4>);
     if (rank % 8 == 0 && rank <= 256) return go(ring::rebuild_ring_kernel<SC, 8>);
     if (rank % 8 == 0) return go(rebuild_blocks_kernel<EI, SC, kMfma>);
+  } else if (rank % 4 == 0) {
+    return go(rebuild_blocks_kernel<EI, SC, kMfma32>);
   }
   return go(rebuild_blocks_kernel<EI, SC, kAny>);
 }

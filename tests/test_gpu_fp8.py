@@ -347,3 +347,15 @@ def test_stacked_weights_equal_their_parts():
     ws = torch.cat([p[1].view(torch.uint8) for p in parts]).view(tb.E8M0)
     y = tb.dense_forward_fp8(x, wq, ws)
     assert torch.equal(y, torch.cat([tb.dense_forward_fp8(x, *p) for p in parts], 1))
+
+
+@pytest.mark.parametrize("kind", SCALES)
+@pytest.mark.parametrize("out,n,r", [
+    (1, 8, 4), (128, 128, 32), (127, 120, 28), (129, 136, 36), (257, 392, 64), (300, 1160, 68), (1024, 264, 128),
+    (130, 520, 260), (64, 136, 30), (200, 200, 3)])
+def test_rebuild_of_fp32_bundles(out, n, r, kind):
+    print(out, n, r, kind, flush=True)
+    s = 1 + 0.1 * randn((out,), 11, 1.0, F32)
+    W0, U, V = randn((out, n), 12, 0.02, F32), randn((out, r), 13, 0.02, F32), randn((n, r), 14, 0.05, F32)
+    q, sc = tb.reconstruct_weight_fp8(s, W0, U, V, SCALES[kind])
+    check_rebuild(q, sc, s, W0, U, V, kind)
