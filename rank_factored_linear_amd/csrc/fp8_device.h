@@ -134,6 +134,26 @@ __device__ __forceinline__ f32x4 mma(const Operand<true>& a, const Operand<true>
   return c;
 }
 
+// Behind a group of products.  The exact form is a chain of 16x16x32 ops into
+// one accumulator whose operands vector code has just written and will rewrite:
+// the case that mfma_operand_guard is for.  So products_issued waits behind the
+// group's last op, and the operands are kept past that: until then they have
+// registers of their own, which nothing rewrites (the compiler stays free to
+// widen one operand while others multiply).  Call products_issued, then keep
+// each operand.
+__device__ __forceinline__ void keep(const Operand<false>&) {}
+__device__ __forceinline__ void keep(const Operand<true>& o) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) asm volatile("" ::"v"(o.v[j]));
+}
+template <bool EXACT> __device__ __forceinline__ void products_issued() {
+  if constexpr (EXACT) {
+    __builtin_amdgcn_sched_barrier(0);
+    mfma_operand_guard();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
 __device__ __forceinline__ i32x8 join(u32x4 lo, u32x4 hi) {
   return i32x8{int(lo[0]), int(lo[1]), int(lo[2]), int(lo[3]), int(hi[0]), int(hi[1]), int(hi[2]), int(hi[3])};
 }

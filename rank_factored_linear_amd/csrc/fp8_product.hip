@@ -257,7 +257,34 @@ __global__ __launch_bounds__(kDecodeWaves* kWave) void fp8_decode_kernel(DecodeA
         if constexpr (XM == kXGiven) xsc = scale_value(s.xs[n]);
       }
       const Operand<kExact> xv = operand<kExact>(xb);
-      if constexpr (NT == 1) {
+      if constexpr (kExact) {
+        const float s0 = xsc * scale_value(s.ws[0]), s1 = xsc * scale_value(s.ws[1]);
+        // Two row tiles' products at a time where there are no more.
+        constexpr int kGroup = RT <= 2 ? RT : 1;
+#pragma unroll
+        for (int r = 0; r < RT; r += kGroup) {
+          Operand<kExact> wv[kGroup];
+          f32x4 p[kGroup];
+#pragma unroll
+          for (int h = 0; h < kGroup; ++h) {
+            i32x8 wb = join(s.lo[r + h], s.hi[r + h]);
+            // Widened anew for every 16 tokens: kept, they would not fit the registers.
+            if constexpr (NT > 1 && RT > 2) asm volatile("" : "+v"(wb));
+            wv[h] = operand<kExact>(wb);
+          }
+#pragma unroll
+          for (int h = 0; h < kGroup; ++h) p[h] = mma(wv[h], xv);
+          products_issued<kExact>();
+#pragma unroll
+          for (int h = 0; h < kGroup; ++h) keep(wv[h]);
+          keep(xv);
+#pragma unroll
+          for (int h = 0; h < kGroup; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[r + h][n][e] += p[h][e] * ((r + h) * 16 + (l >> 4) * 4 + e < edge ? s0 : s1);
+        }
+      } else if constexpr (NT == 1) {
         const float s0 = xsc * scale_value(s.ws[0]);
         if (!two) {
 #pragma unroll
@@ -482,14 +509,19 @@ __global__ __launch_bounds__(kGemmThreads, 2) void fp8_gemm_kernel(GemmArgs a) {
       if constexpr (SC == TB_SCALE_E8M0) sc[j] = scale_value(uint8_t(raw)) * wsc;
       else sc[j] = __uint_as_float(raw) * wsc;
     }
+    Operand<kExact> fw[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const lds_byte* r = s + (wo * 64 + i * 16 + lr) * 128;
-      const Operand<kExact> fw =
-          operand<kExact>(join(*reinterpret_cast<const lds_u32x4*>(r + p0), *reinterpret_cast<const lds_u32x4*>(r + p1)));
+      fw[i] = operand<kExact>(join(*reinterpret_cast<const lds_u32x4*>(r + p0), *reinterpret_cast<const lds_u32x4*>(r + p1)));
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] += mma(fw, fx[j]) * sc[j];
+      for (int j = 0; j < 2; ++j) acc[i][j] += mma(fw[i], fx[j]) * sc[j];
     }
+    products_issued<kExact>();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) keep(fw[i]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) keep(fx[j]);
   };
   issue(0, kb0);
   issue(1, kb0 + 1);

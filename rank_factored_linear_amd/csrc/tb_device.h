@@ -126,15 +126,18 @@ __device__ __forceinline__ f32x4 mma_k32(const Frag8<float>& a, const Frag8<floa
   return c;
 }
 
-// Wait states after a group of matrix-core ops whose A/B registers the
-// following code may rewrite at once: the write-after-read rule for
-// matrix-core source operands (a VGPR that an issued op still reads must not
-// be overwritten before the op has read it).  In a chain of 16x16x32 ops that
-// accumulate into the same registers, an ALU write to the A or B register of
-// an op right behind it gave wrong products on gfx950 (the compiler put no
-// wait states there); 24 wait states after each group removed every error.
-// 24 is empirical (the smallest count tried that did), with room for 16-pass
-// ops.
+// Wait states after a group of matrix-core ops whose A/B registers vector code
+// may rewrite at once.  In kernels whose ops were chains of 16x16x32 into one
+// accumulator, with ALU writes to an op's A or B register right behind it,
+// products came out wrong on gfx950 (the compiler put no wait states there);
+// 24 wait states after each group removed every error.  24 is empirical (the
+// smallest count tried that did).  The write alone does not bring the error
+// about: such a chain, single 16x16x32 and single 16x16x128 ops with both
+// operands overwritten 0, 1, 2, 4, 8 or 24 wait states behind the last op, in
+// workgroups of eight waves, gave 0 wrong lanes of 2.1e8 each.  So the cause is not
+// known beyond the form, and every chain of this form is guarded; ops that
+// start from zero or rotate over accumulators (16x16x128 and 32x32x16 here) have
+// never been wrong and are not.
 __device__ __forceinline__ void mfma_operand_guard() { asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: ); }
 
 // Agent-scope read-modify-write with acquire/release semantics.  On gfx950

@@ -1,0 +1,99 @@
+"""Every kernel of the 8-bit product, whole results bit for bit.
+
+x and w are small whole numbers times powers of two (one per token, one per weight block), chosen so that every step is
+exact: the e4m3 values, products of a group of eight columns within 2^4 of one another, and sums below 2^24 units in
+the last place of fp32.  So y has one right value: the sum, rounded once.  A product that is missing, doubled or read
+from the wrong row, block or scale changes it.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_fp8 import check_product, held, operands, randn
+
+pytestmark = pytest.mark.gpu
+
+tb = pytest.importorskip("rank_factored_linear_amd.binding")
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+SCALES = {"f32": F32, "e8m0": tb.E8M0}
+
+
+def units():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def spread(scale, rows, m, n):
+    return scale.float().repeat_interleave(rows, 0)[:m].repeat_interleave(128, 1)[:, :n]
+
+
+def whole(m, out, n, kind, seed=1):
+    """(x wide, xq, xs, wq, ws, exact sum in fp32)."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    kb, ob = -(-n // 128), -(-out // 128)
+
+    def ints(*shape):
+        return torch.randint(-2, 3, shape, generator=g, device=DEV).float()
+
+    def powers(*shape):
+        return torch.exp2(torch.randint(-1, 3, shape, generator=g, device=DEV).float())
+
+    x, w, xs, ws = ints(m, n), ints(out, n), powers(m, kb), powers(ob, kb)
+    want = (x * spread(xs, 1, m, n)) @ (w * spread(ws, 128, out, n)).t()
+    assert float(want.abs().max()) < 2 ** 22
+    dt = SCALES[kind]
+    return x * spread(xs, 1, m, n), x.to(tb.E4M3), xs.to(dt), w.to(tb.E4M3), ws.to(dt), want
+
+
+def same(y, want):
+    want = want.to(y.dtype)
+    if not torch.equal(y, want):
+        bad = (y != want) | y.isnan()
+        at = bad.nonzero()
+        raise AssertionError(f"{int(bad.sum())} of {y.numel()} wrong, first at {at[0].tolist()}, last at {at[-1].tolist()}")
+
+
+def check_all(m, out, n, kind):
+    """y from x in e4m3 and in bf16 and fp32, both result types, between rows that stay as they were."""
+    x, xq, xs, wq, ws, want = whole(m, out, n, kind)
+    for yt in (BF, F32):
+        room = torch.full((m + 4, out), 5.0, dtype=yt, device=DEV)
+        same(tb.dense_forward_fp8(xq, wq, ws, x_scale=xs, out=room[2:2 + m]), want)
+        assert (room[:2] == 5).all() and (room[2 + m:] == 5).all()
+        if kind == "e8m0":   # powers of two: quantising x within the call is exact as well
+            for xt in (BF, F32):
+                y = tb.dense_forward_fp8(x.to(xt), wq, ws, out_dtype=yt)
+                same(y, want)
+                assert torch.equal(y, tb.dense_forward_fp8(x.to(xt), wq, ws, out_dtype=yt))
+
+
+# Up to 64 tokens: 1, 2, 3, 4 and 6 tiles of 16 rows a workgroup on 256 compute units, one block of columns up to more
+# than the eight waves take at once, each with its ragged last block.
+@pytest.mark.parametrize("kind", SCALES)
+@pytest.mark.parametrize("out", [130, 1000, 6001, 12000, 14000, 16001, 21504, 30003])
+@pytest.mark.parametrize("m,n", [(1, 16), (1, 2064), (5, 400), (16, 1168), (17, 144), (32, 1168), (33, 272), (64, 1168)])
+def test_few_tokens(m, n, out, kind):
+    print(m, out, n, kind, flush=True)
+    check_all(m, out, n, kind)
+
+
+@pytest.mark.parametrize("kind", SCALES)
+@pytest.mark.parametrize("m,out,n", [(65, 1, 16), (65, 129, 144), (200, 1003, 2064), (777, 1152, 1168), (1030, 1300, 272),
+                                     (100, 5000, 6928)])
+def test_middling_tokens(m, out, n, kind):
+    print(m, out, n, kind, flush=True)
+    check_all(m, out, n, kind)
+
+
+# Exact sums say nothing of how real data is rounded in these variants.
+@pytest.mark.parametrize("kind", SCALES)
+@pytest.mark.parametrize("out", [1000, 6001, 12000, 14000, 16001, 21504])
+@pytest.mark.parametrize("m,dtype", [(3, BF), (16, BF), (11, F32)])
+def test_fp32_results_of_few_tokens(m, out, dtype, kind):
+    print(m, out, dtype, kind, flush=True)
+    x, wq, ws = operands(m, out, 1168, kind, dtype=dtype)
+    xq, xs = tb.quantize_activations(x, SCALES[kind])
+    y = tb.dense_forward_fp8(x, wq, ws, out_dtype=F32)
+    check_product(y, xq, xs, wq, ws)
+    assert torch.equal(y, tb.dense_forward_fp8(xq, wq, ws, x_scale=xs, out_dtype=F32))
