@@ -312,8 +312,13 @@ __global__ __launch_bounds__(kDecodeWaves* kWave) void fp8_decode_kernel(DecodeA
   for (int d = 0; d < kDepth; ++d)
     if (d < nkb) fetch(st[d], d);
   // The first weight blocks are on their way while x is quantised.
-  if constexpr (XM == kXInLds)
+  if constexpr (XM == kXInLds) {
     quantise_run<SC, XE>(a, w, nkb, xlds + lds0 * kBlock, xslds + lds0);
+    // Lanes read what others of their wave wrote: its LDS operations complete in order, once the compiler keeps it.
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
   // Rounds without a branch: a branch around a refill would make the compiler
   // wait for the refill itself before it uses the next stage.
   int i = 0;

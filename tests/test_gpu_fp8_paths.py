@@ -97,3 +97,15 @@ def test_fp32_results_of_few_tokens(m, out, dtype, kind):
     y = tb.dense_forward_fp8(x, wq, ws, out_dtype=F32)
     check_product(y, xq, xs, wq, ws)
     assert torch.equal(y, tb.dense_forward_fp8(xq, wq, ws, x_scale=xs, out_dtype=F32))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kind", SCALES)
+@pytest.mark.parametrize("m", [1, 2, 3, 7, 8, 15, 16])
+def test_x_quantised_into_lds_by_its_wave(m, kind, dtype):
+    """Small weights: lanes quantise for others of their wave.  The same numbers as from x quantised beforehand."""
+    x, wq, ws = operands(m, 1000, 2000, kind, dtype=dtype)   # two blocks a wave, the last one ragged
+    xq, xs = tb.quantize_activations(x, SCALES[kind])
+    for yt in (BF, F32):
+        want = tb.dense_forward_fp8(xq, wq, ws, x_scale=xs, out_dtype=yt)
+        assert torch.equal(tb.dense_forward_fp8(x, wq, ws, out_dtype=yt), want)
