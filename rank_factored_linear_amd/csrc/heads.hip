@@ -203,18 +203,22 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs a) {
         fa[k][e] *= r * wa[k][e];
         fb[k][e] *= r * wb[k][e];
       }
+      // Elements that are not rotated are left alone: turned by nothing, they
+      // would still take on an infinity or NaN of their neighbour.
+      const int p0 = (lane + k * a.G) * V;   // the unit's first pair
       if constexpr (INTER && V > 1) {
         // The unit's 2V elements are V pairs: the first V/2 in chunk a, the rest in chunk b.
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
           const float x0 = fa[k][e], x1 = fa[k][e + 1], c0 = cs[k][e / 2], s0 = sn[k][e / 2];
-          fa[k][e] = x0 * c0 - x1 * s0;
-          fa[k][e + 1] = x1 * c0 + x0 * s0;
+          const bool ta = p0 + e / 2 < a.half, tb = p0 + V / 2 + e / 2 < a.half;
+          fa[k][e] = ta ? x0 * c0 - x1 * s0 : x0;
+          fa[k][e + 1] = ta ? x1 * c0 + x0 * s0 : x1;
           const float z0 = fb[k][e], z1 = fb[k][e + 1], c1 = cs[k][V / 2 + e / 2], s1 = sn[k][V / 2 + e / 2];
-          fb[k][e] = z0 * c1 - z1 * s1;
-          fb[k][e + 1] = z1 * c1 + z0 * s1;
+          fb[k][e] = tb ? z0 * c1 - z1 * s1 : z0;
+          fb[k][e + 1] = tb ? z1 * c1 + z0 * s1 : z1;
         }
-      } else {
+      } else if (p0 < a.half) {   // V divides half: a unit is rotated as a whole
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float x0 = fa[k][e], x1 = fb[k][e];
