@@ -743,7 +743,7 @@ def qkv_forward(x: torch.Tensor, q, k, v, head_dim: int, positions: torch.Tensor
     else:
         xq, xs = quantize_activations(x, q[1].dtype)
         ys = [dense_forward_fp8(xq, *p, x_scale=xs, out_dtype=x.dtype) for p in (q, k, v)]
-    yq, yk, yv = (y.view(y.shape[0], -1, head_dim) for y in ys)
+    yq, yk, yv = (y.view(y.shape[0], y.shape[1] // head_dim, head_dim) for y in ys)
     head_norm_rotate([(yq, q_weight), (yk, k_weight)], positions, freqs, eps, weight_offset, interleaved, [yq, yk])
     return yq, yk, yv
 
