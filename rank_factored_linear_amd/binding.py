@@ -730,17 +730,42 @@ def qkv_forward(x: torch.Tensor, q, k, v, head_dim: int, positions: torch.Tensor
     if kinds not in ({4}, {2}):
         raise TBError(TB_ERR_INVALID_ARGUMENT, "q, k and v are all (s, W0, U, V) or all (Wq, w_scale)")
     at = 1 if kinds == {4} else 0
+    if x.dim() != 2:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [m, in]")
     for name, p in zip("qkv", (q, k, v)):
         if head_dim < 1 or p[at].dim() != 2 or p[at].shape[0] % head_dim:
             raise TBError(TB_ERR_INVALID_ARGUMENT, f"{name}: {list(p[at].shape)} is not rows of heads of {head_dim}")
+    # What the later calls would refuse is refused before the first one is made.
+    if head_dim > MAX_HEAD_DIM:
+        raise TBError(TB_ERR_UNSUPPORTED, f"head_dim {head_dim} exceeds {MAX_HEAD_DIM}")
+    if (q[at].shape[0] + k[at].shape[0]) // head_dim > MAX_HEADS:
+        raise TBError(TB_ERR_UNSUPPORTED, f"more than {MAX_HEADS} heads of queries and keys")
+    if not eps >= 0:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "eps must be >= 0")
     _rotated_dims(_kind(positions), _kind(freqs), x.shape[0], head_dim)
     for w in (q_weight, k_weight):
         if w is not None:
             _expect("head weight", w, (head_dim,), x.dtype)
+    if kinds == {2}:
+        _dtype_code(x.dtype)
+        m, in_dim = x.shape
+        sizes = []
+        for name, (Wq, scale) in zip("qkv", (q, k, v)):
+            if scale.dtype != q[1].dtype:
+                raise TBError(TB_ERR_INVALID_ARGUMENT, f"{name}: scales are {scale.dtype}, those of q {q[1].dtype}")
+            xs = (m, _fp8_blocks(in_dim)), scale.dtype
+            sizes.append(_dense_fp8_dims((x.shape, E4M3), _kind(Wq), _kind(scale), xs, None, x.dtype)[:6])
+        if in_dim % 16:
+            raise TBError(TB_ERR_UNSUPPORTED, f"in_dim {in_dim} is not a multiple of 16")
     _need_cuda(positions, freqs, q_weight, k_weight)
     if kinds == {4}:
         ys = linear_forward_group([(x, *p) for p in (q, k, v)])
     else:
+        dev = _here([x, *q, *k, *v])
+        for name, (Wq, _), size in zip("qkv", (q, k, v), sizes):
+            if Wq.data_ptr() % 16:
+                raise TBError(TB_ERR_UNSUPPORTED, f"{name}: Wq must be 16-byte aligned")
+            _fp8_workspace_size(dev, *size)   # (raises where a size is too large)
         xq, xs = quantize_activations(x, q[1].dtype)
         ys = [dense_forward_fp8(xq, *p, x_scale=xs, out_dtype=x.dtype) for p in (q, k, v)]
     yq, yk, yv = (y.view(y.shape[0], y.shape[1] // head_dim, head_dim) for y in ys)
