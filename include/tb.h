@@ -509,7 +509,9 @@ typedef struct tb_head_part {
  *   0 <= rot_dim <= head_dim, even; positions [tokens] int64 and freqs [r]
  *   double, device (may be NULL where rot_dim is 0); eps >= 0.  Heads add up
  *   to TB_MAX_HEADS at most; a part may have none.  Strides are >= 0 and the
- *   rows of a y must not overlap one another.  16-byte aligned parts with
+ *   rows of a y must not overlap one another.  Overlaps between a y and other
+ *   tensors are refused where the two step alike over tokens and heads, or
+ *   start at the same row; elsewhere keeping them apart is up to the caller.  16-byte aligned parts with
  *   strides, head_dim and (unless interleaved) r in multiples of 16 bytes are
  *   read and written in 16-byte pieces; everything else works, more slowly.
  *   x must be small enough for its squares to sum up in fp32.

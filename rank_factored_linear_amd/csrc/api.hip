@@ -692,6 +692,43 @@ bool rows_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t ts, int64_t 
   return (hs >= dim && ts >= (heads - 1) * hs + dim) || (ts >= dim && hs >= (tokens - 1) * ts + dim);
 }
 
+// A tensor of heads in bytes: rows at base + t * ts + h * hs.
+struct HeadRows {
+  int64_t base, heads, ts, hs;
+};
+
+HeadRows head_rows(const void* p, int64_t heads, int64_t ts, int64_t hs, tb_dtype dtype) {
+  const int64_t es = int64_t(esize(dtype));
+  return HeadRows{int64_t(reinterpret_cast<uintptr_t>(p)), heads, ts * es, hs * es};
+}
+
+// Whether rows of `row` bytes of two tensors of heads share memory.  Exact where
+// both step alike over tokens and heads (views of one packed tensor, whose
+// extents interleave); else only tensors whose first rows meet are told from
+// ones that interleave without meeting.
+bool rows_meet(const HeadRows& a, const HeadRows& b, int64_t tokens, int64_t row) {
+  const int64_t delta = a.base - b.base;
+  if (delta < row && -delta < row) return true;
+  const int64_t ea = (tokens - 1) * a.ts + (a.heads - 1) * a.hs + row, eb = (tokens - 1) * b.ts + (b.heads - 1) * b.hs + row;
+  if (delta >= eb || -delta >= ea) return false;
+  if ((tokens > 1 && a.ts != b.ts) || (a.heads > 1 && b.heads > 1 && a.hs != b.hs)) return false;
+  const int64_t ts = tokens > 1 ? a.ts : 0, hs = a.heads > 1 ? a.hs : b.hs;
+  for (int64_t e = 1 - b.heads; e < a.heads; ++e) {
+    // Rows d tokens and e heads apart lie v + d * ts bytes apart.
+    const int64_t v = delta + e * hs;
+    if (ts == 0) {
+      if (v < row && -v < row) return true;
+      continue;
+    }
+    // The d that bring them within a row of each other: -v - row < d * ts < row - v.
+    const int64_t low = -v - row;
+    const int64_t d = (low >= 0 ? low / ts : -((-low + ts - 1) / ts)) + 1;   // the least one past low
+    const int64_t least = std::max(d, 1 - tokens);
+    if (least < tokens && least * ts < row - v) return true;
+  }
+  return false;
+}
+
 }  // namespace
 }  // namespace tb
 
@@ -809,17 +846,27 @@ tb_status tb_head_norm_rotate(int32_t n, const tb_head_part* parts, int64_t toke
       if (s < 0) return fail(TB_ERR_INVALID_ARGUMENT, "part %d: a stride is negative", j);
       if (s > (int64_t(1) << 35)) return fail(TB_ERR_UNSUPPORTED, "part %d: a stride exceeds 2^35", j);
     }
+    if (!aligned_to(p.x, esize(dtype)) || !aligned_to(p.y, esize(dtype)) || !aligned_to(p.weight, esize(dtype)))
+      return fail(TB_ERR_UNSUPPORTED, "part %d: pointers must be aligned to their element size", j);
     // In place means element for element.
     if (p.x == p.y && ((tokens > 1 && p.x_token_stride != p.y_token_stride) ||
                        (p.heads > 1 && p.x_head_stride != p.y_head_stride)))
       return fail(TB_ERR_INVALID_ARGUMENT, "part %d: y is x, with other strides", j);
-    for (int k = 0; k < j; ++k)
-      if (parts[k].heads > 0 && (parts[k].y == p.y || parts[k].y == p.x || parts[k].x == p.y))
+    const HeadRows x = head_rows(p.x, p.heads, p.x_token_stride, p.x_head_stride, dtype);
+    const HeadRows y = head_rows(p.y, p.heads, p.y_token_stride, p.y_head_stride, dtype);
+    const int64_t row = head_dim * int64_t(esize(dtype));
+    if (p.x != p.y && rows_meet(x, y, tokens, row))
+      return fail(TB_ERR_INVALID_ARGUMENT, "part %d: y overlaps x without being x", j);
+    for (int k = 0; k < j; ++k) {
+      const tb_head_part& o = parts[k];
+      if (o.heads == 0) continue;
+      const HeadRows ox = head_rows(o.x, o.heads, o.x_token_stride, o.x_head_stride, dtype);
+      const HeadRows oy = head_rows(o.y, o.heads, o.y_token_stride, o.y_head_stride, dtype);
+      if (rows_meet(oy, y, tokens, row) || rows_meet(oy, x, tokens, row) || rows_meet(ox, y, tokens, row))
         return fail(TB_ERR_INVALID_ARGUMENT, "parts %d and %d: one writes what the other reads or writes", k, j);
+    }
     if (!rows_apart(tokens, p.heads, head_dim, p.y_token_stride, p.y_head_stride))
       return fail(TB_ERR_INVALID_ARGUMENT, "part %d: the rows of y overlap", j);
-    if (!aligned_to(p.x, esize(dtype)) || !aligned_to(p.y, esize(dtype)) || !aligned_to(p.weight, esize(dtype)))
-      return fail(TB_ERR_UNSUPPORTED, "part %d: pointers must be aligned to their element size", j);
   }
   if (tokens == 0 || heads == 0) return ok();
   if (rot_dim > 0 && (!positions || !freqs))
