@@ -463,9 +463,10 @@ tb_status tb_reconstruct_weight_fp8(const void *s, const void *w0, const void *u
  *   y  [m, out_dim] in y_dtype (TB_BF16 or TB_F32), must not alias inputs.
  *   Weights that share an input can be stacked along out_dim into one call
  *   where every one but the last has a multiple of 128 rows.
- *   0 <= m <= TB_FP8_MAX_TOKENS (0: nothing is enqueued), out_dim >= 1,
- *   in_dim % 16 == 0 and <= TB_FP8_MAX_IN_DIM; x, wq 16-byte aligned.  The product xs * ws of two
- *   scales must be finite in fp32.
+ *   0 <= m <= TB_FP8_MAX_TOKENS (0: nothing is enqueued), out_dim >= 1 and
+ *   within one launch (8.0e8 up to 16 tokens, 5.3e8 up to 32, 4.0e8 up to 64),
+ *   in_dim % 16 == 0 and <= TB_FP8_MAX_IN_DIM; x, wq 16-byte aligned.  The
+ *   product xs * ws of two scales must be finite in fp32.
  *   workspace: at least tb_dense_forward_fp8_workspace_size() bytes, 256-byte
  *   aligned, no initial contents (NULL when 0).  Calls that may run at the same
  *   time must not share it.  The size does not grow with m everywhere: query each m.

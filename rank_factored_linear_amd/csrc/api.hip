@@ -781,6 +781,7 @@ tb_status tb_dense_forward_fp8_workspace_size(int64_t m, int64_t out_dim, int64_
   if (!valid_scale(scale_type)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown scale type %d", int(scale_type));
   tb_status st = check_fp8_dims(m, out_dim, in_dim, 16);
   if (st != TB_OK) return st;
+  if (!fp8_decode_fits(m, out_dim)) return fail(TB_ERR_UNSUPPORTED, "out_dim %lld is too large", (long long)out_dim);
   *bytes_out = 0;
   if (m == 0) return ok();
   int cus = 0;
@@ -798,6 +799,7 @@ tb_status tb_dense_forward_fp8(const void* x, const void* x_scale, const void* w
   if (!valid_scale(scale_type)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown scale type %d", int(scale_type));
   tb_status st = check_fp8_dims(m, out_dim, in_dim, 16);
   if (st != TB_OK) return st;
+  if (!fp8_decode_fits(m, out_dim)) return fail(TB_ERR_UNSUPPORTED, "out_dim %lld is too large", (long long)out_dim);
   if (quantised ? (m > 0 && !x_scale) : x_scale != nullptr)
     return fail(TB_ERR_INVALID_ARGUMENT, "x_scale goes with an x in e4m3, and only with one");
   if (m == 0) return ok();

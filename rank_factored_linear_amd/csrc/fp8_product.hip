@@ -53,6 +53,7 @@ __device__ __forceinline__ void store_out4(YE* y, const f32x4& v, int n, bool wi
 // which every workgroup repeats (64 x 21504 x 5376: 47 us).
 // ---------------------------------------------------------------------------
 constexpr int kDecodeWaves = 8;
+static_assert(kDecodeWaves * kWave == kFp8DecodeThreads, "what the launch's size is checked against");
 constexpr int kDecodeLdsX = 32768;   // bytes of Q(x) a workgroup keeps in LDS
 constexpr int kDepth = 2;            // blocks of each wave in flight (3 and 4 gained nothing and cost occupancy)
 
@@ -619,7 +620,7 @@ hipError_t decode_quantising(const DecodeArgs& a, hipStream_t stream) {
 // unit takes at most ~22 GB/s from HBM here), in as few workgroups per unit as
 // the widest kernel for these tokens allows.
 int decode_rows(int64_t m, int64_t out_dim, int cus) {
-  const int most = m <= 16 ? 96 : m <= 32 ? 64 : 48;
+  const int most = fp8_decode_most_rows(m);
   const int64_t k = (out_dim + int64_t(cus) * most - 1) / (int64_t(cus) * most);
   const int64_t rows = (out_dim + cus * k - 1) / (cus * k);
   return int(m <= 16 ? rows : (rows + 3) / 4 * 4);

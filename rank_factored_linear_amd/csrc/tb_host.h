@@ -212,6 +212,18 @@ hipError_t launch_fp8_tiles(const Fp8TilePlan& p, tb_scale scale_type, const voi
                             const void* w, const void* ws, void* y, float* part, int64_t m, int64_t out_dim, int64_t in_dim,
                             hipStream_t stream);
 
+// The few-token kernel: threads of a workgroup, and the most output rows it takes
+// (what its accumulators hold at this many tokens).
+constexpr int kFp8DecodeThreads = 512;
+constexpr int fp8_decode_most_rows(int64_t m) { return m <= 16 ? 96 : m <= 32 ? 64 : 48; }
+// Whether a launch, which holds fewer than 2^32 threads, reaches every row.  Shares
+// are evened out over the compute units (no more than 1024 of them), which costs
+// less than one workgroup each.
+constexpr bool fp8_decode_fits(int64_t m, int64_t out_dim) {
+  return m > kDecodeMaxTokens ||
+         (out_dim / fp8_decode_most_rows(m) + 1024) * kFp8DecodeThreads < (int64_t(1) << 32);
+}
+
 struct Fp8Plan {
   int decode;              // 1: the few-token kernel (m <= kDecodeMaxTokens)
   int fused;               // x is quantised inside it

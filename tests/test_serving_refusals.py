@@ -116,3 +116,26 @@ def test_overlap_is_exact_where_strides_agree():
                                              tokens, dim)
                 assert status == INV
                 assert message.startswith("positions") == a.isdisjoint(b), (ts, hs, shift, ha, hb, message)
+
+
+@pytest.mark.parametrize("m,fits,over", [
+    (1, 800_000_000, 806_000_000), (16, 800_000_000, 806_000_000), (17, 530_000_000, 537_000_000),
+    (32, 530_000_000, 537_000_000), (33, 400_000_000, 403_000_000), (64, 400_000_000, 403_000_000)])
+def test_rows_past_one_launch_are_refused(m, fits, over):
+    """A launch of the few-token kernel (512 threads for 96, 64 or 48 rows) holds fewer than 2^32 threads."""
+    size = ctypes.c_size_t(0)
+
+    def query(out):
+        return lib.tb_dense_forward_fp8_workspace_size(m, out, 16, tb.TB_BF16, tb.TB_BF16, tb.TB_SCALE_F32,
+                                                       ctypes.byref(size))
+
+    assert query(over) == UNS
+    assert query(fits) != UNS           # (without a GPU the query ends at the device)
+    assert lib.tb_dense_forward_fp8(FAKE, None, FAKE, FAKE, FAKE, m, over, 16, tb.TB_BF16, tb.TB_BF16, tb.TB_SCALE_F32,
+                                    None, 0, None) == UNS
+    # The share of a workgroup on 256 compute units, as the kernel takes it.
+    most = 96 if m <= 16 else 64 if m <= 32 else 48
+    k = -(-fits // (256 * most))
+    rows = -(-fits // (256 * k))
+    rows = rows if m <= 16 else (rows + 3) // 4 * 4
+    assert -(-fits // rows) * 512 < 1 << 32
