@@ -109,3 +109,30 @@ def test_x_quantised_into_lds_by_its_wave(m, kind, dtype):
     for yt in (BF, F32):
         want = tb.dense_forward_fp8(xq, wq, ws, x_scale=xs, out_dtype=yt)
         assert torch.equal(tb.dense_forward_fp8(x, wq, ws, out_dtype=yt), want)
+
+
+@pytest.mark.parametrize("kind", SCALES)
+@pytest.mark.parametrize("m,out", [(1, 130), (16, 12001), (33, 700), (64, 6912), (300, 520), (2041, 4099)])
+def test_outliers_that_cancel(m, out, kind):
+    """One product of +-448^2 in each group of eight columns, signs alternating, beside seven of 30.  fp32 y is the sum;
+    bf16 y is off by at most 7 x 2^-13 of the terms' magnitudes, which here is most of the sum itself."""
+    n = 1152
+    x, w = torch.ones(m, n, device=DEV), torch.full((out, n), 30.0, device=DEV)
+    x[:, 0::16], x[:, 8::16], w[:, 0::8] = 448, -448, 448
+    ones = lambda *shape: torch.ones(*shape, device=DEV).to(SCALES[kind])   # noqa: E731
+    args = x.to(tb.E4M3), w.to(tb.E4M3), ones(-(-out // 128), 9), ones(m, 9)
+    want, size = 30.0 * 7 * 144, 144 * (448.0 ** 2 + 7 * 30)
+    assert (tb.dense_forward_fp8(*args, out_dtype=F32) == want).all()
+    off = (tb.dense_forward_fp8(*args).float() - want).abs().max().item()
+    assert off <= 7 * 2.0 ** -13 * size * (1 + 2.0 ** -8) + 2.0 ** -8 * want
+    print("bf16 off by", off, flush=True)
+
+
+@pytest.mark.parametrize("m,out", [(5, 1000), (50, 1000), (300, 1000)])
+def test_outlier_channels(m, out):
+    """Activations with eight channels a hundred times as large as the others."""
+    x, wq, ws = operands(m, out, 1152, "f32")
+    x[:, 7::144] *= 100
+    xq, xs = tb.quantize_activations(x)
+    check_product(tb.dense_forward_fp8(x, wq, ws), xq, xs, wq, ws)
+    check_product(tb.dense_forward_fp8(x, wq, ws, out_dtype=F32), xq, xs, wq, ws)
