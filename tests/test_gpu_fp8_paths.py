@@ -136,3 +136,98 @@ def test_outlier_channels(m, out):
     xq, xs = tb.quantize_activations(x)
     check_product(tb.dense_forward_fp8(x, wq, ws), xq, xs, wq, ws)
     check_product(tb.dense_forward_fp8(x, wq, ws, out_dtype=F32), xq, xs, wq, ws)
+
+
+# ---- the 256 x 256 tiles: bf16 results with tiles for half the compute units ----------------------------------------
+
+
+def tiles(m, out):
+    return -(-m // 256) * -(-out // 256)
+
+
+def cut_tiles(m, out, n):
+    """(tiles cut into slices, slices of each), by the rule at plan_fp8_tiles."""
+    rest, kb = tiles(m, out) % units(), -(-n // 128)
+    s = min(units() // rest, kb // 4, 8) if rest else 1
+    return (rest, s) if s > 1 and kb - kb // s > 12 else (0, 1)
+
+
+def takes_tiles(m, out):
+    return m > 64 and 2 * tiles(m, out) >= units()
+
+
+MANY = [  # 136 tiles on 256 units; one, two, three blocks of columns and more, ragged ones; out even, odd, not wide
+    (2041, 4099, 16), (2048, 4352, 128), (2041, 4104, 144), (1800, 4099, 272), (2041, 4100, 400), (2000, 4347, 1168),
+    (2041, 4099, 2064),                    # (odd numbers of blocks)
+    # 264 and 300 tiles: a second round, whole and cut into slices.
+    (2041, 8387, 144), (2041, 8387, 2064), (2555, 7424, 2048), (2100, 8400, 2560), (4097, 4999, 1040), (2041, 8387, 4112),
+    (2040, 4090, 3600)]                    # 128 tiles, all of them cut in two
+
+
+@pytest.mark.parametrize("kind", SCALES)
+@pytest.mark.parametrize("m,out,n", MANY)
+def test_many_tokens(m, out, n, kind):
+    print(m, out, n, kind, flush=True)
+    assert takes_tiles(m, out)
+    check_all(m, out, n, kind)
+
+
+def test_the_sizes_above_reach_whole_and_cut_tiles():
+    cuts = [cut_tiles(m, out, n) for m, out, n in MANY]
+    assert units() == 256 and {s for _, s in cuts} >= {1, 2, 4, 8}
+    assert {tiles(m, out) > 256 for (m, out, _), c in zip(MANY, cuts) if c[1] == 1} == {True, False}
+
+
+@pytest.mark.parametrize("kind", SCALES)
+@pytest.mark.parametrize("m,out,n", [(2041, 4099, 400), (2041, 8387, 2064)])
+def test_tiles_of_real_data(m, out, n, kind):
+    """x in e4m3 (scales token by token) and quantised in the call (block by block): the same bits, twice, from a
+    workspace full of NaN patterns; a token that is not finite stays alone."""
+    assert takes_tiles(m, out)
+    x, wq, ws = operands(m, out, n, kind)
+    xq, xs = tb.quantize_activations(x, SCALES[kind])
+    y = tb.dense_forward_fp8(x, wq, ws)
+    rows = torch.tensor(sorted({0, 1, 63, 64, 255, 256, 1111, m - 2, m - 1}), device=DEV)
+    check_product(y[rows], xq[rows], xs[rows], wq, ws)
+    assert torch.equal(y, tb.dense_forward_fp8(x, wq, ws))
+    for xdt, args in ((BF, (x, wq, ws)), (tb.E4M3, (xq, wq, ws, xs))):
+        need = tb.dense_forward_fp8_workspace_size(m, out, n, xdt, BF, SCALES[kind])
+        dirty = torch.full((max(need, 256),), 0xFF, dtype=torch.uint8, device=DEV)
+        assert torch.equal(y, tb.dense_forward_fp8(*args, workspace=dirty))
+    x[1111, n - 1] = float("nan")
+    x[300, 5] = float("inf")
+    y2 = tb.dense_forward_fp8(x, wq, ws)
+    assert y2[[300, 1111]].isnan().all()
+    keep = torch.ones(m, dtype=torch.bool, device=DEV)
+    keep[[300, 1111]] = False
+    assert torch.equal(y2[keep], y[keep])
+    w = randn((out, n), 2, 0.02)           # the weight that operands() made
+    w[out - 5, n - 3] = float("inf")
+    y3 = tb.dense_forward_fp8(xq, *tb.quantize_weight(w, SCALES[kind]), x_scale=xs)
+    block = (out - 5) // 128 * 128
+    assert y3[:, block:block + 128].isnan().all() and torch.equal(y3[:, :block], y[:, :block])
+    assert torch.equal(y3[:, block + 128:], y[:, block + 128:])
+
+
+def test_tiles_captured_and_on_another_stream():
+    m, out, n = 2041, 8387, 2064
+    x, wq, ws = operands(m, out, n, "f32")
+    want = tb.dense_forward_fp8(x, wq, ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = tb.dense_forward_fp8(x, wq, ws)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(other, want)
+    graphs = []
+    for _ in range(2):
+        xin, y, g = x.clone(), torch.empty_like(want), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            tb.dense_forward_fp8(xin, wq, ws, out=y)
+        graphs.append((g, xin, y))
+    for step in range(3):
+        for j, (g, xin, _) in enumerate(graphs):
+            xin.copy_(randn(x.shape, 100 + 2 * step + j))
+            g.replay()
+        for g, xin, y in graphs:
+            assert torch.equal(y, tb.dense_forward_fp8(xin, wq, ws))
