@@ -31,6 +31,49 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
+// Loads through buffer descriptors.  The range check covers the sum of the lane
+// offset and the scalar offset, for loads to registers and for loads to LDS
+// (probed on gfx950, inside one allocation, up to scalar offsets far past the
+// descriptor): what lies past num_records reads as zeros.  So rows past a tile's
+// end may be named by either offset, and kPast names nothing at all.
+constexpr unsigned kRsrcFlags = 0x00020000u;  // descriptor word 3: 32-bit data format
+constexpr int kPast = int(0x80000000u);       // lane offset past every buffer
+
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+typedef __attribute__((address_space(3))) uint32_t lds_u32;
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// One direct-to-LDS load of a wave: 16 bytes per lane, 1 KB at dst.  M0 takes one
+// wait state before a load reads it.  Written as assembly so that the compiler
+// does not drain it before each LDS read; wait_loads is the wait.
+__device__ __forceinline__ void dma(unsigned dst, __amdgpu_buffer_rsrc_t r, int v, int soff) {
+  asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
+               [v] "v"(v), [r] "s"(r), [s] "s"(soff)
+               : "memory", "m0");
+}
+// One scale per lane, four bytes apart in LDS (a byte is widened).
+template <int SC>
+__device__ __forceinline__ void dma_scale(unsigned dst, __amdgpu_buffer_rsrc_t r, int v, int soff) {
+  if constexpr (SC == TB_SCALE_E8M0)
+    asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_ubyte %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
+                 [v] "v"(v), [r] "s"(r), [s] "s"(soff)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_dword %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
+                 [v] "v"(v), [r] "s"(r), [s] "s"(soff)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// At most N of this wave's loads are still out, and its LDS reads are done.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
 // Scale storage by scale type.
 template <int SC> struct ScaleOf;
 template <> struct ScaleOf<TB_SCALE_F32> { typedef float type; };

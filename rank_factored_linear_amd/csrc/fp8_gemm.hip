@@ -35,18 +35,12 @@ constexpr int kOpBytes = BT * kBlock;         // one operand's block in LDS
 constexpr int kBOffset = 2 * kOpBytes;        // ring [W0][W1][x0][x1]
 constexpr int kRingBytes = 4 * kOpBytes;
 constexpr int kScaleBytes = 2 * kWaves * 256; // each wave's 64 activation scales of two blocks
-constexpr unsigned kRsrcFlags = 0x00020000u;  // buffer descriptor word 3: 32-bit data format
-constexpr int kPast = int(0x80000000u);       // lane offset past every buffer: the load returns zeros
 // Finished tiles leave through LDS, 16 tokens x 64 outputs of bf16 at a time
 // per wave, rows 144 bytes apart, beside the ring.
 constexpr int kStagePitch = 144, kStageBytes = 16 * kStagePitch;
 static_assert(kRingBytes + kScaleBytes + kWaves * kStageBytes <= 160 * 1024, "ring, scales and staging fit the LDS");
+static_assert(int64_t(BT) * TB_FP8_MAX_IN_DIM < (int64_t(1) << 31), "a tile's rows are addressed with 31-bit offsets");
 constexpr int kPieces = 32;                   // pieces of four results per lane and tile
-
-typedef __attribute__((address_space(3))) uint8_t lds_byte;
-typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
-typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
-typedef __attribute__((address_space(3))) uint32_t lds_u32;
 
 struct Args {
   const uint8_t* x;
@@ -127,38 +121,6 @@ __device__ __forceinline__ Lanes make_lanes(uint8_t* ring, uint8_t* scales) {
   }
   ln.s_rd = opaque((lds_byte*)scales + w * 256 + lr * 4);
   return ln;
-}
-
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-// One direct-to-LDS load of a wave: eight rows of 128 bytes, 1 KB at dst.  M0
-// takes one wait state before a load reads it.  Written as assembly so that the
-// compiler does not drain it before each LDS read; wait_loads is the wait.
-__device__ __forceinline__ void dma(unsigned dst, __amdgpu_buffer_rsrc_t r, int v, int soff) {
-  asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
-               [v] "v"(v), [r] "s"(r), [s] "s"(soff)
-               : "memory", "m0");
-}
-// One scale per lane, four bytes apart in LDS (a byte is widened).
-template <int SC>
-__device__ __forceinline__ void dma_scale(unsigned dst, __amdgpu_buffer_rsrc_t r, int v, int soff) {
-  if constexpr (SC == TB_SCALE_E8M0)
-    asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_ubyte %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
-                 [v] "v"(v), [r] "s"(r), [s] "s"(soff)
-                 : "memory", "m0");
-  else
-    asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_dword %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
-                 [v] "v"(v), [r] "s"(r), [s] "s"(soff)
-                 : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-
-// At most N of this wave's loads are still out, and its LDS reads are done.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ const uint8_t* uniform_ptr(const uint8_t* p) {

@@ -69,9 +69,6 @@ struct DecodeArgs {
   int xs_t, xs_k;   // strides of xs (ScaleStrides)
 };
 
-constexpr unsigned kRsrcFlags = 0x00020000u;  // buffer descriptor word 3: 32-bit data format
-constexpr int kPast = int(0x80000000u);       // offset past every buffer: the load returns zeros
-
 // Loads go through buffer descriptors: rows, pieces and blocks past the end are
 // given an offset past the buffer and read as zeros, without a branch that
 // would keep the compiler from having many loads in flight.
@@ -413,39 +410,6 @@ __device__ __forceinline__ void tile_at(const GemmArgs& a, int u, int& m0, int& 
   n0 = r / gs * kTile;
 }
 
-typedef __attribute__((address_space(3))) uint8_t lds_byte;
-typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
-typedef __attribute__((address_space(3))) uint32_t lds_u32;
-
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-// One direct-to-LDS load: 16 bytes per lane, 1 KB at dst.  M0 takes one wait
-// state before a load reads it.
-__device__ __forceinline__ void dma16(unsigned dst, __amdgpu_buffer_rsrc_t r, int v, int soff) {
-  asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
-               [v] "v"(v), [r] "s"(r), [s] "s"(soff)
-               : "memory", "m0");
-}
-// A scale per lane, four bytes apart in LDS (a byte is widened).
-template <int SC>
-__device__ __forceinline__ void dma_scale(unsigned dst, __amdgpu_buffer_rsrc_t r, int v, int soff) {
-  if constexpr (SC == TB_SCALE_E8M0)
-    asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_ubyte %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
-                 [v] "v"(v), [r] "s"(r), [s] "s"(soff)
-                 : "memory", "m0");
-  else
-    asm volatile("s_mov_b32 m0, %[d]\n\ts_nop 0\n\tbuffer_load_dword %[v], %[r], %[s] offen lds" ::[d] "s"(dst),
-                 [v] "v"(v), [r] "s"(r), [s] "s"(soff)
-                 : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-// At most N of this wave's loads are still out, and its LDS reads are done.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-}
-
 template <int SC, typename YE>
 __global__ __launch_bounds__(kGemmThreads, 2) void fp8_gemm_kernel(GemmArgs a) {
   constexpr bool kExact = sizeof(YE) == 4;
@@ -484,10 +448,10 @@ __global__ __launch_bounds__(kGemmThreads, 2) void fp8_gemm_kernel(GemmArgs a) {
 #pragma unroll
     for (int j = 0; j < kW; ++j) {
       const int row8 = w * kW + j;
-      dma16(d + row8 * 1024, rw, (row8 & 1) ? vo : ve, k + row8 * 8 * a.I);
+      dma(d + row8 * 1024, rw, (row8 & 1) ? vo : ve, k + row8 * 8 * a.I);
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) dma16(d + kX + (w * 2 + j) * 1024, rx, j ? vo : ve, k + (w * 2 + j) * 8 * a.I);
+    for (int j = 0; j < 2; ++j) dma(d + kX + (w * 2 + j) * 1024, rx, j ? vo : ve, k + (w * 2 + j) * 8 * a.I);
     dma_scale<SC>(d + kScales + w * 256, rows_rsrc(xs + min(kb, kb1 - 1) * a.xs_k, xs_bytes), xs_off, 0);
   };
 
@@ -673,10 +637,9 @@ Fp8Plan plan_fp8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, tb_
     p.off_xs = at;
     at = align_up(at + size_t(m) * KB * (scale_type == TB_SCALE_E8M0 ? 1 : 4), 256);
   }
-  // The 256 x 256 kernel makes bf16 results, needs tiles for half the compute
-  // units and addresses a tile's rows with 31-bit offsets.
-  p.big = !p.decode && y_dtype == TB_BF16 && in_dim <= (int64_t(1) << 31) / 256 - 128 &&
-          ((m + 255) / 256) * ((out_dim + 255) / 256) * 2 >= cus;
+  // The 256 x 256 kernel makes bf16 results and needs tiles for half the compute
+  // units.
+  p.big = !p.decode && y_dtype == TB_BF16 && ((m + 255) / 256) * ((out_dim + 255) / 256) * 2 >= cus;
   if (p.big) {
     p.tile = plan_fp8_tiles(m, out_dim, in_dim, cus);
     p.off_part = at;

@@ -270,12 +270,8 @@ constexpr int BK = 32, kRingSlots = 3;
 constexpr int kOpBytes = kBlock * BK * 2;      // one operand's k-tile: 128 rows of 64 bytes
 constexpr int kSlotBytes = 2 * kOpBytes;
 constexpr int kLds = kRingSlots * kSlotBytes;
-constexpr unsigned kRsrcFlags = 0x00020000u;   // buffer descriptor word 3: 32-bit data format
-constexpr int kPast = int(0x80000000u);        // lane offset past every buffer: zeros
 static_assert(kLds >= 64 * kPitch * 4, "half a tile of fp32 fits the ring's room");
 
-typedef __attribute__((address_space(3))) uint8_t lds_byte;
-typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 typedef rebuild::t128::f32x16 f32x16;
 
@@ -293,11 +289,6 @@ __device__ __forceinline__ void dma2(unsigned dst, __amdgpu_buffer_rsrc_t r, int
       : "memory", "m0");
 }
 #pragma clang diagnostic pop
-
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");   // and this wave's LDS reads are done
-}
 
 // KT: k-tiles of the rank (those past it load zeros).
 template <int SC, int KT>
@@ -356,8 +347,8 @@ __global__ __launch_bounds__(kThreads, 3) void rebuild_ring_kernel(const bf16_t*
 #pragma unroll
   for (int st = 0; st < KT; ++st) {
     // Loads land in order: k-tile st has when at most the four of the next one are out.
-    if (st + 1 < KT) wait_vm<4>();
-    else wait_vm<0>();
+    if (st + 1 < KT) wait_loads<4>();
+    else wait_loads<0>();
     __builtin_amdgcn_s_barrier();   // published; and every wave has left the slot filled next
     if (st + kRingSlots - 1 < KT) issue((st + kRingSlots - 1) % kRingSlots, st + kRingSlots - 1);
     __builtin_amdgcn_sched_barrier(0);

@@ -215,9 +215,9 @@ __device__ __forceinline__ Tile tile_at(int t, int tiles_i, const bf16_t* s, con
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 // Two direct-to-LDS loads: load j writes 1 KB at dst + j KB (lane l at
-// +16 l) from lane offset v[j] + soff.  The buffer's range check covers the
-// lane offset only, so every lane offset carries its row and chunk (or lies
-// past the buffer: the lane then writes zeros).  M0 takes one wait state
+// +16 l) from lane offset v[j] + soff.  A lane past the buffer writes zeros
+// (the range check covers the sum of both offsets; here every lane offset
+// carries its row and chunk, or lies past the buffer by itself).  M0 takes one wait state
 // before a load that reads it.
 __device__ __forceinline__ void dma2(unsigned dst, __amdgpu_buffer_rsrc_t r, const int (&v)[2], int soff) {
   asm volatile(
