@@ -424,7 +424,8 @@ tb_status tb_refine_shared_block(const void *const *weights, const float *const 
  * e4m3 rounds to nearest, ties to even.  A block that holds an infinity or NaN
  * gets a NaN scale and NaN entries.
  *   0 <= m <= TB_FP8_MAX_TOKENS (0: nothing is enqueued), in_dim >= 8, % 8 == 0
- *   and <= TB_FP8_MAX_IN_DIM.  x and q 16-byte aligned, scale element aligned.
+ *   and <= TB_FP8_MAX_IN_DIM.  x and q 16-byte aligned, scale element aligned; q
+ *   and scale must not alias x.
  *   Errors: TB_ERR_INVALID_ARGUMENT, TB_ERR_UNSUPPORTED, TB_ERR_HIP.
  */
 tb_status tb_quantize_activations(const void *x, void *q, void *scale, int64_t m, int64_t in_dim, tb_dtype dtype,
@@ -437,7 +438,8 @@ tb_status tb_quantize_activations(const void *x, void *q, void *scale, int64_t m
  *   scale [ceil(out_dim / 128), ceil(in_dim / 128)]       scale_type
  * one scale per 128 x 128 block, by the rules of tb_quantize_activations.
  * A dense weight is quantised with s = NULL (unit scale) and rank = 0.
- *   s, w0, u, v in dtype; in_dim % 8 == 0; w0, u, v and q 16-byte aligned.
+ *   s, w0, u, v in dtype; in_dim % 8 == 0; w0, u, v and q 16-byte aligned; q and
+ *   scale must not alias inputs.
  *   Errors as above.
  */
 tb_status tb_reconstruct_weight_fp8(const void *s, const void *w0, const void *u, const void *v, void *q, void *scale,
@@ -455,11 +457,10 @@ tb_status tb_reconstruct_weight_fp8(const void *s, const void *w0, const void *u
  * each eight columns (8j .. 8j + 7) towards zero at 2^-13 of the largest
  * 2^(a + b) among them, a and b the exponents of a product's factors, before
  * the fp32 sum: y is off by at most 7 * 2^-13 of the sum of its terms'
- * magnitudes.  For normally distributed
- * values that comes to about 2^-16 of the result, below the rounding of y.
- * Where a few large terms cancel (channels of outliers) it is no bound on the
- * result: take y in TB_F32 there, which cuts nothing.  Results are
- * deterministic run to run.
+ * magnitudes.  For normally distributed values that comes to about 2^-16 of the
+ * result, below the rounding of y.  Where a few large terms cancel (channels of
+ * outliers) it is no bound on the result: take y in TB_F32 there, which cuts
+ * nothing.  Results are deterministic run to run.
  *   x  [m, in_dim]  in x_dtype.  TB_BF16 or TB_F32: x_scale is NULL and x is
  *      quantised within the call as tb_quantize_activations does (scales of
  *      scale_type).  TB_E4M3: x_scale [m, ceil(in_dim / 128)] are its scales;
@@ -520,7 +521,8 @@ typedef struct tb_head_part {
  *   start at the same row; elsewhere keeping them apart is up to the caller.  16-byte aligned parts with
  *   strides, head_dim and (unless interleaved) r in multiples of 16 bytes are
  *   read and written in 16-byte pieces; everything else works, more slowly.
- *   x must be small enough for its squares to sum up in fp32.
+ *   x must be small enough for its squares to sum up in fp32 (and, where eps is
+ *   0, large enough for the sum not to vanish).
  *   Errors: TB_ERR_INVALID_ARGUMENT, TB_ERR_UNSUPPORTED, TB_ERR_HIP.
  */
 tb_status tb_head_norm_rotate(int32_t n, const tb_head_part *parts, int64_t tokens, int64_t head_dim, int64_t rot_dim,

@@ -611,7 +611,9 @@ def dense_forward_fp8(x: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, 
     """y = Q(x) @ Wq.T with the block scales applied, via tb_dense_forward_fp8.
 
     x [m, in] in bfloat16 or float32 is quantised within the call (scales of w_scale's dtype); in float8_e4m3fn it
-    comes with x_scale (quantize_activations).  y has out's dtype, out_dtype, x's dtype, or bfloat16 for an e4m3 x."""
+    comes with x_scale (quantize_activations).  y has out's dtype, out_dtype, x's dtype, or bfloat16 for an e4m3 x.
+    In bfloat16 y is off by up to 7 x 2^-13 of its terms' magnitudes beside its rounding (much, where outliers cancel);
+    float32 sums without that, at half the matrix rate."""
     m, out_dim, in_dim, x_code, y_code, sc, y_dtype = _dense_fp8_dims(_kind(x), _kind(Wq), _kind(w_scale),
                                                                       _kind(x_scale), _kind(out), out_dtype)
     dev = _here([t for t in (x, Wq, w_scale, x_scale, out, workspace) if t is not None])

@@ -13,8 +13,11 @@
 // and block (four for each product of 32 cycles); each product's results are
 // added while the next one runs.
 //
-// 4096 x 5376 x 8192, powers of two: products 165 us of a call of 192;
-// 4096 x 21504 x 5376, fp32 scales: call 438 us, 2.16 PFLOP/s.
+// 4096 x 5376 x 8192, powers of two: 161 us of a call of 194; 4096 x 21504 x
+// 5376, fp32 scales: 420 us (2.26 PFLOP/s) of a call of 444 (2.13), calls 438 to
+// 472 from one card to another.  Both under the power limit: in a burst after
+// idling the second takes 430 us at first, 470 from the fourth call to about the
+// fifteenth, and settles at 420.
 //
 // Workgroups are persistent, one per compute unit, and take whole tiles in
 // rounds.  What is left over for a last, partly filled round is cut into

@@ -47,10 +47,12 @@ __device__ __forceinline__ void store_out4(YE* y, const f32x4& v, int n, bool wi
 // lane's 32 bytes of a block are two 16-byte pieces 64 apart, so that one load
 // of a wave covers 64 contiguous bytes of each of 16 rows.
 //
-// Bound by HBM for large weights (4 x 21504 x 5376: 24.7 us, 4.7 TB/s, 92% of
-// a large copy's rate; 1 x 5376 x 21504: 28.3 us, 4.1 TB/s), by latency for
-// small ones (1 x 1536 x 1152: 4.0 us), and from 33 tokens on by the reads of x,
-// which every workgroup repeats (64 x 21504 x 5376: 47 us).
+// Bound by HBM for large weights (4 x 21504 x 5376: 24.2 us, 4.8 TB/s, 94% of
+// a large copy's rate; 1 x 5376 x 21504: 27 to 28 us, 4.1 to 4.3 TB/s) and by
+// latency for small ones (1 x 1536 x 1152: 4.0 us).  From 33 tokens on it is
+// neither (64 x 21504 x 5376: 43.7 us); which of the reads of x, which every
+// workgroup repeats, the second round of workgroups and their start and end
+// bounds it was not measured.
 // ---------------------------------------------------------------------------
 constexpr int kDecodeWaves = 8;
 static_assert(kDecodeWaves * kWave == kFp8DecodeThreads, "what the launch's size is checked against");
@@ -381,10 +383,13 @@ __global__ __launch_bounds__(kDecodeWaves* kWave) void fp8_decode_kernel(DecodeA
 // not depend on timing.
 //
 // Bound by the rate at which blocks reach LDS from the memory-side cache (24 KB
-// per block and tile) and, for fp32 results, by the bf16 matrix rate: 777 x
-// 1152 x 6912 takes 21.3 us in fp32 (four slices, and 4.4 us to join them) and
-// 16.7 us in bf16; 2000 x 8192 x 5376 in fp32 216 us (0.81 PFLOP/s). 128 tokens
-// per workgroup (eight waves) were no faster: 22.3, 16.4 and 232 us.
+// per block and tile) and, for fp32 results, by the bf16 matrix rate and the
+// widening beside it: 777 x 1152 x 6912 takes 23.3 us in fp32 (four slices, and
+// 4.4 us to join them) and 15.6 us in bf16; 2000 x 8192 x 5376 in fp32 220 us in
+// a long burst and up to 250 in a short one (0.80 PFLOP/s).  fp32 results keep a
+// step's operands to its end (fp8_device.h, keep), which costs 8 to 15 %.  128
+// tokens per workgroup (eight waves) were no faster when that was not so: 22.3,
+// 16.4 and 232 us against 21.3, 16.7 and 216.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128, TM = 64, kSlots = 3;   // outputs and tokens of a tile; LDS slots
 constexpr int kGemmThreads = 4 * TM;
@@ -595,7 +600,7 @@ int decode_rows(int64_t m, int64_t out_dim, int cus) {
 // against 25.0 and a launch of about 3), and else where Q(x) fits its LDS
 // (1 x 5376 x 21504: 28.3 us against 28.0 and a launch).  Where neither holds
 // the work per workgroup is mostly that quantisation (8 x 1152 x 6912 in fp32:
-// 13.1 us against 7.3 and a launch).
+// 13.1 us against 7.3 and a launch of 3.1).
 bool decode_fused(int64_t m, int64_t out_dim, int64_t in_dim, int cus) {
   return m <= kFp8FusedTokens &&
          (decode_rows(m, out_dim, cus) > 32 || m * fp8_blocks(in_dim) * kBlock <= kDecodeLdsX);

@@ -60,7 +60,8 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const E* __rest
 // One workgroup makes one block: the product U V^T on the matrix cores, then
 // through LDS (fp32) so that sixteen lanes cover a row of 128: W0 is read in
 // 16- or 32-byte pieces per lane and the e4m3 bytes leave 128 to a row.  The
-// W0 loads are issued ahead of the product and arrive under it.  Each thread
+// W0 loads are issued ahead of the product's; loads retire in order, so its first
+// step waits for them as well.  Each thread
 // keeps its 64 rebuilt values in registers between the block's maximum and
 // their rounding, so W is formed once, in fp32, and never written wide: bf16
 // bundles move 3 bytes per weight through HBM.  This kernel serves fp32 bundles,
@@ -254,16 +255,17 @@ __global__ __launch_bounds__(kThreads, 2) void rebuild_blocks_kernel(const EI* _
 // passing through LDS in two halves, so that three workgroups fit a compute
 // unit and hide each other's waits.
 //
-// 21504 x 5376 at rank 256: 124 us (2.8 TB/s of W0 read and e4m3 written;
-// staged through registers, two workgroups per compute unit: 154 us). HBM does
-// not bound it (8192 x 5376 at rank 64: 3.7 TB/s; rank 0: 4.6 TB/s). Counters
-// at rank 256: 10300 cycles of a compute unit per block, matrix units busy 20 %
-// of them, vector instructions 26 %, LDS reads and writes of the waves 19 %
-// with no bank conflict; waves spend 45 % of their cycles in waits and 35 %
-// ready but not issued. No unit is full; which wait costs most was not
-// measured (direct-to-LDS writes and L1 are not in these counters). U and V
-// through registers with three workgroups a unit took 125 us, two persistent
-// workgroups that keep loading across blocks 153.
+// 21504 x 5376 at rank 256: 120 to 135 us by card and clock (2.6 to 2.9 TB/s of
+// W0 read and e4m3 written; staged through registers, two workgroups per compute
+// unit: 154 us). HBM does not bound it (8192 x 5376 at rank 64: 3.7 TB/s; rank 0:
+// 4.5 TB/s). Counters at rank 256: 10300 cycles of a compute unit per block,
+// matrix units busy 20 % of them, vector instructions 26 %, LDS reads and writes
+// of the waves 19 % with no bank conflict; waves spend 45 % of their cycles in
+// waits and 35 % ready but not issued. No unit is full; which wait costs most was
+// not measured (direct-to-LDS writes and L1 are not in these counters). One of
+// them is for W0: a wave's loads retire in order, so the first k-tile's wait is
+// for W0 too. U and V through registers with three workgroups a unit took 125 us,
+// two persistent workgroups that keep loading across blocks 153.
 namespace ring {
 
 constexpr int BK = 32, kRingSlots = 3;
@@ -323,7 +325,9 @@ __global__ __launch_bounds__(kThreads, 3) void rebuild_ring_kernel(const bf16_t*
     dma2(dst + slot * kSlotBytes + kOpBytes, rv, ok ? a0 : kPast, ok ? a1 : kPast, kt * BK * 2);
   };
 
-  // W0 first: it arrives under the product.
+  // W0 first.  Loads retire in order, so the first step's wait below is for W0 as
+  // well: it hides behind the other workgroups of the compute unit, not behind
+  // this one's product.
   Frag8<bf16_t> f[8];
 #pragma unroll
   for (int p = 0; p < 8; ++p) {

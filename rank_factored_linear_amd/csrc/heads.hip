@@ -260,7 +260,10 @@ hipError_t heads_typed(HeadArgs& a, bool interleaved, hipStream_t stream) {
 }
 
 // Whether every part can be taken in chunks of V elements: sizes, strides and
-// addresses are multiples of one.
+// addresses are multiples of one.  What is not walks in pairs or single elements,
+// whose loads and stores are then what counts: 4096 tokens of 32 + 8 heads of 250,
+// 63 pairs rotated, one element at a time: 83 us (2.0 TB/s), against 35 for heads
+// of 256 in chunks of 16 bytes.
 template <typename E>
 bool chunks_fit(const HeadArgs& a, bool interleaved, int V) {
   if (a.D % V != 0 || (!interleaved && a.half % V != 0)) return false;
