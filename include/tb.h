@@ -56,7 +56,8 @@ typedef enum tb_status {
 typedef enum tb_dtype {
   TB_F32 = 0,  /* IEEE binary32 */
   TB_BF16 = 1, /* bfloat16, round-to-nearest-even on every store */
-  TB_E4M3 = 2  /* 8-bit: 4 exponent bits, 3 mantissa bits, largest 448, no infinities; only where a call says so */
+  TB_E4M3 = 2, /* 8-bit: 4 exponent bits, 3 mantissa bits, largest 448, no infinities; only where a call says so */
+  TB_INT8 = 3  /* 8-bit whole numbers -127 .. 127; only where a call says so */
 } tb_dtype;
 
 /* How the scales of 8-bit blocks are stored (see tb_quantize_activations). */
@@ -76,6 +77,11 @@ typedef enum tb_scale {
 #define TB_MAX_HEAD_DIM 1024
 #define TB_MAX_HEADS 65535
 #define TB_MAX_HEAD_TOKENS (1 << 25)
+
+/* Largest in_dim of the 8-bit integer calls, longest row of tb_residual_norm, most axes of a rotation. */
+#define TB_INT8_MAX_IN_DIM 65536
+#define TB_MAX_NORM_DIM 32768
+#define TB_MAX_AXES 4
 
 /* Most projections one tb_linear_forward_group call takes. */
 #define TB_MAX_GROUP 8
@@ -485,6 +491,106 @@ tb_status tb_dense_forward_fp8(const void *x, const void *x_scale, const void *w
                                tb_scale scale_type, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * 8-bit integers with one scale per row, for activations (a scale per token) and
+ * weights (a scale per output channel).
+ *
+ * tb_quantize_rows_int8 -- x [m, in_dim] (dtype, device) to
+ *   q     [m, in_dim]  whole numbers, TB_INT8
+ *   scale [m]          fp32
+ * With a the row's largest magnitude and a' = max(a, 2^-100):
+ *   scale = a' * (1 / 127),  q = round(x * (127 * (1 / a'))),
+ * each operation rounded to fp32, ties to even.  A row that holds an infinity or
+ * NaN gets a NaN scale and zeros.
+ *   0 <= m <= TB_FP8_MAX_TOKENS (0: nothing is enqueued), in_dim >= 8, % 8 == 0
+ *   and <= TB_INT8_MAX_IN_DIM.  x 16-byte, q 8-byte, scale element aligned; q and
+ *   scale must not alias x.
+ *   Errors: TB_ERR_INVALID_ARGUMENT, TB_ERR_UNSUPPORTED, TB_ERR_HIP.
+ */
+tb_status tb_quantize_rows_int8(const void *x, void *q, float *scale, int64_t m, int64_t in_dim, tb_dtype dtype,
+                                void *stream);
+
+/*
+ * tb_dense_forward_int8 -- tb_dense_forward for a weight in 8-bit integers:
+ *
+ *     y[t, o] = (sum_i xq[t, i] wq[o, i]) * (xs[t] * ws[o])
+ *
+ * The sum is a whole number, held in 32 bits and exact, whatever y's type; it is
+ * turned to fp32, scaled and rounded to y (fp32 operations, one rounding each).
+ * So a result does not depend on how the call splits its work: a token's row is
+ * the same bits in a batch and alone.
+ *   x  [m, in_dim]  in x_dtype.  TB_BF16 or TB_F32: x_scale is NULL and x is
+ *      quantised within the call as tb_quantize_rows_int8 does.  TB_INT8: x_scale
+ *      [m] are its scales; projections that share an input quantise it once.
+ *   wq [out_dim, in_dim] TB_INT8, w_scale [out_dim] fp32
+ *   y  [m, out_dim] in y_dtype (TB_BF16 or TB_F32), must not alias inputs.
+ *   Weights that share an input can be stacked along out_dim into one call.
+ *   0 <= m <= TB_FP8_MAX_TOKENS (0: nothing is enqueued), out_dim >= 1, in_dim %
+ *   16 == 0 and <= TB_INT8_MAX_IN_DIM; x, wq 16-byte aligned; the matrix must fit
+ *   one launch as in tb_dense_forward_fp8.  q of -128 is allowed for.  The product
+ *   xs * ws of two scales must be finite in fp32.
+ *   workspace: at least tb_dense_forward_int8_workspace_size() bytes, 256-byte
+ *   aligned, no initial contents (NULL when 0).  Calls that may run at the same
+ *   time must not share it.  The size does not grow with m everywhere: query each m.
+ *   Errors: TB_ERR_INVALID_ARGUMENT, TB_ERR_UNSUPPORTED, TB_ERR_HIP.
+ */
+tb_status tb_dense_forward_int8_workspace_size(int64_t m, int64_t out_dim, int64_t in_dim, tb_dtype x_dtype,
+                                               tb_dtype y_dtype, size_t *bytes_out);
+tb_status tb_dense_forward_int8(const void *x, const float *x_scale, const void *wq, const float *w_scale, void *y,
+                                int64_t m, int64_t out_dim, int64_t in_dim, tb_dtype x_dtype, tb_dtype y_dtype,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The tensors of tb_residual_norm: rows of n adjacent elements, row t of h at
+ * h + t * h_stride (strides in elements).
+ */
+typedef struct tb_residual {
+  const void *h;           /* [m, n] the residual stream (h_dtype) */
+  const void *y;           /* [m, n] the block's output (dtype), or NULL: no block, h' = h */
+  const void *post_weight; /* [n] (dtype) or NULL: none (and no offset) */
+  const void *gate;        /* (dtype) row t takes row t / gate_rows; NULL: none */
+  const void *weight;      /* [n] (dtype) or NULL: none (and no offset) */
+  void *h_out;             /* [m, n] (h_dtype); NULL iff y is */
+  void *z;                 /* [m, n] (z_dtype), or NULL: h' alone is wanted */
+  void *z_scale;           /* the scales of an 8-bit z, else NULL */
+  int64_t h_stride, y_stride, h_out_stride;
+  int64_t z_stride;        /* of a z in dtype; an 8-bit z is dense */
+  int64_t gate_rows;       /* consecutive rows that share a row of the gate, >= 1 */
+  int64_t gate_stride;     /* between rows of the gate */
+  int64_t gate_channels;   /* 1: a row of the gate holds n elements; 0: one, for the whole row */
+} tb_residual;
+
+/*
+ * tb_residual_norm -- the norms before and after a block with its gate and
+ * residual scale, in one pass: for each row
+ *
+ *     a  = y, or with post_norm y / sqrt(mean(y^2) + eps) * (post_weight + weight_offset)
+ *     h' = residual_scale * h + gate * a
+ *     z  = h' / sqrt(mean(h'^2) + eps) * (weight + weight_offset)
+ *
+ * h' is written to h_out, z to z in the type that the next projection takes.
+ * Sums and products in fp32; h' and z are rounded once each, z from the h' that
+ * is not yet rounded.
+ *   z_dtype: dtype; TB_INT8 (z_scale [m] fp32, by the rules of
+ *   tb_quantize_rows_int8); or TB_E4M3 (z_scale [m, ceil(n / 128)] scale_type, by
+ *   the rules of tb_quantize_activations).
+ *   0 <= m <= TB_FP8_MAX_TOKENS (0: nothing is enqueued), 1 <= n <=
+ *   TB_MAX_NORM_DIM; an 8-bit z needs n % 8 == 0, rows (the gate's too where it has
+ *   channels) and weights 16-byte aligned.  A wide z takes any n and element
+ *   alignment; rows, weights and strides in multiples of 16 bytes are read and
+ *   written in pieces of eight elements, everything else element by element, more
+ *   slowly.  Strides of tensors with several rows are 0 .. 2^35, those of outputs
+ *   >= n.  h_out may be h, and a z in dtype may be y (same strides); other
+ *   overlaps of an output with another tensor are refused, but for rows that
+ *   interleave at one stride.  Without y there is no gate, post_norm or residual
+ *   scale (1).  eps >= 0; rows must be small enough for their squares to sum up in
+ *   fp32 (and, where eps is 0, large enough for the sum not to vanish).
+ *   Errors: TB_ERR_INVALID_ARGUMENT, TB_ERR_UNSUPPORTED, TB_ERR_HIP.
+ */
+tb_status tb_residual_norm(const tb_residual *tensors, int64_t m, int64_t n, float residual_scale, float eps,
+                           float weight_offset, int32_t post_norm, tb_dtype dtype, tb_dtype h_dtype, tb_dtype z_dtype,
+                           tb_scale scale_type, void *stream);
+
+/*
  * One tensor of heads in tb_head_norm_rotate: element (token t, head h, d) of
  * x is at x + t * x_token_stride + h * x_head_stride + d (strides in
  * elements), so queries and keys may be views of one packed projection output,
@@ -528,6 +634,30 @@ typedef struct tb_head_part {
 tb_status tb_head_norm_rotate(int32_t n, const tb_head_part *parts, int64_t tokens, int64_t head_dim, int64_t rot_dim,
                               int32_t interleaved, const int64_t *positions, const double *freqs, float eps,
                               float weight_offset, tb_dtype dtype, void *stream);
+
+/* Where pair p of a rotation of r = rot_dim / 2 pairs lies. */
+typedef enum tb_pairs {
+  TB_PAIRS_HALF = 0,        /* (p, p + r) */
+  TB_PAIRS_INTERLEAVED = 1, /* (2p, 2p + 1) */
+  TB_PAIRS_AXIS = 2         /* in its axis's own span: with s pairs of the axes before and c of its own, (s + p, s + p + c) */
+} tb_pairs;
+
+/*
+ * tb_head_norm_rotate_axes -- tb_head_norm_rotate for tokens with a position on
+ * each of several axes (time, height, width): the angle of pair p is
+ * positions[pair_axis[p]][t] * freqs[p].  With one axis and norm it is
+ * tb_head_norm_rotate, bit for bit.
+ *   positions [axes][tokens] int64, device; 1 <= axes <= TB_MAX_AXES.
+ *   pair_axis: HOST array of rot_dim / 2 axes, each below `axes`; with
+ *   TB_PAIRS_AXIS each axis's pairs are consecutive.  rot_dim >= 2.
+ *   norm: 0: z = x, and no part has a weight (eps and weight_offset are not used).
+ *   TB_PAIRS_AXIS takes 16-byte pieces where every axis's pairs come in multiples of them.
+ *   Everything else, errors too, as tb_head_norm_rotate.
+ */
+tb_status tb_head_norm_rotate_axes(int32_t n, const tb_head_part *parts, int64_t tokens, int64_t head_dim,
+                                   int64_t rot_dim, tb_pairs pairs, int32_t axes, const int64_t *positions,
+                                   const uint8_t *pair_axis, const double *freqs, int32_t norm, float eps,
+                                   float weight_offset, tb_dtype dtype, void *stream);
 
 /*
  * tb_debug_set_wait_polls -- bound, in polls about 0.1 us apart, of the

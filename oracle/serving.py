@@ -89,3 +89,70 @@ def head_norm_rotate(x, weight, positions, freqs, eps, offset=0.0, interleaved=F
                 y[i], y[j] = z[i] * c - z[j] * s, z[j] * c + z[i] * s
             out[t, h] = y
     return out
+
+
+def quantize_rows_int8(a: np.ndarray):
+    """(whole numbers [m, n], scales [m]) of a [m, n] float64 matrix of fp32 values: scale = largest * (1 / 127) and
+    value * (127 * (1 / largest)), each operation rounded to fp32."""
+    f32 = np.float32
+    q, scales = np.zeros(a.shape), np.empty(a.shape[0])
+    with np.errstate(all="ignore"):
+        for t, row in enumerate(a):
+            if not np.isfinite(row).all():
+                scales[t] = np.nan
+                continue
+            top = f32(max(np.abs(row).max(), 2.0 ** -100))
+            scales[t] = f32(top * f32(f32(1) / f32(127)))
+            by = f32(f32(127) * f32(f32(1) / top))
+            q[t] = np.rint((row.astype(f32) * by).astype(np.float64))
+    return q, scales
+
+
+def row_product(xq, xs, wq, ws) -> np.ndarray:
+    """y = (xq wq^T) * (xs ws) of whole numbers and row scales: the sum exact (in 64-bit integers), then three fp32
+    operations, as fp32 values."""
+    acc = xq.astype(np.int64) @ wq.astype(np.int64).T
+    with np.errstate(all="ignore"):
+        return acc.astype(np.float32) * (xs.astype(np.float32)[:, None] * ws.astype(np.float32)[None, :])
+
+
+def residual_norm(h, y, weight, post_norm, post_weight, gate, scale, eps, offset):
+    """(h', z, a) in float64; gate [m, n] or None, spread over rows and channels."""
+    def normed(x, w):
+        x = x / np.sqrt(np.mean(x ** 2, axis=1, keepdims=True) + eps)
+        return x if w is None else x * (w + offset)
+
+    a = np.zeros_like(h)
+    if y is not None:
+        a = normed(y, post_weight) if post_norm else y
+        if gate is not None:
+            a = a * gate
+    out = scale * h + a
+    return out, normed(out, weight), a
+
+
+def pair_places(axes, pairs: str):
+    """[(i, j)] of each rotated pair: "half", "interleaved", or "axis" (in its axis's own span)."""
+    half, got = len(axes), []
+    for p, axis in enumerate(axes):
+        if pairs == "half":
+            got.append((p, p + half))
+        elif pairs == "interleaved":
+            got.append((2 * p, 2 * p + 1))
+        else:
+            first, count = axes.index(axis), axes.count(axis)
+            got.append((2 * first + (p - first), 2 * first + (p - first) + count))
+    return got
+
+
+def head_norm_rotate_axes(x, weight, positions, axes, freqs, eps, offset, pairs: str, norm: bool) -> np.ndarray:
+    """head_norm_rotate of tokens with positions [axes, tokens], in float64."""
+    z = x / np.sqrt(np.mean(x ** 2, axis=2, keepdims=True) + eps) if norm else x.copy()
+    if weight is not None:
+        z = z * (weight + offset)
+    y = z.copy()
+    for p, (i, j) in enumerate(pair_places(list(axes), pairs)):
+        angle = positions[axes[p]] * freqs[p]
+        c, s = np.cos(angle)[:, None], np.sin(angle)[:, None]
+        y[:, :, i], y[:, :, j] = z[:, :, i] * c - z[:, :, j] * s, z[:, :, j] * c + z[:, :, i] * s
+    return y

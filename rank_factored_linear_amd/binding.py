@@ -19,11 +19,15 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libtb.so")
 
 TB_OK, TB_ERR_INVALID_ARGUMENT, TB_ERR_UNSUPPORTED, TB_ERR_HIP = 0, 1, 2, 3
-TB_F32, TB_BF16, TB_E4M3 = 0, 1, 2
+TB_F32, TB_BF16, TB_E4M3, TB_INT8 = 0, 1, 2, 3
 TB_SCALE_F32, TB_SCALE_E8M0 = 0, 1
 FP8_BLOCK = 128
 FP8_MAX_IN_DIM = 1 << 22
 FP8_MAX_TOKENS = 1 << 24
+INT8_MAX_IN_DIM = 65536
+MAX_NORM_DIM = 32768
+MAX_AXES = 4
+TB_PAIRS_HALF, TB_PAIRS_INTERLEAVED, TB_PAIRS_AXIS = 0, 1, 2
 MAX_HEAD_DIM = 1024
 MAX_HEADS = 65535
 MAX_HEAD_TOKENS = 1 << 25
@@ -39,7 +43,8 @@ EXPORTED = (
     "tb_lowrank_factors_batch", "tb_refine_shared_block_workspace_size", "tb_refine_shared_block",
     "tb_debug_set_wait_polls", "tb_status_string", "tb_last_error", "tb_linear_forward_no_alloc",
     "tb_quantize_activations", "tb_reconstruct_weight_fp8", "tb_dense_forward_fp8_workspace_size",
-    "tb_dense_forward_fp8", "tb_head_norm_rotate",
+    "tb_dense_forward_fp8", "tb_head_norm_rotate", "tb_head_norm_rotate_axes",
+    "tb_quantize_rows_int8", "tb_dense_forward_int8_workspace_size", "tb_dense_forward_int8", "tb_residual_norm",
 )
 NO_ALLOC_SCRATCH_BYTES = 96 << 20
 DEFAULT_WAIT_POLLS = 1 << 20
@@ -59,6 +64,15 @@ class HeadPart(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("heads", ctypes.c_int64),
                 ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
                 ("y_token_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64)]
+
+
+class Residual(ctypes.Structure):
+    """tb_residual: the tensors of tb_residual_norm."""
+    _fields_ = [("h", ctypes.c_void_p), ("y", ctypes.c_void_p), ("post_weight", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("h_out", ctypes.c_void_p),
+                ("z", ctypes.c_void_p), ("z_scale", ctypes.c_void_p), ("h_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("h_out_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("gate_rows", ctypes.c_int64), ("gate_stride", ctypes.c_int64), ("gate_channels", ctypes.c_int64)]
 
 
 class TBError(RuntimeError):
@@ -107,6 +121,15 @@ def _load() -> ctypes.CDLL:
                                          ctypes.c_int, c_p, c_sz, c_p]
     lib.tb_head_norm_rotate.argtypes = [c_i32, c_p, c_i64, c_i64, c_i64, c_i32, c_p, c_p,
                                         ctypes.c_float, ctypes.c_float, ctypes.c_int, c_p]
+    lib.tb_head_norm_rotate_axes.argtypes = [c_i32, c_p, c_i64, c_i64, c_i64, ctypes.c_int, c_i32, c_p, c_p, c_p, c_i32,
+                                             ctypes.c_float, ctypes.c_float, ctypes.c_int, c_p]
+    lib.tb_quantize_rows_int8.argtypes = [c_p, c_p, c_p, c_i64, c_i64, ctypes.c_int, c_p]
+    lib.tb_dense_forward_int8_workspace_size.argtypes = [c_i64, c_i64, c_i64, ctypes.c_int, ctypes.c_int,
+                                                         ctypes.POINTER(c_sz)]
+    lib.tb_dense_forward_int8.argtypes = [c_p, c_p, c_p, c_p, c_p, c_i64, c_i64, c_i64, ctypes.c_int, ctypes.c_int, c_p,
+                                          c_sz, c_p]
+    lib.tb_residual_norm.argtypes = [c_p, c_i64, c_i64, ctypes.c_float, ctypes.c_float, ctypes.c_float, c_i32,
+                                     ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, c_p]
     lib.tb_status_string.argtypes = [ctypes.c_int]
     lib.tb_status_string.restype = ctypes.c_char_p
     lib.tb_last_error.argtypes = []
@@ -633,16 +656,245 @@ def dense_forward_fp8(x: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, 
 
 
 # ---------------------------------------------------------------------------
+# 8-bit integers: whole numbers with a scale per token of an activation and per
+# output channel of a weight
+# ---------------------------------------------------------------------------
+INT8 = torch.int8
+
+
+@functools.lru_cache(maxsize=4096)
+def _rows_int8_dims(x, q, scale):
+    """(m, in_dim, dtype code) of quantize_rows_int8's operands by kind."""
+    if len(x[0]) != 2:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [m, in]")
+    code = _dtype_code(x[1])
+    m, in_dim = x[0]
+    if q is not None:
+        _expect_kind("out", q, (m, in_dim), INT8)
+        _expect_kind("out", scale, (m,), torch.float32)
+    return m, in_dim, code
+
+
+def quantize_rows_int8(x: torch.Tensor, out=None) -> tuple:
+    """(int8 [m, in], float32 scales [m]) of x [m, in], each row scaled by its largest value, via tb_quantize_rows_int8
+    (into the pair `out` when given)."""
+    q, scale = (None, None) if out is None else out
+    m, in_dim, code = _rows_int8_dims(_kind(x), _kind(q), _kind(scale))
+    dev = _here([t for t in (x, q, scale) if t is not None])
+    if q is None:
+        q, scale = x.new_empty((m, in_dim), dtype=INT8), x.new_empty((m,), dtype=torch.float32)
+    _check(lib.tb_quantize_rows_int8(x.data_ptr(), q.data_ptr(), scale.data_ptr(), m, in_dim, code,
+                                     torch._C._cuda_getCurrentRawStream(dev)))
+    return q, scale
+
+
+def quantize_weight_int8(W: torch.Tensor, out=None) -> tuple:
+    """A dense weight [out, in] as (int8, a scale per output channel): quantize_rows_int8 of its rows."""
+    return quantize_rows_int8(W, out)
+
+
+def reconstruct_weight_int8(s: torch.Tensor, W0: torch.Tensor, U: torch.Tensor | None, V: torch.Tensor | None,
+                            out=None) -> tuple:
+    """diag(s) @ W0 + U @ V.T as (int8 [out, in], float32 scales [out]): rebuilt in float32, then quantised by rows.  The
+    rebuilt weight is a temporary of 4 x out x in bytes."""
+    if out is not None:
+        _rows_int8_dims((W0.shape, torch.float32), _kind(out[0]), _kind(out[1]))
+    return quantize_rows_int8(reconstruct_weight(s, W0, U, V), out)
+
+
+@functools.lru_cache(maxsize=4096)
+def _int8_workspace_size(device: int, m: int, out_dim: int, in_dim: int, x_code: int, y_code: int) -> int:
+    """By sizes and types (and the device, whose compute units the plan counts): a serving loop asks once per shape."""
+    out = ctypes.c_size_t(0)
+    _check(lib.tb_dense_forward_int8_workspace_size(m, out_dim, in_dim, x_code, y_code, ctypes.byref(out)))
+    return out.value
+
+
+def dense_forward_int8_workspace_size(m: int, out_dim: int, in_dim: int, x_dtype: torch.dtype,
+                                      out_dtype: torch.dtype) -> int:
+    """Bytes of workspace that dense_forward_int8 takes on the current device for these sizes."""
+    code = TB_INT8 if x_dtype == INT8 else _dtype_code(x_dtype)
+    return _int8_workspace_size(torch.cuda.current_device(), m, out_dim, in_dim, code, _dtype_code(out_dtype))
+
+
+@functools.lru_cache(maxsize=4096)
+def _dense_int8_dims(x, Wq, w_scale, x_scale, out, out_dtype):
+    """(m, out_dim, in_dim, x code, y code, y dtype) of dense_forward_int8's operands by kind."""
+    (x_shape, x_dtype), (w_shape, _) = x, Wq
+    if len(x_shape) != 2 or len(w_shape) != 2:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [m, in] and Wq [out, in]")
+    quantised = x_dtype == INT8
+    x_code = TB_INT8 if quantised else _dtype_code(x_dtype)
+    m, in_dim = x_shape
+    out_dim = w_shape[0]
+    _expect_kind("Wq", Wq, (out_dim, in_dim), INT8)
+    _expect_kind("w_scale", w_scale, (out_dim,), torch.float32)
+    if quantised != (x_scale is not None):
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "x_scale goes with an x in int8, and only with one")
+    if quantised:
+        _expect_kind("x_scale", x_scale, (m,), torch.float32)
+    if out_dtype is None:
+        out_dtype = out[1] if out is not None else torch.bfloat16 if quantised else x_dtype
+    y_code = _dtype_code(out_dtype)
+    if out is not None:
+        _expect_kind("out", out, (m, out_dim), out_dtype)
+    return m, out_dim, in_dim, x_code, y_code, out_dtype
+
+
+def dense_forward_int8(x: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor, x_scale: torch.Tensor | None = None,
+                       out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                       workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """y = Q(x) @ Wq.T with the scales of tokens and channels applied, via tb_dense_forward_int8.
+
+    x [m, in] in bfloat16 or float32 is quantised within the call (quantize_rows_int8); in int8 it comes with x_scale.
+    y has out's dtype, out_dtype, x's dtype, or bfloat16 for an int8 x.  Sums are exact: a token's row is the same bits
+    in a batch and alone."""
+    m, out_dim, in_dim, x_code, y_code, y_dtype = _dense_int8_dims(_kind(x), _kind(Wq), _kind(w_scale), _kind(x_scale),
+                                                                   _kind(out), out_dtype)
+    dev = _here([t for t in (x, Wq, w_scale, x_scale, out, workspace) if t is not None])
+    if out is None:
+        out = x.new_empty((m, out_dim), dtype=y_dtype)
+    if workspace is None:
+        nbytes = _int8_workspace_size(dev, m, out_dim, in_dim, x_code, y_code)
+        # From torch's allocator, per call: it follows the stream and, under graph capture, the graph's own pool,
+        # so no two graphs share it.
+        workspace = x.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    _check(lib.tb_dense_forward_int8(x.data_ptr(), _ptr(x_scale), Wq.data_ptr(), w_scale.data_ptr(), out.data_ptr(), m,
+                                     out_dim, in_dim, x_code, y_code, _ptr(workspace), nbytes,
+                                     torch._C._cuda_getCurrentRawStream(dev)))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# The norms before and after a block, with its gate and residual scale
+# ---------------------------------------------------------------------------
+
+
+@functools.lru_cache(maxsize=4096)
+def _residual_dims(h, y, weight, post_weight, gate, out_dtype, scale_dtype, norm, dtype, h_out, z, z_scale):
+    """(m, n, dtype code, h code, z code, scale code, z shape and dtype, its scales' shape and dtype, rows per gate row)
+    of residual_norm's operands by kind."""
+    shape, h_dtype = h
+    if len(shape) != 2:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "h must be [m, n]")
+    m, n = shape
+    h_code, code = _dtype_code(h_dtype), _dtype_code(dtype)
+    if y is not None:
+        _expect_kind("y", y, (m, n), dtype)
+    for name, w in (("weight", weight), ("post_weight", post_weight)):
+        if w is not None:
+            _expect_kind(name, w, (n,), dtype)
+    rows = 1
+    if gate is not None:
+        g, _ = gate
+        if g == (n,):
+            rows = max(m, 1)
+        elif len(g) == 2 and g[1] in (n, 1) and (g[0] > 0 and m % g[0] == 0 or g[0] == m):
+            rows = max(m // max(g[0], 1), 1)
+        else:
+            raise TBError(TB_ERR_INVALID_ARGUMENT, f"gate must be [n], or [g, n] or [g, 1] with g dividing {m} rows of {n}, "
+                                                   f"got {list(g)}")
+        _expect_kind("gate", gate, g, dtype)
+    z_code, sc, scales = code, TB_SCALE_F32, None
+    if out_dtype == INT8:
+        z_code, scales = TB_INT8, ((m,), torch.float32)
+    elif out_dtype == E4M3:
+        z_code, sc, scales = TB_E4M3, _scale_code(scale_dtype), ((m, _fp8_blocks(n)), scale_dtype)
+    elif out_dtype is not None and out_dtype != dtype:
+        raise TBError(TB_ERR_UNSUPPORTED, f"z is in {dtype}, int8 or float8_e4m3fn, not {out_dtype}")
+    if not norm and (weight is not None or out_dtype is not None):
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "weight and out_dtype go with the norm")
+    z_kind = ((m, n), out_dtype or dtype) if norm else None
+    if h_out is not None:
+        _expect_kind("out", h_out, (m, n), h_dtype)
+    if z is not None:
+        if not norm:
+            raise TBError(TB_ERR_INVALID_ARGUMENT, "an output for z goes with the norm")
+        _expect_kind("out", z, *z_kind)
+        if (z_scale is None) != (scales is None):
+            raise TBError(TB_ERR_INVALID_ARGUMENT, "an 8-bit z comes with its scales, and only an 8-bit one")
+        if scales is not None:
+            _expect_kind("out", z_scale, *scales)
+    return m, n, code, h_code, z_code, sc, z_kind, scales, rows
+
+
+def residual_norm(h: torch.Tensor, y: torch.Tensor | None = None, weight: torch.Tensor | None = None, *,
+                  post_norm: bool = False, post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                  residual_scale: float = 1.0, eps: float = 1e-6, weight_offset: float = 0.0, norm: bool = True,
+                  out_dtype: torch.dtype | None = None, scale_dtype: torch.dtype = torch.float32, outs=None) -> tuple:
+    """(h', z): the norms before and after a block with its gate and residual scale in one pass, via tb_residual_norm.
+
+    h' = residual_scale * h + gate * a with a = y, or y normed and weighted by post_weight (post_norm); z is h' normed and
+    weighted by weight, for the next projection.  h [m, n] may be float32 beside bfloat16 blocks.  gate: [n], or [g, n] or
+    [g, 1] whose rows serve m / g rows each.  Weights count as weight + weight_offset.  z is in y's dtype (h's without a
+    y), or with out_dtype int8 or float8_e4m3fn a pair (numbers, scales) that the 8-bit projections take.  Without y h' is
+    h itself; with norm=False z is None.  outs: (h', z or None), h' may be h and z y; h, y and the outputs may be strided
+    with adjacent elements (an 8-bit z is dense)."""
+    ho = zo = so = None
+    if outs is not None:
+        ho, zo = outs
+        if isinstance(zo, (tuple, list)):
+            zo, so = zo
+            scale_dtype = so.dtype
+            if out_dtype is None:
+                out_dtype = zo.dtype
+    dtype = h.dtype if y is None else y.dtype
+    if out_dtype is dtype:
+        out_dtype = None
+    m, n, code, h_code, z_code, sc, z_kind, scales, gate_rows = _residual_dims(
+        _kind(h), _kind(y), _kind(weight), _kind(post_weight), _kind(gate), out_dtype, scale_dtype, norm, dtype, _kind(ho),
+        _kind(zo), _kind(so))
+    if y is None and ho is not None:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "without a y there is no h' to write")
+    dev = h.get_device()
+    fine = dev >= 0 and dev == torch.cuda.current_device()
+    for t in (y, gate, ho, zo):
+        fine = fine and (t is None or t.get_device() == dev)
+    for t in (weight, post_weight, so, zo if scales is not None else None):
+        fine = fine and (t is None or (t.get_device() == dev and t.is_contiguous()))
+    if not fine:
+        _need_device(h, y, gate, ho, zo)
+        _need_cuda(weight, post_weight, so, zo if scales is not None else None)
+    if ho is None and y is not None:
+        ho = h.new_empty((m, n))
+    if norm and zo is None:
+        zo = h.new_empty(z_kind[0], dtype=z_kind[1])
+        if scales is not None:
+            so = h.new_empty(scales[0], dtype=scales[1])
+    hs, he = h.stride()
+    ys, ye = y.stride() if y is not None else (0, 1)
+    hos, hoe = ho.stride() if ho is not None else (0, 1)
+    zs, ze = zo.stride() if zo is not None else (0, 1)
+    gs = ge = 0
+    if gate is not None:
+        ge = gate.stride(-1)
+        gs = gate.stride(0) if gate.dim() == 2 else 0
+    channels = gate is not None and gate.shape[-1] == n and (n > 1 or gate.dim() == 1)
+    if n > 1 and (he != 1 or ye != 1 or hoe != 1 or ze != 1 or (channels and ge != 1)):
+        raise TBError(TB_ERR_UNSUPPORTED, "the elements of a row must be adjacent")
+    # tb_residual, every field eight bytes
+    fields = (h.data_ptr(), _ptr(y) or 0, _ptr(post_weight) or 0, _ptr(gate) or 0, _ptr(weight) or 0, _ptr(ho) or 0,
+              _ptr(zo) or 0, _ptr(so) or 0, hs, ys, hos, zs, gate_rows, gs, int(channels))
+    _check(lib.tb_residual_norm((ctypes.c_int64 * 15)(*fields), m, n, residual_scale, eps, weight_offset, post_norm, code,
+                                h_code, z_code, sc, torch._C._cuda_getCurrentRawStream(dev)))
+    return ho if y is not None else h, (zo, so) if scales is not None else zo
+
+
+# ---------------------------------------------------------------------------
 # Head norms with the position rotation, and the path that ends in them
 # ---------------------------------------------------------------------------
 
 
-def _rotated_dims(positions, freqs, tokens: int, dim: int) -> int:
-    """rot_dim after checking the kinds of positions [tokens] and freqs [rot_dim / 2] (both None: 0) against heads of
-    dim."""
+def _rotated_dims(positions, freqs, tokens: int, dim: int, axes=None) -> int:
+    """rot_dim after checking the kinds of positions [tokens] ([axes, tokens] where the pairs have axes) and freqs
+    [rot_dim / 2] (both None: 0) against heads of dim."""
     if (positions is None) != (freqs is None):
         raise TBError(TB_ERR_INVALID_ARGUMENT, "positions and freqs are given together or not at all")
     if freqs is None:
+        if axes is not None:
+            raise TBError(TB_ERR_INVALID_ARGUMENT, "axes go with positions and freqs")
         return 0
     if len(freqs[0]) != 1:
         raise TBError(TB_ERR_INVALID_ARGUMENT, "freqs must be [rot_dim / 2]")
@@ -650,13 +902,32 @@ def _rotated_dims(positions, freqs, tokens: int, dim: int) -> int:
     if rot > dim:
         raise TBError(TB_ERR_INVALID_ARGUMENT, f"{rot} rotated dimensions, but heads of {dim}")
     _expect_kind("freqs", freqs, (rot // 2,), torch.float64)
-    _expect_kind("positions", positions, (tokens,), torch.int64)
+    if axes is None:
+        _expect_kind("positions", positions, (tokens,), torch.int64)
+        return rot
+    if len(axes) != rot // 2 or rot == 0:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, f"axes names the axis of each of {rot // 2} pairs, got {len(axes)}")
+    if len(positions[0]) != 2 or not 1 <= positions[0][0] <= MAX_AXES:
+        raise TBError(TB_ERR_INVALID_ARGUMENT, f"positions must be [1..{MAX_AXES} axes, tokens], got {list(positions[0])}")
+    _expect_kind("positions", positions, (positions[0][0], tokens), torch.int64)
+    if not all(isinstance(a, int) and 0 <= a < positions[0][0] for a in axes):
+        raise TBError(TB_ERR_INVALID_ARGUMENT, f"an axis lies outside 0..{positions[0][0] - 1}")
     return rot
 
 
+def _axis_layout(axes, axis_halves: bool, interleaved: bool, norm: bool) -> None:
+    if axes is None and (axis_halves or not norm):
+        raise TBError(TB_ERR_INVALID_ARGUMENT, "axis_halves and norm=False go with axes")
+    if axis_halves:
+        if interleaved:
+            raise TBError(TB_ERR_INVALID_ARGUMENT, "pairs are interleaved or in halves of their axis's span, not both")
+        if sum(a != b for a, b in zip(axes, axes[1:])) != len(set(axes)) - 1:
+            raise TBError(TB_ERR_INVALID_ARGUMENT, "with axis_halves the pairs of each axis are consecutive")
+
+
 @functools.lru_cache(maxsize=4096)
-def _heads_dims(parts, positions, freqs, outs):
-    """(tokens, head_dim, rot_dim, dtype code) of head_norm_rotate's operands by kind."""
+def _heads_dims(parts, positions, freqs, outs, axes=None):
+    """(tokens, head_dim, rot_dim, dtype code, the axes as bytes) of head_norm_rotate's operands by kind."""
     if not 1 <= len(parts) <= MAX_GROUP:
         raise TBError(TB_ERR_INVALID_ARGUMENT, f"a call takes 1..{MAX_GROUP} parts")
     if outs is not None and len(outs) != len(parts):
@@ -666,26 +937,35 @@ def _heads_dims(parts, positions, freqs, outs):
             raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [tokens, heads, head_dim]")
     (tokens, _, dim), dtype = parts[0][0]
     code = _dtype_code(dtype)
-    rot = _rotated_dims(positions, freqs, tokens, dim)
+    rot = _rotated_dims(positions, freqs, tokens, dim, axes)
     for j, (x, w) in enumerate(parts):
         _expect_kind(f"part {j}", x, (tokens, x[0][1], dim), dtype)
         if w is not None:
             _expect_kind("weight", w, (dim,), dtype)
         if outs is not None:
             _expect_kind("out", outs[j], x[0], dtype)
-    return tokens, dim, rot, code
+    return tokens, dim, rot, code, None if axes is None else bytes(axes)
 
 
 def head_norm_rotate(parts, positions: torch.Tensor | None, freqs: torch.Tensor | None, eps: float = 1e-6,
-                     weight_offset: float = 0.0, interleaved: bool = False, outs=None) -> list:
+                     weight_offset: float = 0.0, interleaved: bool = False, outs=None, axes=None,
+                     axis_halves: bool = False, norm: bool = True) -> list:
     """Per-head norm and position rotation of several tensors of heads in one pass, via tb_head_norm_rotate.
 
     parts: (x [tokens, heads, head_dim], weight [head_dim] or None) pairs of one dtype, e.g. queries and keys; x may
     be strided (a view of packed rows) with adjacent elements.  positions int64 [tokens], freqs float64 [rot_dim / 2]
     (radians per position; both None: no rotation).  Returns new tensors, or writes `outs` (x itself for in place, or
-    a view of a cache)."""
-    tokens, dim, rot, code = _heads_dims(tuple([(_kind(x), _kind(w)) for x, w in parts]), _kind(positions),
-                                         _kind(freqs), None if outs is None else tuple([_kind(y) for y in outs]))
+    a view of a cache).
+
+    With several axes (time, height, width; via tb_head_norm_rotate_axes) positions are [axes, tokens] and `axes` names
+    the axis of each of the rot_dim / 2 pairs (a tuple of ints); with axis_halves a pair's elements lie in the two halves
+    of its axis's own span instead of the head's.  With norm=False (and axes) the heads are rotated only."""
+    if axes is not None:
+        axes = tuple(axes)
+    tokens, dim, rot, code, pair_axis = _heads_dims(
+        tuple([(_kind(x), _kind(w)) for x, w in parts]), _kind(positions), _kind(freqs),
+        None if outs is None else tuple([_kind(y) for y in outs]), axes)
+    _axis_layout(axes, axis_halves, interleaved, norm)
     dev = parts[0][0].get_device()
     fine = dev >= 0 and dev == torch.cuda.current_device()
     ys, fields = [], []
@@ -715,25 +995,42 @@ def head_norm_rotate(parts, positions: torch.Tensor | None, freqs: torch.Tensor 
     if not fine:
         _need_device(*[x for x, _ in parts], *ys)
         _need_cuda(positions, freqs, *[w for _, w in parts])
-    _check(lib.tb_head_norm_rotate(len(parts), (ctypes.c_int64 * len(fields))(*fields), tokens, dim, rot, interleaved,
-                                   _ptr(positions), _ptr(freqs), eps, weight_offset, code,
-                                   torch._C._cuda_getCurrentRawStream(dev)))
+    if axes is None:
+        _check(lib.tb_head_norm_rotate(len(parts), (ctypes.c_int64 * len(fields))(*fields), tokens, dim, rot, interleaved,
+                                       _ptr(positions), _ptr(freqs), eps, weight_offset, code,
+                                       torch._C._cuda_getCurrentRawStream(dev)))
+    else:
+        pairs = TB_PAIRS_AXIS if axis_halves else TB_PAIRS_INTERLEAVED if interleaved else TB_PAIRS_HALF
+        _check(lib.tb_head_norm_rotate_axes(len(parts), (ctypes.c_int64 * len(fields))(*fields), tokens, dim, rot, pairs,
+                                            positions.shape[0], positions.data_ptr(), pair_axis, freqs.data_ptr(), norm,
+                                            eps, weight_offset, code, torch._C._cuda_getCurrentRawStream(dev)))
     return ys
 
 
-def qkv_forward(x: torch.Tensor, q, k, v, head_dim: int, positions: torch.Tensor | None, freqs: torch.Tensor | None,
+def qkv_forward(x, q, k, v, head_dim: int, positions: torch.Tensor | None, freqs: torch.Tensor | None,
                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
-                weight_offset: float = 0.0, interleaved: bool = False) -> tuple:
+                weight_offset: float = 0.0, interleaved: bool = False, axes=None, axis_halves: bool = False,
+                out_dtype: torch.dtype | None = None) -> tuple:
     """The input half of an attention layer: (queries, keys, values), each [m, heads, head_dim], of x [m, in].
 
-    q, k, v are the layer's projections, all as bundles (s, W0, U, V) in one grouped launch, or all in 8-bit blocks
-    (Wq, w_scale) with x quantised once; queries and keys then get their head norms and rotation in place."""
+    q, k, v are the layer's projections, all as bundles (s, W0, U, V) in one grouped launch, or all in 8 bits (Wq,
+    w_scale), e4m3 blocks or int8 channels, with x quantised once; for these x may be the pair (numbers, scales) that
+    residual_norm made, and out_dtype (bfloat16) is the type of the heads.  Queries and keys then get their head norms and
+    rotation in place (axes, axis_halves: as in head_norm_rotate)."""
     kinds = {len(p) for p in (q, k, v)}
     if kinds not in ({4}, {2}):
         raise TBError(TB_ERR_INVALID_ARGUMENT, "q, k and v are all (s, W0, U, V) or all (Wq, w_scale)")
     at = 1 if kinds == {4} else 0
+    x_scale = None
+    if isinstance(x, (tuple, list)):
+        if kinds == {4} or len(x) != 2:
+            raise TBError(TB_ERR_INVALID_ARGUMENT, "an x of (numbers, scales) goes with projections in 8 bits")
+        x, x_scale = x
     if x.dim() != 2:
         raise TBError(TB_ERR_INVALID_ARGUMENT, "x must be [m, in]")
+    if x_scale is None and out_dtype not in (None, x.dtype):
+        raise TBError(TB_ERR_INVALID_ARGUMENT, f"the heads of an x in {x.dtype} are in {x.dtype}")
+    dtype = (out_dtype or torch.bfloat16) if x_scale is not None else x.dtype
     for name, p in zip("qkv", (q, k, v)):
         if head_dim < 1 or p[at].dim() != 2 or p[at].shape[0] % head_dim:
             raise TBError(TB_ERR_INVALID_ARGUMENT, f"{name}: {list(p[at].shape)} is not rows of heads of {head_dim}")
@@ -744,34 +1041,49 @@ def qkv_forward(x: torch.Tensor, q, k, v, head_dim: int, positions: torch.Tensor
         raise TBError(TB_ERR_UNSUPPORTED, f"more than {MAX_HEADS} heads of queries and keys")
     if not eps >= 0:
         raise TBError(TB_ERR_INVALID_ARGUMENT, "eps must be >= 0")
-    _rotated_dims(_kind(positions), _kind(freqs), x.shape[0], head_dim)
+    if axes is not None:
+        axes = tuple(axes)
+    _rotated_dims(_kind(positions), _kind(freqs), x.shape[0], head_dim, axes)
+    _axis_layout(axes, axis_halves, interleaved, True)
     for w in (q_weight, k_weight):
         if w is not None:
-            _expect("head weight", w, (head_dim,), x.dtype)
+            _expect("head weight", w, (head_dim,), dtype)
+    int8 = kinds == {2} and q[0].dtype == INT8
     if kinds == {2}:
-        _dtype_code(x.dtype)
+        _dtype_code(dtype)
         m, in_dim = x.shape
         sizes = []
         for name, (Wq, scale) in zip("qkv", (q, k, v)):
+            if int8:
+                xs = _kind(x_scale) if x_scale is not None else ((m,), torch.float32)
+                x_kind = _kind(x) if x_scale is not None else (x.shape, INT8)
+                sizes.append(_dense_int8_dims(x_kind, _kind(Wq), _kind(scale), xs, None, dtype)[:5])
+                continue
             if scale.dtype != q[1].dtype:
                 raise TBError(TB_ERR_INVALID_ARGUMENT, f"{name}: scales are {scale.dtype}, those of q {q[1].dtype}")
-            xs = (m, _fp8_blocks(in_dim)), scale.dtype
-            sizes.append(_dense_fp8_dims((x.shape, E4M3), _kind(Wq), _kind(scale), xs, None, x.dtype)[:6])
+            xs = _kind(x_scale) if x_scale is not None else ((m, _fp8_blocks(in_dim)), scale.dtype)
+            x_kind = _kind(x) if x_scale is not None else (x.shape, E4M3)
+            sizes.append(_dense_fp8_dims(x_kind, _kind(Wq), _kind(scale), xs, None, dtype)[:6])
         if in_dim % 16:
             raise TBError(TB_ERR_UNSUPPORTED, f"in_dim {in_dim} is not a multiple of 16")
+        if x_scale is None:
+            _dtype_code(x.dtype)
     _need_cuda(positions, freqs, q_weight, k_weight)
     if kinds == {4}:
         ys = linear_forward_group([(x, *p) for p in (q, k, v)])
     else:
-        dev = _here([x, *q, *k, *v])
+        dev = _here([t for t in (x, x_scale, *q, *k, *v) if t is not None])
         for name, (Wq, _), size in zip("qkv", (q, k, v), sizes):
             if Wq.data_ptr() % 16:
                 raise TBError(TB_ERR_UNSUPPORTED, f"{name}: Wq must be 16-byte aligned")
-            _fp8_workspace_size(dev, *size)   # (raises where a size is too large)
-        xq, xs = quantize_activations(x, q[1].dtype)
-        ys = [dense_forward_fp8(xq, *p, x_scale=xs, out_dtype=x.dtype) for p in (q, k, v)]
+            (_int8_workspace_size if int8 else _fp8_workspace_size)(dev, *size)   # (raises where a size is too large)
+        if x_scale is None:
+            x, x_scale = quantize_rows_int8(x) if int8 else quantize_activations(x, q[1].dtype)
+        dense = dense_forward_int8 if int8 else dense_forward_fp8
+        ys = [dense(x, *p, x_scale=x_scale, out_dtype=dtype) for p in (q, k, v)]
     yq, yk, yv = (y.view(y.shape[0], y.shape[1] // head_dim, head_dim) for y in ys)
-    head_norm_rotate([(yq, q_weight), (yk, k_weight)], positions, freqs, eps, weight_offset, interleaved, [yq, yk])
+    head_norm_rotate([(yq, q_weight), (yk, k_weight)], positions, freqs, eps, weight_offset, interleaved, [yq, yk], axes,
+                     axis_halves)
     return yq, yk, yv
 
 

@@ -729,6 +729,80 @@ bool rows_meet(const HeadRows& a, const HeadRows& b, int64_t tokens, int64_t row
   return false;
 }
 
+// The same for 8-bit integers, whose sums of in_dim products stay within 32 bits.
+tb_status check_int8_dims(int64_t m, int64_t out_dim, int64_t in_dim, int64_t step) {
+  if (in_dim > TB_INT8_MAX_IN_DIM)
+    return fail(TB_ERR_UNSUPPORTED, "in_dim %lld exceeds %d", (long long)in_dim, TB_INT8_MAX_IN_DIM);
+  return check_fp8_dims(m, out_dim, in_dim, step);
+}
+
+// The arguments that tb_head_norm_rotate and tb_head_norm_rotate_axes share; *empty: there is nothing to do.
+tb_status check_heads(int32_t n, const tb_head_part* parts, int64_t tokens, int64_t head_dim, int64_t rot_dim,
+                      const int64_t* positions, const double* freqs, float eps, tb_dtype dtype, bool* empty) {
+  if (!valid_dtype(dtype)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(dtype));
+  if (n < 1 || n > TB_MAX_GROUP) return fail(TB_ERR_INVALID_ARGUMENT, "n %d outside [1, %d]", n, TB_MAX_GROUP);
+  if (!parts) return fail(TB_ERR_INVALID_ARGUMENT, "parts is NULL");
+  if (tokens < 0 || head_dim < 1 || rot_dim < 0 || rot_dim > head_dim || rot_dim % 2 != 0)
+    return fail(TB_ERR_INVALID_ARGUMENT, "need tokens >= 0, head_dim >= 1 and an even rot_dim in [0, head_dim] (got %lld, %lld, %lld)",
+                (long long)tokens, (long long)head_dim, (long long)rot_dim);
+  if (!(eps >= 0.f)) return fail(TB_ERR_INVALID_ARGUMENT, "eps must be >= 0");
+  if (head_dim > TB_MAX_HEAD_DIM || tokens > TB_MAX_HEAD_TOKENS)
+    return fail(TB_ERR_UNSUPPORTED, "head_dim exceeds %d or tokens %d", TB_MAX_HEAD_DIM, TB_MAX_HEAD_TOKENS);
+  int64_t heads = 0;
+  for (int j = 0; j < n; ++j) {
+    const tb_head_part& p = parts[j];
+    if (p.heads < 0) return fail(TB_ERR_INVALID_ARGUMENT, "part %d: heads < 0", j);
+    if (p.heads > TB_MAX_HEADS || (heads += p.heads) > TB_MAX_HEADS)
+      return fail(TB_ERR_UNSUPPORTED, "more than %d heads", TB_MAX_HEADS);
+    if (tokens == 0 || p.heads == 0) continue;
+    if (!p.x || !p.y) return fail(TB_ERR_INVALID_ARGUMENT, "part %d: x and y must be non-NULL", j);
+    const int64_t strides[4] = {p.x_token_stride, p.x_head_stride, p.y_token_stride, p.y_head_stride};
+    for (int64_t s : strides) {
+      if (s < 0) return fail(TB_ERR_INVALID_ARGUMENT, "part %d: a stride is negative", j);
+      if (s > (int64_t(1) << 35)) return fail(TB_ERR_UNSUPPORTED, "part %d: a stride exceeds 2^35", j);
+    }
+    if (!aligned_to(p.x, esize(dtype)) || !aligned_to(p.y, esize(dtype)) || !aligned_to(p.weight, esize(dtype)))
+      return fail(TB_ERR_UNSUPPORTED, "part %d: pointers must be aligned to their element size", j);
+    // In place means element for element.
+    if (p.x == p.y && ((tokens > 1 && p.x_token_stride != p.y_token_stride) ||
+                       (p.heads > 1 && p.x_head_stride != p.y_head_stride)))
+      return fail(TB_ERR_INVALID_ARGUMENT, "part %d: y is x, with other strides", j);
+    const HeadRows x = head_rows(p.x, p.heads, p.x_token_stride, p.x_head_stride, dtype);
+    const HeadRows y = head_rows(p.y, p.heads, p.y_token_stride, p.y_head_stride, dtype);
+    const int64_t row = head_dim * int64_t(esize(dtype));
+    if (p.x != p.y && rows_meet(x, y, tokens, row))
+      return fail(TB_ERR_INVALID_ARGUMENT, "part %d: y overlaps x without being x", j);
+    for (int k = 0; k < j; ++k) {
+      const tb_head_part& o = parts[k];
+      if (o.heads == 0) continue;
+      const HeadRows ox = head_rows(o.x, o.heads, o.x_token_stride, o.x_head_stride, dtype);
+      const HeadRows oy = head_rows(o.y, o.heads, o.y_token_stride, o.y_head_stride, dtype);
+      if (rows_meet(oy, y, tokens, row) || rows_meet(oy, x, tokens, row) || rows_meet(ox, y, tokens, row))
+        return fail(TB_ERR_INVALID_ARGUMENT, "parts %d and %d: one writes what the other reads or writes", k, j);
+    }
+    if (!rows_apart(tokens, p.heads, head_dim, p.y_token_stride, p.y_head_stride))
+      return fail(TB_ERR_INVALID_ARGUMENT, "part %d: the rows of y overlap", j);
+  }
+  *empty = tokens == 0 || heads == 0;
+  if (*empty) return TB_OK;
+  if (rot_dim > 0 && (!positions || !freqs))
+    return fail(TB_ERR_INVALID_ARGUMENT, "positions and freqs must be non-NULL when rot_dim > 0");
+  if (rot_dim > 0 && (!aligned_to(positions, 8) || !aligned_to(freqs, 8)))
+    return fail(TB_ERR_UNSUPPORTED, "positions and freqs must be 8-byte aligned");
+  return TB_OK;
+}
+
+// Whether rows of la and lb bytes at steps sa and sb share memory: exact for equal steps, extents else.
+bool rows_share(const void* a, int64_t la, int64_t sa, const void* b, int64_t lb, int64_t sb, int64_t m) {
+  const int64_t pa = int64_t(reinterpret_cast<uintptr_t>(a)), pb = int64_t(reinterpret_cast<uintptr_t>(b));
+  const int64_t ea = pa + (m - 1) * sa + la, eb = pb + (m - 1) * sb + lb;
+  if (pa >= eb || pb >= ea) return false;
+  if (m == 1 || sa != sb || sa == 0) return true;
+  // Rows of b start at multiples of the step from a's first: a's next one must begin behind b's end.
+  const int64_t d = ((pb - pa) % sa + sa) % sa;
+  return d < la || d + lb > sa;
+}
+
 }  // namespace
 }  // namespace tb
 
@@ -826,58 +900,204 @@ tb_status tb_dense_forward_fp8(const void* x, const void* x_scale, const void* w
 tb_status tb_head_norm_rotate(int32_t n, const tb_head_part* parts, int64_t tokens, int64_t head_dim, int64_t rot_dim,
                               int32_t interleaved, const int64_t* positions, const double* freqs, float eps,
                               float weight_offset, tb_dtype dtype, void* stream) {
-  if (!valid_dtype(dtype)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(dtype));
-  if (n < 1 || n > TB_MAX_GROUP) return fail(TB_ERR_INVALID_ARGUMENT, "n %d outside [1, %d]", n, TB_MAX_GROUP);
-  if (!parts) return fail(TB_ERR_INVALID_ARGUMENT, "parts is NULL");
-  if (tokens < 0 || head_dim < 1 || rot_dim < 0 || rot_dim > head_dim || rot_dim % 2 != 0)
-    return fail(TB_ERR_INVALID_ARGUMENT, "need tokens >= 0, head_dim >= 1 and an even rot_dim in [0, head_dim] (got %lld, %lld, %lld)",
-                (long long)tokens, (long long)head_dim, (long long)rot_dim);
-  if (!(eps >= 0.f)) return fail(TB_ERR_INVALID_ARGUMENT, "eps must be >= 0");
-  if (head_dim > TB_MAX_HEAD_DIM || tokens > TB_MAX_HEAD_TOKENS)
-    return fail(TB_ERR_UNSUPPORTED, "head_dim exceeds %d or tokens %d", TB_MAX_HEAD_DIM, TB_MAX_HEAD_TOKENS);
-  int64_t heads = 0;
-  for (int j = 0; j < n; ++j) {
-    const tb_head_part& p = parts[j];
-    if (p.heads < 0) return fail(TB_ERR_INVALID_ARGUMENT, "part %d: heads < 0", j);
-    if (p.heads > TB_MAX_HEADS || (heads += p.heads) > TB_MAX_HEADS)
-      return fail(TB_ERR_UNSUPPORTED, "more than %d heads", TB_MAX_HEADS);
-    if (tokens == 0 || p.heads == 0) continue;
-    if (!p.x || !p.y) return fail(TB_ERR_INVALID_ARGUMENT, "part %d: x and y must be non-NULL", j);
-    const int64_t strides[4] = {p.x_token_stride, p.x_head_stride, p.y_token_stride, p.y_head_stride};
-    for (int64_t s : strides) {
-      if (s < 0) return fail(TB_ERR_INVALID_ARGUMENT, "part %d: a stride is negative", j);
-      if (s > (int64_t(1) << 35)) return fail(TB_ERR_UNSUPPORTED, "part %d: a stride exceeds 2^35", j);
-    }
-    if (!aligned_to(p.x, esize(dtype)) || !aligned_to(p.y, esize(dtype)) || !aligned_to(p.weight, esize(dtype)))
-      return fail(TB_ERR_UNSUPPORTED, "part %d: pointers must be aligned to their element size", j);
-    // In place means element for element.
-    if (p.x == p.y && ((tokens > 1 && p.x_token_stride != p.y_token_stride) ||
-                       (p.heads > 1 && p.x_head_stride != p.y_head_stride)))
-      return fail(TB_ERR_INVALID_ARGUMENT, "part %d: y is x, with other strides", j);
-    const HeadRows x = head_rows(p.x, p.heads, p.x_token_stride, p.x_head_stride, dtype);
-    const HeadRows y = head_rows(p.y, p.heads, p.y_token_stride, p.y_head_stride, dtype);
-    const int64_t row = head_dim * int64_t(esize(dtype));
-    if (p.x != p.y && rows_meet(x, y, tokens, row))
-      return fail(TB_ERR_INVALID_ARGUMENT, "part %d: y overlaps x without being x", j);
-    for (int k = 0; k < j; ++k) {
-      const tb_head_part& o = parts[k];
-      if (o.heads == 0) continue;
-      const HeadRows ox = head_rows(o.x, o.heads, o.x_token_stride, o.x_head_stride, dtype);
-      const HeadRows oy = head_rows(o.y, o.heads, o.y_token_stride, o.y_head_stride, dtype);
-      if (rows_meet(oy, y, tokens, row) || rows_meet(oy, x, tokens, row) || rows_meet(ox, y, tokens, row))
-        return fail(TB_ERR_INVALID_ARGUMENT, "parts %d and %d: one writes what the other reads or writes", k, j);
-    }
-    if (!rows_apart(tokens, p.heads, head_dim, p.y_token_stride, p.y_head_stride))
-      return fail(TB_ERR_INVALID_ARGUMENT, "part %d: the rows of y overlap", j);
-  }
-  if (tokens == 0 || heads == 0) return ok();
-  if (rot_dim > 0 && (!positions || !freqs))
-    return fail(TB_ERR_INVALID_ARGUMENT, "positions and freqs must be non-NULL when rot_dim > 0");
-  if (rot_dim > 0 && (!aligned_to(positions, 8) || !aligned_to(freqs, 8)))
-    return fail(TB_ERR_UNSUPPORTED, "positions and freqs must be 8-byte aligned");
+  bool empty;
+  tb_status st = check_heads(n, parts, tokens, head_dim, rot_dim, positions, freqs, eps, dtype, &empty);
+  if (st != TB_OK) return st;
+  if (empty) return ok();
   hipError_t e = launch_heads(dtype, n, parts, tokens, int(head_dim), int(rot_dim), interleaved != 0, positions, freqs,
                               eps, weight_offset, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "launching the head norms");
+  return ok();
+}
+
+tb_status tb_head_norm_rotate_axes(int32_t n, const tb_head_part* parts, int64_t tokens, int64_t head_dim,
+                                   int64_t rot_dim, tb_pairs pairs, int32_t axes, const int64_t* positions,
+                                   const uint8_t* pair_axis, const double* freqs, int32_t norm, float eps,
+                                   float weight_offset, tb_dtype dtype, void* stream) {
+  if (pairs != TB_PAIRS_HALF && pairs != TB_PAIRS_INTERLEAVED && pairs != TB_PAIRS_AXIS)
+    return fail(TB_ERR_INVALID_ARGUMENT, "unknown layout of pairs %d", int(pairs));
+  if (axes < 1 || axes > TB_MAX_AXES)
+    return fail(TB_ERR_INVALID_ARGUMENT, "axes %d outside [1, %d]", axes, TB_MAX_AXES);
+  if (rot_dim < 2) return fail(TB_ERR_INVALID_ARGUMENT, "rot_dim %lld < 2", (long long)rot_dim);
+  bool empty;
+  tb_status st = check_heads(n, parts, tokens, head_dim, rot_dim, positions, freqs, norm ? eps : 0.f, dtype, &empty);
+  if (st != TB_OK) return st;
+  if (!pair_axis) return fail(TB_ERR_INVALID_ARGUMENT, "pair_axis is NULL");
+  unsigned seen = 0;   // axes whose pairs have begun
+  for (int64_t p = 0; p < rot_dim / 2; ++p) {
+    const int ax = pair_axis[p];
+    if (ax >= axes) return fail(TB_ERR_INVALID_ARGUMENT, "pair %lld: axis %d of %d", (long long)p, ax, axes);
+    if (pairs == TB_PAIRS_AXIS && (p == 0 || ax != pair_axis[p - 1]) && (seen >> ax & 1u))
+      return fail(TB_ERR_INVALID_ARGUMENT, "pair %lld: the pairs of axis %d are not consecutive", (long long)p, ax);
+    seen |= 1u << ax;
+  }
+  if (!norm)
+    for (int j = 0; j < n; ++j)
+      if (parts[j].weight) return fail(TB_ERR_INVALID_ARGUMENT, "part %d has a weight, but there is no norm", j);
+  if (empty) return ok();
+  hipError_t e = launch_heads_axes(dtype, n, parts, tokens, int(head_dim), int(rot_dim),
+                                   HeadAxes{pairs, axes, pair_axis, norm != 0}, positions, freqs, eps, weight_offset,
+                                   static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "launching the head norms");
+  return ok();
+}
+
+tb_status tb_quantize_rows_int8(const void* x, void* q, float* scale, int64_t m, int64_t in_dim, tb_dtype dtype,
+                                void* stream) {
+  if (!valid_dtype(dtype)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(dtype));
+  tb_status st = check_int8_dims(m, 1, in_dim, 8);
+  if (st != TB_OK) return st;
+  if (m == 0) return ok();
+  if (!x || !q || !scale) return fail(TB_ERR_INVALID_ARGUMENT, "x, q and scale must be non-NULL");
+  if (!aligned16(x) || !aligned_to(q, 8)) return fail(TB_ERR_UNSUPPORTED, "x must be 16-byte and q 8-byte aligned");
+  if (!aligned_to(scale, 4)) return fail(TB_ERR_UNSUPPORTED, "scale must be aligned to its element size");
+  hipError_t e = launch_int8_rows(dtype, x, q, scale, m, in_dim, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "launching the row quantiser");
+  return ok();
+}
+
+tb_status tb_dense_forward_int8_workspace_size(int64_t m, int64_t out_dim, int64_t in_dim, tb_dtype x_dtype,
+                                               tb_dtype y_dtype, size_t* bytes_out) {
+  if (bytes_out == nullptr) return fail(TB_ERR_INVALID_ARGUMENT, "bytes_out is NULL");
+  if (!valid_dtype(x_dtype) && x_dtype != TB_INT8)
+    return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(x_dtype));
+  if (!valid_dtype(y_dtype)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(y_dtype));
+  tb_status st = check_int8_dims(m, out_dim, in_dim, 16);
+  if (st != TB_OK) return st;
+  *bytes_out = 0;
+  if (m == 0) return ok();
+  int cus = 0;
+  if (int e = device_cu_count(&cus)) return hip_fail(hipError_t(e), "querying the compute-unit count");
+  *bytes_out = plan_int8(m, out_dim, in_dim, x_dtype == TB_INT8, y_dtype, cus).bytes;
+  return ok();
+}
+
+tb_status tb_dense_forward_int8(const void* x, const float* x_scale, const void* wq, const float* w_scale, void* y,
+                                int64_t m, int64_t out_dim, int64_t in_dim, tb_dtype x_dtype, tb_dtype y_dtype,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  const bool quantised = x_dtype == TB_INT8;
+  if (!valid_dtype(x_dtype) && !quantised) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(x_dtype));
+  if (!valid_dtype(y_dtype)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(y_dtype));
+  tb_status st = check_int8_dims(m, out_dim, in_dim, 16);
+  if (st != TB_OK) return st;
+  if (quantised ? (m > 0 && !x_scale) : x_scale != nullptr)
+    return fail(TB_ERR_INVALID_ARGUMENT, "x_scale goes with an x in 8-bit integers, and only with one");
+  if (m == 0) return ok();
+  if (!x || !wq || !w_scale || !y) return fail(TB_ERR_INVALID_ARGUMENT, "x, wq, w_scale and y must be non-NULL");
+  if (!aligned16(x) || !aligned16(wq)) return fail(TB_ERR_UNSUPPORTED, "x and wq must be 16-byte aligned");
+  if (!aligned_to(x_scale, 4) || !aligned_to(w_scale, 4) || !aligned_to(y, esize(y_dtype)))
+    return fail(TB_ERR_UNSUPPORTED, "scales and y must be aligned to their element size");
+  int cus = 0;
+  if (int e = device_cu_count(&cus)) return hip_fail(hipError_t(e), "querying the compute-unit count");
+  const Int8Plan p = plan_int8(m, out_dim, in_dim, quantised, y_dtype, cus);
+  if (p.bytes > 0) {
+    if (!workspace) return fail(TB_ERR_INVALID_ARGUMENT, "workspace must be non-NULL");
+    if (!aligned_to(workspace, 256)) return fail(TB_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
+    if (workspace_bytes < p.bytes)
+      return fail(TB_ERR_INVALID_ARGUMENT, "workspace of %zu bytes is below the %zu needed", workspace_bytes, p.bytes);
+  }
+  hipError_t e = launch_int8_product(p, x_dtype, y_dtype, x, x_scale, wq, w_scale, y, m, out_dim, in_dim,
+                                     static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "launching the 8-bit integer product");
+  return ok();
+}
+
+tb_status tb_residual_norm(const tb_residual* tensors, int64_t m, int64_t n, float residual_scale, float eps,
+                           float weight_offset, int32_t post_norm, tb_dtype dtype, tb_dtype h_dtype, tb_dtype z_dtype,
+                           tb_scale scale_type, void* stream) {
+  if (!valid_dtype(dtype)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(dtype));
+  if (!valid_dtype(h_dtype)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(h_dtype));
+  if (z_dtype != dtype && z_dtype != TB_INT8 && z_dtype != TB_E4M3)
+    return fail(TB_ERR_INVALID_ARGUMENT, "z is in dtype or in 8 bits, not %d", int(z_dtype));
+  if (!valid_scale(scale_type)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown scale type %d", int(scale_type));
+  if (!tensors) return fail(TB_ERR_INVALID_ARGUMENT, "tensors is NULL");
+  if (m < 0 || n < 1)
+    return fail(TB_ERR_INVALID_ARGUMENT, "need m >= 0 and n >= 1 (got %lld, %lld)", (long long)m, (long long)n);
+  if (m > TB_FP8_MAX_TOKENS || n > TB_MAX_NORM_DIM)
+    return fail(TB_ERR_UNSUPPORTED, "m exceeds %d or n %d", TB_FP8_MAX_TOKENS, TB_MAX_NORM_DIM);
+  if (!(eps >= 0.f)) return fail(TB_ERR_INVALID_ARGUMENT, "eps must be >= 0");
+  const tb_residual& r = *tensors;
+  const bool held = z_dtype != dtype;
+  if (held && n % 8 != 0) return fail(TB_ERR_UNSUPPORTED, "an 8-bit z needs n %% 8 == 0, not %lld", (long long)n);
+  if (m == 0) return ok();   // (the tensors may be NULL)
+  if (!r.y && (r.gate || post_norm || residual_scale != 1.f))
+    return fail(TB_ERR_INVALID_ARGUMENT, "a gate, post_norm and a residual scale go with a y");
+  if (r.post_weight && !post_norm) return fail(TB_ERR_INVALID_ARGUMENT, "post_weight goes with post_norm");
+  if (r.gate && r.gate_rows < 1) return fail(TB_ERR_INVALID_ARGUMENT, "gate_rows must be >= 1");
+  if (r.gate && r.gate_channels != 0 && r.gate_channels != 1)
+    return fail(TB_ERR_INVALID_ARGUMENT, "gate_channels is 0 or 1");
+  if (!r.h) return fail(TB_ERR_INVALID_ARGUMENT, "h must be non-NULL");
+  if (!r.y != !r.h_out) return fail(TB_ERR_INVALID_ARGUMENT, "y and h_out are given together or not at all");
+  if (!r.z && (!r.y || r.z_scale || r.weight || held))
+    return fail(TB_ERR_INVALID_ARGUMENT, r.y ? "weight and 8 bits go with a z" : "neither y nor z is given");
+  if (r.z && held != (r.z_scale != nullptr)) return fail(TB_ERR_INVALID_ARGUMENT, "z_scale goes with an 8-bit z, and only with one");
+  const size_t es = esize(dtype), hs = esize(h_dtype);
+  const int64_t blocks = fp8_blocks(n), zes = held ? 1 : int64_t(es);
+  const size_t ss = z_dtype == TB_INT8 ? 4 : scale_bytes(scale_type);
+  struct Rows {
+    const char* name;
+    const void* p;
+    int64_t stride, bytes, size;   // stride and row in bytes
+  };
+  const Rows in[2] = {{"h", r.h, r.h_stride * int64_t(hs), n * int64_t(hs), int64_t(hs)},
+                      {"y", r.y, r.y_stride * int64_t(es), n * int64_t(es), int64_t(es)}};
+  const int64_t scales = z_dtype == TB_INT8 ? 4 : blocks * int64_t(ss);
+  const Rows out[3] = {{"h_out", r.h_out, r.h_out_stride * int64_t(hs), n * int64_t(hs), int64_t(hs)},
+                       {"z", r.z, held ? n : r.z_stride * int64_t(es), n * zes, zes},
+                       {"z_scale", r.z ? r.z_scale : nullptr, scales, scales, int64_t(ss)}};
+  if (m > 1) {
+    const struct { const char* name; const void* p; int64_t s; } strides[4] = {
+        {"h", r.h, r.h_stride}, {"y", r.y, r.y_stride}, {"h_out", r.h_out, r.h_out_stride},
+        {"z", held ? nullptr : r.z, r.z_stride}};
+    for (int j = 0; j < 4; ++j) {
+      if (!strides[j].p) continue;
+      if (strides[j].s < 0) return fail(TB_ERR_INVALID_ARGUMENT, "the stride of %s is negative", strides[j].name);
+      if (strides[j].s > (int64_t(1) << 35)) return fail(TB_ERR_UNSUPPORTED, "the stride of %s exceeds 2^35", strides[j].name);
+      if (j >= 2 && strides[j].s < n) return fail(TB_ERR_INVALID_ARGUMENT, "the rows of %s overlap", strides[j].name);
+    }
+  }
+  if (r.gate && (m - 1) / r.gate_rows > 0) {
+    if (r.gate_stride < 0) return fail(TB_ERR_INVALID_ARGUMENT, "the stride of gate is negative");
+    if (r.gate_stride > (int64_t(1) << 35)) return fail(TB_ERR_UNSUPPORTED, "the stride of gate exceeds 2^35");
+  }
+  for (const Rows& t : in)
+    if (!aligned_to(t.p, size_t(t.size))) return fail(TB_ERR_UNSUPPORTED, "%s must be aligned to its element size", t.name);
+  for (const Rows& t : out)
+    if (!aligned_to(t.p, size_t(t.size))) return fail(TB_ERR_UNSUPPORTED, "%s must be aligned to its element size", t.name);
+  const struct { const char* name; const void* p; int64_t bytes; bool whole; } small[3] = {
+      {"post_weight", r.post_weight, n * int64_t(es), true}, {"weight", r.weight, n * int64_t(es), true},
+      {"gate", r.gate, r.gate ? ((m - 1) / r.gate_rows * r.gate_stride + (r.gate_channels ? n : 1)) * int64_t(es) : 0,
+       r.gate_channels == 1}};
+  for (const auto& t : small)
+    if (!aligned_to(t.p, es)) return fail(TB_ERR_UNSUPPORTED, "%s must be aligned to its element size", t.name);
+  if (held && r.z) {
+    bool fits = aligned16(r.h) && aligned16(r.y) && aligned16(r.h_out) && aligned16(r.z);
+    for (const auto& t : small) fits = fits && (!t.whole || aligned16(t.p));
+    if (m > 1) fits = fits && (r.h_stride * int64_t(hs)) % 16 == 0 && (!r.y || ((r.y_stride * int64_t(es)) % 16 == 0 && (r.h_out_stride * int64_t(hs)) % 16 == 0));
+    if (r.gate && r.gate_channels && (m - 1) / r.gate_rows > 0) fits = fits && (r.gate_stride * int64_t(es)) % 16 == 0;
+    if (!fits) return fail(TB_ERR_UNSUPPORTED, "an 8-bit z needs rows and weights that are 16-byte aligned");
+  }
+  for (int j = 0; j < 3; ++j) {
+    const Rows& o = out[j];
+    if (!o.p) continue;
+    for (int k = 0; k < 2; ++k) {
+      const Rows& i = in[k];
+      if (!i.p) continue;
+      const bool same = o.p == i.p && (m == 1 || o.stride == i.stride) && o.size == i.size;
+      if (same && j == k && !(j == 1 && held)) continue;   // h_out is h, z is y: element for element
+      if (rows_share(o.p, o.bytes, o.stride, i.p, i.bytes, i.stride, m))
+        return fail(TB_ERR_INVALID_ARGUMENT, "%s overlaps %s", o.name, i.name);
+    }
+    for (int k = 0; k < j; ++k)
+      if (out[k].p && rows_share(o.p, o.bytes, o.stride, out[k].p, out[k].bytes, out[k].stride, m))
+        return fail(TB_ERR_INVALID_ARGUMENT, "%s overlaps %s", o.name, out[k].name);
+    for (const auto& t : small)
+      if (t.p && rows_share(o.p, (m - 1) * o.stride + o.bytes, 0, t.p, t.bytes, 0, 1))
+        return fail(TB_ERR_INVALID_ARGUMENT, "%s overlaps %s", o.name, t.name);
+  }
+  hipError_t e = launch_residual_norm(r, m, n, residual_scale, eps, weight_offset, post_norm != 0, dtype, h_dtype,
+                                      z_dtype, scale_type, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, "launching the residual norm");
   return ok();
 }
 

@@ -13,6 +13,12 @@
 // walks heads, so they are computed once per token, chunk and wave.  Angles
 // are fp64 products reduced to a fraction of a turn in fp64 (a position of a
 // million leaves fp32 no correct digits of the fraction), then fp32.
+//
+// With several axes (time, height, width) a token has a position on each, and a
+// pair's angle takes the one of its axis; pairs may then lie within the span of
+// their axis, (j, j + count) behind the elements of the axes before, and the
+// norm may be left out.  Which axis a pair belongs to travels with the launch
+// (two bits each), so it is checked on the host.
 #include "tb_device.h"
 #include "tb_host.h"
 
@@ -36,6 +42,22 @@ struct HeadArgs {
   const double* freq;
   float eps, offset, inv_d;
 };
+
+// What a launch with several axes knows besides; SPAN: pairs lie within the span of their axis.
+struct AxesTable {
+  int axes, norm;
+  uint32_t axis[TB_MAX_HEAD_DIM / 2 / 16];   // of pair p: two bits at 2 (p % 16) of word p / 16
+  int start[kMaxAxes], count[kMaxAxes];      // an axis's first pair and pairs, where pairs lie within its span
+};
+template <bool SPAN_> struct AxesArgs : HeadArgs {
+  static constexpr bool kAxes = true, kSpan = SPAN_;
+  AxesTable m;
+};
+struct OneAxisArgs : HeadArgs {
+  static constexpr bool kAxes = false, kSpan = false;
+};
+
+__device__ __forceinline__ int axis_of(const AxesTable& m, int p) { return int(m.axis[p >> 4] >> (2 * (p & 15)) & 3u); }
 
 // V consecutive elements as they are in memory.
 template <typename E, int V> struct Raw { uint4 v; };
@@ -93,9 +115,10 @@ __device__ __forceinline__ void store_chunk(E* p, const float (&f)[V]) {
 }
 
 // V: elements of a chunk (16 bytes, 2, or 1 for any size and alignment); UPL:
-// units (pairs of chunks) per lane; INTER: interleaved pairs.
-template <typename E, int V, int UPL, bool INTER>
-__global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs a) {
+// units (pairs of chunks) per lane; INTER: interleaved pairs; A: for one axis or
+// for several.
+template <typename E, int V, int UPL, bool INTER, typename A>
+__global__ __launch_bounds__(kThreads) void heads_kernel(A a) {
   const int l = int(threadIdx.x) & 63;
   const int64_t t = int64_t(blockIdx.x) * (kThreads / kWave) + __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
   if (t >= a.T) return;
@@ -119,6 +142,12 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs a) {
       ea[k] = 2 * a.half + 2 * (u * V - a.half);
       eb[k] = ea[k] + V;
     }
+    if constexpr (A::kSpan)
+      if (u * V < a.half) {   // (V divides every axis's pairs: a unit belongs to one)
+        const int ax = axis_of(a.m, u * V);
+        ea[k] = a.m.start[ax] + u * V;
+        eb[k] = ea[k] + a.m.count[ax];
+      }
   }
 
   // The part that owns group g (uniform), and this lane's head of the group.
@@ -142,6 +171,10 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs a) {
 
   float cs[UPL][V], sn[UPL][V];
   const double where = a.half > 0 ? double(a.pos[t]) : 0.;
+  double on[kMaxAxes] = {where, 0., 0., 0.};
+  if constexpr (A::kAxes)
+#pragma unroll
+    for (int i = 1; i < kMaxAxes; ++i) on[i] = i < a.m.axes ? double(a.pos[i * a.T + t]) : 0.;
 #pragma unroll
   for (int k = 0; k < UPL; ++k)
 #pragma unroll
@@ -150,7 +183,12 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs a) {
       cs[k][e] = 1.f;
       sn[k][e] = 0.f;
       if (p < a.half) {
-        const double turns = where * a.freq[p] * 0.15915494309189533577;   // 1 / (2 pi)
+        double at = where;
+        if constexpr (A::kAxes) {
+          const int ax = axis_of(a.m, p);
+          at = ax < 2 ? (ax == 0 ? on[0] : on[1]) : ax == 2 ? on[2] : on[3];
+        }
+        const double turns = at * a.freq[p] * 0.15915494309189533577;   // 1 / (2 pi)
         sincospif(2.f * float(turns - rint(turns)), &sn[k][e], &cs[k][e]);
       }
     }
@@ -193,7 +231,9 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs a) {
       fetch(g + 1, j);
     }
     for (int d = 1; d < a.G; d *= 2) sum += __shfl_xor(sum, d);
-    const float r = 1.f / sqrtf(sum * a.inv_d + a.eps);
+    float r = 1.f / sqrtf(sum * a.inv_d + a.eps);
+    if constexpr (A::kAxes)
+      if (!a.m.norm) r = 1.f;
     E* y = static_cast<E*>(a.part[jn].y) + t * a.part[jn].y_token_stride + h * a.part[jn].y_head_stride;
     const bool live = h < int(a.part[jn].heads);
 #pragma unroll
@@ -233,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadArgs a) {
 }
 
 template <typename E, int V>
-hipError_t heads_typed(HeadArgs& a, bool interleaved, hipStream_t stream) {
+hipError_t heads_typed(HeadArgs& a, bool interleaved, bool span, const AxesTable* axes, hipStream_t stream) {
   const int units = (a.D + 2 * V - 1) / (2 * V);
   a.G = 1;
   while (a.G < kWave && a.G < units) a.G *= 2;
@@ -245,17 +285,28 @@ hipError_t heads_typed(HeadArgs& a, bool interleaved, hipStream_t stream) {
   // unless that leaves too few waves for the chip.
   a.iters = std::max(1, int(std::min<int64_t>(groups, groups * a.T / 4096)));
   const dim3 grid(unsigned((a.T + kThreads / kWave - 1) / (kThreads / kWave)), unsigned((groups + a.iters - 1) / a.iters));
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a);
-    return hipGetLastError();
+  auto go = [&](auto units) {
+    constexpr int UPL = decltype(units)::value;
+    auto launch = [&](auto kernel, auto args) {
+      static_cast<HeadArgs&>(args) = a;
+      if constexpr (decltype(args)::kAxes) args.m = *axes;
+      hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, args);
+      return hipGetLastError();
+    };
+    if (!axes)
+      return interleaved ? launch(heads_kernel<E, V, UPL, true, OneAxisArgs>, OneAxisArgs{})
+                         : launch(heads_kernel<E, V, UPL, false, OneAxisArgs>, OneAxisArgs{});
+    if (interleaved) return launch(heads_kernel<E, V, UPL, true, AxesArgs<false>>, AxesArgs<false>{});
+    return span ? launch(heads_kernel<E, V, UPL, false, AxesArgs<true>>, AxesArgs<true>{})
+                : launch(heads_kernel<E, V, UPL, false, AxesArgs<false>>, AxesArgs<false>{});
   };
-  if (upl == 1) return interleaved ? go(heads_kernel<E, V, 1, true>) : go(heads_kernel<E, V, 1, false>);
+  if (upl == 1) return go(std::integral_constant<int, 1>{});
   if constexpr (V <= 4)
-    if (upl == 2) return interleaved ? go(heads_kernel<E, V, 2, true>) : go(heads_kernel<E, V, 2, false>);
+    if (upl == 2) return go(std::integral_constant<int, 2>{});
   if constexpr (V <= 2)
-    if (upl <= 4) return interleaved ? go(heads_kernel<E, V, 4, true>) : go(heads_kernel<E, V, 4, false>);
+    if (upl <= 4) return go(std::integral_constant<int, 4>{});
   if constexpr (V == 1)
-    if (upl <= 8) return interleaved ? go(heads_kernel<E, V, 8, true>) : go(heads_kernel<E, V, 8, false>);
+    if (upl <= 8) return go(std::integral_constant<int, 8>{});
   return hipErrorInvalidValue;
 }
 
@@ -265,8 +316,11 @@ hipError_t heads_typed(HeadArgs& a, bool interleaved, hipStream_t stream) {
 // 63 pairs rotated, one element at a time: 83 us (2.0 TB/s), against 35 for heads
 // of 256 in chunks of 16 bytes.
 template <typename E>
-bool chunks_fit(const HeadArgs& a, bool interleaved, int V) {
+bool chunks_fit(const HeadArgs& a, bool interleaved, bool span, const AxesTable* axes, int V) {
   if (a.D % V != 0 || (!interleaved && a.half % V != 0)) return false;
+  if (span)
+    for (int i = 0; i < axes->axes; ++i)
+      if (axes->count[i] % V != 0) return false;
   for (int j = 0; j < a.n; ++j) {
     const tb_head_part& p = a.part[j];
     if (p.heads > 0 &&
@@ -279,18 +333,15 @@ bool chunks_fit(const HeadArgs& a, bool interleaved, int V) {
 }
 
 template <typename E>
-hipError_t heads_vec(HeadArgs& a, bool interleaved, hipStream_t stream) {
+hipError_t heads_vec(HeadArgs& a, bool interleaved, bool span, const AxesTable* axes, hipStream_t stream) {
   constexpr int V = 16 / sizeof(E);
-  if (chunks_fit<E>(a, interleaved, V)) return heads_typed<E, V>(a, interleaved, stream);
-  return chunks_fit<E>(a, interleaved, 2) ? heads_typed<E, 2>(a, interleaved, stream)
-                                          : heads_typed<E, 1>(a, interleaved, stream);
+  if (chunks_fit<E>(a, interleaved, span, axes, V)) return heads_typed<E, V>(a, interleaved, span, axes, stream);
+  return chunks_fit<E>(a, interleaved, span, axes, 2) ? heads_typed<E, 2>(a, interleaved, span, axes, stream)
+                                                      : heads_typed<E, 1>(a, interleaved, span, axes, stream);
 }
 
-}  // namespace
-
-hipError_t launch_heads(tb_dtype dtype, int n, const tb_head_part* parts, int64_t tokens, int head_dim, int rot_dim,
-                        bool interleaved, const int64_t* positions, const double* freqs, float eps, float offset,
-                        hipStream_t stream) {
+HeadArgs head_args(int n, const tb_head_part* parts, int64_t tokens, int head_dim, int rot_dim, const int64_t* positions,
+                   const double* freqs, float eps, float offset) {
   HeadArgs a{};
   a.n = n;
   for (int j = 0; j < n; ++j) {
@@ -304,7 +355,38 @@ hipError_t launch_heads(tb_dtype dtype, int n, const tb_head_part* parts, int64_
   a.eps = eps;
   a.offset = offset;
   a.inv_d = 1.f / float(head_dim);
-  return dtype == TB_BF16 ? heads_vec<bf16_t>(a, interleaved, stream) : heads_vec<float>(a, interleaved, stream);
+  return a;
+}
+
+}  // namespace
+
+hipError_t launch_heads(tb_dtype dtype, int n, const tb_head_part* parts, int64_t tokens, int head_dim, int rot_dim,
+                        bool interleaved, const int64_t* positions, const double* freqs, float eps, float offset,
+                        hipStream_t stream) {
+  HeadArgs a = head_args(n, parts, tokens, head_dim, rot_dim, positions, freqs, eps, offset);
+  return dtype == TB_BF16 ? heads_vec<bf16_t>(a, interleaved, false, nullptr, stream)
+                          : heads_vec<float>(a, interleaved, false, nullptr, stream);
+}
+
+hipError_t launch_heads_axes(tb_dtype dtype, int n, const tb_head_part* parts, int64_t tokens, int head_dim, int rot_dim,
+                             const HeadAxes& axes, const int64_t* positions, const double* freqs, float eps, float offset,
+                             hipStream_t stream) {
+  if (axes.axes == 1 && axes.norm)   // (with one axis its span is all pairs)
+    return launch_heads(dtype, n, parts, tokens, head_dim, rot_dim, axes.pairs == TB_PAIRS_INTERLEAVED, positions, freqs,
+                        eps, offset, stream);
+  HeadArgs a = head_args(n, parts, tokens, head_dim, rot_dim, positions, freqs, eps, offset);
+  AxesTable m{};
+  m.axes = axes.axes;
+  m.norm = axes.norm;
+  for (int p = a.half - 1; p >= 0; --p) {
+    const int ax = axes.pair_axis[p];
+    m.axis[p / 16] |= uint32_t(ax) << (2 * (p % 16));
+    m.start[ax] = p;
+    ++m.count[ax];
+  }
+  const bool interleaved = axes.pairs == TB_PAIRS_INTERLEAVED, span = axes.pairs == TB_PAIRS_AXIS;
+  return dtype == TB_BF16 ? heads_vec<bf16_t>(a, interleaved, span, &m, stream)
+                          : heads_vec<float>(a, interleaved, span, &m, stream);
 }
 
 }  // namespace tb

@@ -240,9 +240,42 @@ hipError_t launch_fp8_product(const Fp8Plan& p, tb_dtype x_dtype, tb_dtype y_dty
                               const void* xs, const void* w, const void* ws, void* y, int64_t m, int64_t out_dim,
                               int64_t in_dim, char* data, hipStream_t stream);
 
+// ---- 8-bit integers with a scale per row -------------------------------------
+// x [m, in_dim] -> whole numbers and one scale per row.
+hipError_t launch_int8_rows(tb_dtype dtype, const void* x, void* q, float* scale, int64_t m, int64_t in_dim,
+                            hipStream_t stream);
+
+struct Int8Plan {
+  int tiles_m, tiles_n, S;   // tiles of 64 tokens x 128 outputs and their slices of in_dim
+  size_t off_xq, off_xs, off_part, bytes;   // Q(x), its scales and the slices' sums in the workspace
+};
+// quantised: x comes in 8 bits with its scales.
+Int8Plan plan_int8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, tb_dtype y_dtype, int cus);
+hipError_t launch_int8_product(const Int8Plan& p, tb_dtype x_dtype, tb_dtype y_dtype, const void* x, const float* xs,
+                               const void* w, const float* ws, void* y, int64_t m, int64_t out_dim, int64_t in_dim,
+                               char* data, hipStream_t stream);
+
+// ---- the norms before and after a block ----------------------------------------
+hipError_t launch_residual_norm(const tb_residual& r, int64_t m, int64_t n, float residual_scale, float eps,
+                                float weight_offset, bool post_norm, tb_dtype dtype, tb_dtype h_dtype, tb_dtype z_dtype,
+                                tb_scale scale_type, hipStream_t stream);
+
 // ---- head norms with the position rotation ----------------------------------
 hipError_t launch_heads(tb_dtype dtype, int n, const tb_head_part* parts, int64_t tokens, int head_dim, int rot_dim,
                         bool interleaved, const int64_t* positions, const double* freqs, float eps, float offset,
                         hipStream_t stream);
+
+// Rotation over several axes: whose position turns each pair, and where the pairs lie.
+constexpr int kMaxAxes = TB_MAX_AXES;
+struct HeadAxes {
+  tb_pairs pairs;
+  int axes;
+  const uint8_t* pair_axis;   // host: [rot_dim / 2]
+  bool norm;
+};
+// positions [axes][tokens].
+hipError_t launch_heads_axes(tb_dtype dtype, int n, const tb_head_part* parts, int64_t tokens, int head_dim, int rot_dim,
+                             const HeadAxes& axes, const int64_t* positions, const double* freqs, float eps, float offset,
+                             hipStream_t stream);
 
 }  // namespace tb
