@@ -964,6 +964,7 @@ tb_status tb_dense_forward_int8_workspace_size(int64_t m, int64_t out_dim, int64
   if (!valid_dtype(y_dtype)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(y_dtype));
   tb_status st = check_int8_dims(m, out_dim, in_dim, 16);
   if (st != TB_OK) return st;
+  if (!fp8_decode_fits(m, out_dim)) return fail(TB_ERR_UNSUPPORTED, "out_dim %lld is too large", (long long)out_dim);
   *bytes_out = 0;
   if (m == 0) return ok();
   int cus = 0;
@@ -980,6 +981,7 @@ tb_status tb_dense_forward_int8(const void* x, const float* x_scale, const void*
   if (!valid_dtype(y_dtype)) return fail(TB_ERR_INVALID_ARGUMENT, "unknown dtype %d", int(y_dtype));
   tb_status st = check_int8_dims(m, out_dim, in_dim, 16);
   if (st != TB_OK) return st;
+  if (!fp8_decode_fits(m, out_dim)) return fail(TB_ERR_UNSUPPORTED, "out_dim %lld is too large", (long long)out_dim);
   if (quantised ? (m > 0 && !x_scale) : x_scale != nullptr)
     return fail(TB_ERR_INVALID_ARGUMENT, "x_scale goes with an x in 8-bit integers, and only with one");
   if (m == 0) return ok();

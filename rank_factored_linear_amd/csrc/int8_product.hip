@@ -46,6 +46,193 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, in
 }
 
 // ---------------------------------------------------------------------------
+// Few tokens (m <= 64): the weight streams once, at HBM rate.
+//
+// Each workgroup owns an equal share of the output rows, in tiles of 16 that
+// need not be full: rows past its share are not loaded.  Its eight waves take
+// blocks of 128 columns in turn, so that together they read runs of a kilobyte
+// of each row; their sums meet in LDS.  Weights go from global memory straight
+// into registers, kDepth blocks ahead: each byte is used once.  A lane's 32
+// bytes of a block are two 16-byte pieces 64 apart, so that one load of a wave
+// covers 64 contiguous bytes of each of 16 rows.
+// ---------------------------------------------------------------------------
+constexpr int kDecodeWaves = 8, kDecodeThreads = kDecodeWaves * kWave;
+static_assert(kDecodeThreads == kFp8DecodeThreads, "what the launch's size is checked against");
+constexpr int kDepth = 2;   // blocks of each wave in flight
+
+struct DecodeArgs {
+  const void* x;
+  const float* xs;
+  const uint8_t* w;
+  const float* ws;
+  void* y;
+  int M, O, I, KB;
+  int wide;   // y rows can be written four outputs at a time
+  int rows;   // output rows of a workgroup
+};
+
+// Q(x) of a workgroup's own in LDS: rows 16 bytes apart beyond whole blocks, so
+// that the pieces of 16 tokens spread over the banks.
+constexpr int x_pitch(int KB) { return KB * kBlock + 16; }
+
+// All tokens (at most 16) into LDS by the whole workgroup: P2 of them side by
+// side, each by an equal share of the threads, in two passes over x (the second
+// finds it in the nearest caches).  red: kDecodeWaves words.
+template <typename XE>
+__device__ __forceinline__ void quantise_tokens(const DecodeArgs& a, uint8_t* xq, float* xs, uint32_t* red) {
+  int p2 = 1;
+  while (p2 < a.M) p2 *= 2;
+  const int G = kDecodeThreads / p2, t = int(threadIdx.x) / G, li = int(threadIdx.x) % G;
+  const XE* x = static_cast<const XE*>(a.x) + size_t(min(t, a.M - 1)) * a.I;
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int c = li * 8; c < a.I; c += G * 8) {
+    float f[8];
+    unpack8(load_frag<XE>(x + c), f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, abs_bits(f[e]));
+  }
+  for (int d = 1; d < min(G, kWave); d *= 2) top = max(top, uint32_t(__shfl_xor(int(top), d)));
+  if (G > kWave) {
+    const int w = int(threadIdx.x) / kWave, per = G / kWave;
+    red[w] = top;
+    __syncthreads();
+    for (int j = w / per * per; j < w / per * per + per; ++j) top = max(top, red[j]);
+  }
+  float stored, by;
+  int8::row_scale(top, stored, by);
+  if (t < a.M) {
+    if (li == 0) xs[t] = stored;
+    uint8_t* q = xq + t * x_pitch(a.KB);
+#pragma unroll 4
+    for (int c = li * 8; c < a.I; c += G * 8) {
+      float f[8];
+      unpack8(load_frag<XE>(x + c), f);
+      *reinterpret_cast<u32x2*>(q + c) = u32x2{int8::pack4(f[0], f[1], f[2], f[3], by), int8::pack4(f[4], f[5], f[6], f[7], by)};
+    }
+    // Columns past the last up to a whole block meet weights that were read as zeros.
+  }
+}
+
+constexpr int kLdsX = 65536;   // bytes of Q(x) a workgroup keeps
+
+// XE: uint8_t where x comes in 8 bits, else the type it is quantised from.
+template <int NT, int RT, typename XE, typename YE>
+__global__ __launch_bounds__(kDecodeThreads) void int8_decode_kernel(DecodeArgs a) {
+  constexpr bool kFused = sizeof(XE) > 1;
+  __shared__ i32x4 red[kDecodeWaves / 2][RT * NT][kWave];
+  __shared__ __attribute__((aligned(16))) uint8_t xlds[kFused ? kLdsX : 16];
+  __shared__ float xslds[16];
+  __shared__ uint32_t tops[kDecodeWaves];
+  const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave), l = int(threadIdx.x) % kWave;
+  const int lr = l & 15, kq = (l >> 4) * 16;
+  const int o0 = int(blockIdx.x) * a.rows, rows = min(a.rows, a.O - o0);   // rows <= 16 RT
+  const int nkb = (a.KB - w + kDecodeWaves - 1) / kDecodeWaves;            // this wave's blocks w, w + 8, ..
+
+  const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + size_t(o0) * a.I, int64_t(rows) * a.I);
+  const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x, kFused ? 0 : int64_t(a.M) * a.I);
+  const int row = lr * a.I + kq;
+  // Tokens past the last repeat it; their results are not stored.
+  const uint8_t* xl[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xl[n] = xlds + (kFused ? min(n * 16 + lr, a.M - 1) * x_pitch(a.KB) + kq : 0);
+
+  i32x4 acc[RT][NT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[r][n] = i32x4{0, 0, 0, 0};
+
+  struct Stage {
+    u32x4 w[2][RT], x[2][kFused ? 1 : NT];
+  } st[kDepth];
+
+  auto fetch = [&](Stage& s, int i) {
+    const int k = (w + i * kDecodeWaves) * kBlock, left = a.I - k;   // I % 16 == 0: a piece is all in or all out
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = kq + 64 * h < left ? row + 64 * h : kPast;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) s.w[h][r] = __builtin_amdgcn_raw_buffer_load_b128(rw, at, k + r * 16 * a.I, 0);
+      if constexpr (!kFused) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s.x[h][n] = __builtin_amdgcn_raw_buffer_load_b128(rx, at, k + n * 16 * a.I, 0);
+      }
+    }
+  };
+  auto multiply = [&](const Stage& s, int i) {
+    const int k = (w + i * kDecodeWaves) * kBlock;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        u32x4 x;
+        if constexpr (kFused) x = *reinterpret_cast<const u32x4*>(xl[n] + k + 64 * h);
+        else x = s.x[h][n];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[r][n] = int8::mma(s.w[h][r], x, acc[r][n]);
+      }
+  };
+
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d)
+    if (d < nkb) fetch(st[d], d);
+  // The first weight blocks are on their way while x is quantised.
+  if constexpr (kFused) {
+    quantise_tokens<XE>(a, xlds, xslds, tops);
+    __syncthreads();
+  }
+  // Rounds without a branch: a branch around a refill would make the compiler
+  // wait for the refill itself before it uses the next stage.
+  int i = 0;
+  for (; i + 2 * kDepth <= nkb; i += kDepth) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      multiply(st[d], i + d);
+      __builtin_amdgcn_sched_barrier(0);
+      fetch(st[d], i + d + kDepth);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  for (; i < nkb; i += kDepth) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      if (i + d < nkb) {
+        multiply(st[d], i + d);
+        if (i + d + kDepth < nkb) fetch(st[d], i + d + kDepth);
+      }
+    }
+  }
+
+  // The eight waves' sums: wave w + 4's into wave w's, then those four.
+  if (w >= kDecodeWaves / 2) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) red[w - kDecodeWaves / 2][r * NT + n][l] = acc[r][n];
+  }
+  __syncthreads();
+  if (w < kDecodeWaves / 2) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) red[w][r * NT + n][l] += acc[r][n];
+  }
+  __syncthreads();
+  for (int j = int(threadIdx.x); j < RT * NT * kWave; j += kDecodeThreads) {
+    const int tile = j / kWave, ln = j % kWave;
+    const int t = (tile % NT) * 16 + (ln & 15), o = (tile / NT) * 16 + (ln >> 4) * 4;
+    if (t >= a.M || o >= rows) continue;
+    i32x4 v = red[0][tile][ln];
+#pragma unroll
+    for (int q = 1; q < kDecodeWaves / 2; ++q) v += red[q][tile][ln];
+    store_out4(static_cast<YE*>(a.y) + size_t(t) * a.O + o0 + o,
+               int8::scaled(v, kFused ? xslds[t] : a.xs[t], channel_scales(a.ws, o0 + o, a.O)), rows - o,
+               a.wide && o + 4 <= rows);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // 64 tokens x 128 outputs per workgroup, four waves of 64 outputs x 32 tokens,
 // 128 columns per step.  Both operands come straight into a ring of three LDS
 // slots, two steps ahead.  Rows of 128 bytes keep their 16-byte pieces
@@ -211,18 +398,71 @@ hipError_t ring_go(const Args& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int NT, int RT, typename XE, typename YE>
+hipError_t decode_go(const DecodeArgs& a, hipStream_t stream) {
+  const dim3 grid(unsigned((a.O + a.rows - 1) / a.rows));
+  hipLaunchKernelGGL((int8_decode_kernel<NT, RT, XE, YE>), grid, dim3(kDecodeThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <int NT, typename XE, typename YE>
+hipError_t decode_rt(const DecodeArgs& a, hipStream_t stream) {
+  const int rt = (a.rows + 15) / 16;
+  if (rt == 1) return decode_go<NT, 1, XE, YE>(a, stream);
+  if (rt == 2) return decode_go<NT, 2, XE, YE>(a, stream);
+  if (rt == 3) return decode_go<NT, 3, XE, YE>(a, stream);
+  if constexpr (NT <= 2)
+    if (rt == 4) return decode_go<NT, 4, XE, YE>(a, stream);
+  if constexpr (NT == 1)
+    if (rt <= 6) return decode_go<NT, 6, XE, YE>(a, stream);
+  return hipErrorInvalidValue;
+}
+
+template <typename YE>
+hipError_t decode_x(tb_dtype x_dtype, const DecodeArgs& a, hipStream_t stream) {
+  if (x_dtype == TB_BF16) return decode_rt<1, bf16_t, YE>(a, stream);
+  if (x_dtype == TB_F32) return decode_rt<1, float, YE>(a, stream);
+  if (a.M <= 16) return decode_rt<1, uint8_t, YE>(a, stream);
+  return a.M <= 32 ? decode_rt<2, uint8_t, YE>(a, stream) : decode_rt<4, uint8_t, YE>(a, stream);
+}
+
+// Output rows of a workgroup: equal shares of the weight for every compute
+// unit (one with twice the rows of another would finish last), in as few
+// workgroups per unit as the widest kernel for these tokens allows; from 17
+// tokens on in multiples of four, so that results leave four at a time.
+int decode_rows(int64_t m, int64_t out_dim, int cus) {
+  const int most = fp8_decode_most_rows(m);
+  const int64_t k = (out_dim + int64_t(cus) * most - 1) / (int64_t(cus) * most);
+  const int64_t rows = (out_dim + cus * k - 1) / (cus * k);
+  return int(m <= 16 ? rows : (rows + 3) / 4 * 4);
+}
+
 }  // namespace
 
 Int8Plan plan_int8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, tb_dtype y_dtype, int cus) {
   Int8Plan p{};
   const int64_t KB = fp8_blocks(in_dim);
   p.S = 1;
+  p.decode = m <= kDecodeMaxTokens;
+  p.rows = p.decode ? decode_rows(m, out_dim, cus) : 0;
+  p.fused = p.decode && !quantised && m <= 16 && m * x_pitch(int(KB)) <= kLdsX;
   size_t at = 0;
-  if (!quantised) {
+  if (!quantised && !p.fused) {
     p.off_xq = at;
     at = align_up(at + size_t(m) * in_dim, 256);
     p.off_xs = at;
     at = align_up(at + size_t(m) * 4, 256);
+  }
+  if (p.decode) {
+    p.bytes = at;
+    return p;
+  }
+  p.big = ((m + 255) / 256) * ((out_dim + 255) / 256) * 2 >= cus;
+  if (p.big) {
+    p.tile = plan_int8_tiles(m, out_dim, in_dim, cus);
+    p.off_part = at;
+    p.bytes = at + p.tile.part_bytes;
+    return p;
   }
   p.tiles_n = int((out_dim + kTile - 1) / kTile);
   p.tiles_m = int((m + TM - 1) / TM);
@@ -243,16 +483,25 @@ Int8Plan plan_int8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, t
 hipError_t launch_int8_product(const Int8Plan& p, tb_dtype x_dtype, tb_dtype y_dtype, const void* x, const float* xs,
                                const void* w, const float* ws, void* y, int64_t m, int64_t out_dim, int64_t in_dim,
                                char* data, hipStream_t stream) {
-  if (x_dtype != TB_INT8) {
+  if (x_dtype != TB_INT8 && !p.fused) {
     void* xq = data + p.off_xq;
     float* sq = reinterpret_cast<float*>(data + p.off_xs);
     hipError_t e = launch_int8_rows(x_dtype, x, xq, sq, m, in_dim, stream);
     if (e != hipSuccess) return e;
     x = xq;
     xs = sq;
+    x_dtype = TB_INT8;
   }
   const size_t ys = y_dtype == TB_BF16 ? 2 : 4;
   const int wide = out_dim % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & (4 * ys - 1)) == 0;
+  if (p.decode) {
+    const DecodeArgs a{x, xs, static_cast<const uint8_t*>(w), ws, y, int(m), int(out_dim), int(in_dim),
+                       int(fp8_blocks(in_dim)), wide && p.rows % 4 == 0, p.rows};
+    return y_dtype == TB_BF16 ? decode_x<bf16_t>(x_dtype, a, stream) : decode_x<float>(x_dtype, a, stream);
+  }
+  if (p.big)
+    return launch_int8_tiles(p.tile, y_dtype, x, xs, w, ws, y, reinterpret_cast<int*>(data + p.off_part), m, out_dim,
+                             in_dim, stream);
   const Args a{static_cast<const uint8_t*>(x), xs, static_cast<const uint8_t*>(w), ws, y,
                reinterpret_cast<int*>(data + p.off_part), int(m), int(out_dim), int(in_dim), int(fp8_blocks(in_dim)),
                p.tiles_m, p.tiles_n, p.S, wide};

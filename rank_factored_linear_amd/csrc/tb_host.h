@@ -245,8 +245,25 @@ hipError_t launch_fp8_product(const Fp8Plan& p, tb_dtype x_dtype, tb_dtype y_dty
 hipError_t launch_int8_rows(tb_dtype dtype, const void* x, void* q, float* scale, int64_t m, int64_t in_dim,
                             hipStream_t stream);
 
+// The 256 x 256 tiles of the many-token kernel.
+struct Int8TilePlan {
+  int tiles_m, tiles_n;
+  int split_tiles, S;   // the first split_tiles tiles are cut into S slices of in_dim
+  int grid, xcd_major;
+  size_t part_bytes;
+};
+Int8TilePlan plan_int8_tiles(int64_t m, int64_t out_dim, int64_t in_dim, int cus);
+hipError_t launch_int8_tiles(const Int8TilePlan& p, tb_dtype y_dtype, const void* x, const float* xs, const void* w,
+                             const float* ws, void* y, int* part, int64_t m, int64_t out_dim, int64_t in_dim,
+                             hipStream_t stream);
+
 struct Int8Plan {
-  int tiles_m, tiles_n, S;   // tiles of 64 tokens x 128 outputs and their slices of in_dim
+  int decode;              // 1: the few-token kernel (m <= kDecodeMaxTokens)
+  int fused;               // x is quantised inside it
+  int rows;                // output rows of its workgroups
+  int big;                 // 1: the 256 x 256 tiles of `tile`; 0: tiles of 64 tokens x 128 outputs
+  Int8TilePlan tile;
+  int tiles_m, tiles_n, S;   // those tiles and their slices of in_dim
   size_t off_xq, off_xs, off_part, bytes;   // Q(x), its scales and the slices' sums in the workspace
 };
 // quantised: x comes in 8 bits with its scales.

@@ -241,3 +241,43 @@ def test_two_graphs_do_not_share_a_workspace():
             graphs[1].replay()
         torch.cuda.synchronize()
         assert torch.equal(ys[0], want[0]) and torch.equal(ys[1], want[1])
+
+
+def check_on_gpu(y, xq, xs, wq, ws):
+    """check_product for large results: sums below 2^53 are exact in float64, the rest as there."""
+    want = (torch.mm(xq.double(), wq.double().t().contiguous()).float() * (xs[:, None] * ws[None, :])).to(y.dtype)
+    bad = y != want
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4].tolist())
+
+
+# 256 x 256 tiles: 136 whole ones with cut edges; 128 in two slices; 264 of which the last 8 are cut into eight; three
+# columns, fewer than two steps of the reduction.  And 64 x 128 tiles in slices.
+LARGE = [(2000, 4100, 1168), (1000, 8190, 3344), (2048, 8448, 4112), (2049, 4097, 48), (1030, 12345, 144), (777, 1152, 6912),
+         (70, 5376, 21504), (130, 300, 65536)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("m,out,n", LARGE)
+def test_large_products(m, out, n, dtype):
+    print(m, out, n, dtype, flush=True)
+    xq, wq, xs, ws = ints((m, n), 1), ints((out, n), 2), scales(m, 3), scales(out, 4)
+    y = torch.full((m * out + 16,), 7.0, dtype=dtype, device=DEV)
+    tb.dense_forward_int8(xq, wq, ws, xs, out=y[8:8 + m * out].view(m, out))
+    check_on_gpu(y[8:8 + m * out].view(m, out), xq, xs, wq, ws)
+    assert (y[:8] == 7).all() and (y[8 + m * out:] == 7).all()
+
+
+def test_a_large_product_in_a_graph():
+    m, out, n = 1000, 8190, 3344
+    xs = [randn((m, n), k) for k in range(2)]
+    wq, ws = ints((out, n), 2), scales(out, 4)
+    want = [tb.dense_forward_int8(x, wq, ws) for x in xs]
+    x, graph = xs[0].clone(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = tb.dense_forward_int8(x, wq, ws)
+    for k in range(4):
+        x.copy_(xs[k % 2])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[k % 2])
+        assert torch.equal(tb.dense_forward_int8(xs[1], wq, ws), want[1])
