@@ -569,7 +569,8 @@ typedef struct tb_residual {
  *
  * h' is written to h_out, z to z in the type that the next projection takes.
  * Sums and products in fp32; h' and z are rounded once each, z from the h' that
- * is not yet rounded.
+ * is not yet rounded.  A row's results do not depend on the other rows or on how
+ * many there are.
  *   z_dtype: dtype; TB_INT8 (z_scale [m] fp32, by the rules of
  *   tb_quantize_rows_int8); or TB_E4M3 (z_scale [m, ceil(n / 128)] scale_type, by
  *   the rules of tb_quantize_activations).

@@ -772,6 +772,9 @@ def dense_forward_int8(x: torch.Tensor, Wq: torch.Tensor, w_scale: torch.Tensor,
 # ---------------------------------------------------------------------------
 
 
+_RESIDUAL = ctypes.c_int64 * 15
+
+
 @functools.lru_cache(maxsize=4096)
 def _residual_dims(h, y, weight, post_weight, gate, out_dtype, scale_dtype, norm, dtype, h_out, z, z_scale):
     """(m, n, dtype code, h code, z code, scale code, z shape and dtype, its scales' shape and dtype, rows per gate row)
@@ -844,41 +847,59 @@ def residual_norm(h: torch.Tensor, y: torch.Tensor | None = None, weight: torch.
     if out_dtype is dtype:
         out_dtype = None
     m, n, code, h_code, z_code, sc, z_kind, scales, gate_rows = _residual_dims(
-        _kind(h), _kind(y), _kind(weight), _kind(post_weight), _kind(gate), out_dtype, scale_dtype, norm, dtype, _kind(ho),
-        _kind(zo), _kind(so))
+        (h.shape, h.dtype), _kind(y), _kind(weight), _kind(post_weight), _kind(gate), out_dtype, scale_dtype, norm, dtype,
+        _kind(ho), _kind(zo), _kind(so))
     if y is None and ho is not None:
         raise TBError(TB_ERR_INVALID_ARGUMENT, "without a y there is no h' to write")
     dev = h.get_device()
     fine = dev >= 0 and dev == torch.cuda.current_device()
-    for t in (y, gate, ho, zo):
-        fine = fine and (t is None or t.get_device() == dev)
-    for t in (weight, post_weight, so, zo if scales is not None else None):
-        fine = fine and (t is None or (t.get_device() == dev and t.is_contiguous()))
+    hs, he = h.stride()
+    # tb_residual, every field eight bytes
+    yp = pp = gp = wp = hop = zp = sp = ys = hos = zs = gs = 0
+    adjacent = he == 1
+    if y is not None:
+        ys, e = y.stride()
+        yp = y.data_ptr()
+        if ho is None:
+            ho = h if not fine else torch.empty_like(h) if hs == n and adjacent else h.new_empty((m, n))
+        hos, oe = ho.stride()
+        hop = ho.data_ptr()
+        fine = fine and y.get_device() == dev and ho.get_device() == dev
+        adjacent = adjacent and e == 1 and oe == 1
+    if weight is not None:
+        wp = weight.data_ptr()
+        fine = fine and weight.get_device() == dev and weight.is_contiguous()
+    if post_weight is not None:
+        pp = post_weight.data_ptr()
+        fine = fine and post_weight.get_device() == dev and post_weight.is_contiguous()
+    channels = False
+    if gate is not None:
+        gp = gate.data_ptr()
+        gs = gate.stride(0) if gate.dim() == 2 else 0
+        fine = fine and gate.get_device() == dev
+        channels = gate.shape[-1] == n
+        adjacent = adjacent and (not channels or gate.stride(-1) == 1)
+    if z_kind is not None:
+        if zo is None and fine:
+            zo = torch.empty(z_kind[0], dtype=z_kind[1], device=h.device)
+            if scales is not None:
+                so = torch.empty(scales[0], dtype=scales[1], device=h.device)
+        if zo is not None:
+            zs, e = zo.stride()
+            zp = zo.data_ptr()
+            fine = fine and zo.get_device() == dev
+            adjacent = adjacent and e == 1
+            if so is not None:
+                sp = so.data_ptr()
+                fine = fine and so.get_device() == dev and so.is_contiguous() and zo.is_contiguous()
     if not fine:
         _need_device(h, y, gate, ho, zo)
         _need_cuda(weight, post_weight, so, zo if scales is not None else None)
-    if ho is None and y is not None:
-        ho = h.new_empty((m, n))
-    if norm and zo is None:
-        zo = h.new_empty(z_kind[0], dtype=z_kind[1])
-        if scales is not None:
-            so = h.new_empty(scales[0], dtype=scales[1])
-    hs, he = h.stride()
-    ys, ye = y.stride() if y is not None else (0, 1)
-    hos, hoe = ho.stride() if ho is not None else (0, 1)
-    zs, ze = zo.stride() if zo is not None else (0, 1)
-    gs = ge = 0
-    if gate is not None:
-        ge = gate.stride(-1)
-        gs = gate.stride(0) if gate.dim() == 2 else 0
-    channels = gate is not None and gate.shape[-1] == n and (n > 1 or gate.dim() == 1)
-    if n > 1 and (he != 1 or ye != 1 or hoe != 1 or ze != 1 or (channels and ge != 1)):
+    if not adjacent and n > 1:
         raise TBError(TB_ERR_UNSUPPORTED, "the elements of a row must be adjacent")
-    # tb_residual, every field eight bytes
-    fields = (h.data_ptr(), _ptr(y) or 0, _ptr(post_weight) or 0, _ptr(gate) or 0, _ptr(weight) or 0, _ptr(ho) or 0,
-              _ptr(zo) or 0, _ptr(so) or 0, hs, ys, hos, zs, gate_rows, gs, int(channels))
-    _check(lib.tb_residual_norm((ctypes.c_int64 * 15)(*fields), m, n, residual_scale, eps, weight_offset, post_norm, code,
-                                h_code, z_code, sc, torch._C._cuda_getCurrentRawStream(dev)))
+    _check(lib.tb_residual_norm(_RESIDUAL(h.data_ptr(), yp, pp, gp, wp, hop, zp, sp, hs, ys, hos, zs, gate_rows, gs, channels), m, n,
+                                residual_scale, eps, weight_offset, post_norm, code, h_code, z_code, sc,
+                                torch._C._cuda_getCurrentRawStream(dev)))
     return ho if y is not None else h, (zo, so) if scales is not None else zo
 
 

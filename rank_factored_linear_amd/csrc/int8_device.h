@@ -62,32 +62,71 @@ __device__ __forceinline__ f32x4 scaled(i32x4 sum, float xs, const f32x4& ws) {
 
 }  // namespace int8
 
-// Sums and maxima over the threads that hold a row: T of them, a multiple of a
-// wave; where that is more than one wave, the whole workgroup.  Every call uses
-// the other half of `lds`, so one barrier is enough: a wave writes a half again
-// only behind the barrier of the call in between, which every wave reaches after
-// it has read that half.
-constexpr int kRowMaxWaves = 16;
+// A wave's sum and maximum, in every lane: across the lanes of each sixteen by
+// cross-lane adds (neighbours, pairs, then halves of eight and sixteen mirrored,
+// which by then hold the same in every lane), across the four sixteens through
+// LDS permutes.  The order is fixed.
+template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xf, 0xf, false));
+}
+constexpr int kDppSwap1 = 0xb1, kDppSwap2 = 0x4e, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+__device__ __forceinline__ float wave_sum(float v) {
+  v += __uint_as_float(dpp<kDppSwap1>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<kDppSwap2>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<kDppHalfMirror>(__float_as_uint(v)));
+  v += __uint_as_float(dpp<kDppMirror>(__float_as_uint(v)));
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  return v;
+}
+__device__ __forceinline__ uint32_t max16(uint32_t v) {   // over sixteen lanes
+  v = max(v, dpp<kDppSwap1>(v));
+  v = max(v, dpp<kDppSwap2>(v));
+  v = max(v, dpp<kDppHalfMirror>(v));
+  return max(v, dpp<kDppMirror>(v));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max16(v);
+  v = max(v, uint32_t(__shfl_xor(int(v), 16)));
+  return max(v, uint32_t(__shfl_xor(int(v), 32)));
+}
+
+// Sums and maxima over the threads that hold a row: one wave, or the whole
+// workgroup.  Every call uses the other half of `lds`, so one barrier is enough:
+// a wave writes a half again only behind the barrier of the call in between,
+// which every wave reaches after it has read that half.
+constexpr int kRowMaxParts = 64;
 struct RowThreads {
-  float (*lds)[kRowMaxWaves];   // [2][kRowMaxWaves]
+  float (*lds)[kRowMaxParts];   // [2][kRowMaxParts]
   int waves;                    // of a row
   int half;
 
-  __device__ __forceinline__ float sum(float v) {
+  // Of CH parts, where part c of wave w is number c * waves + w of the row: each
+  // is summed over its wave, then they are added in the order of their numbers.
+  // So the sum depends on what each part is, not on how the parts are spread over
+  // threads.  CH * waves <= kRowMaxParts.
+  template <int CH>
+  __device__ __forceinline__ float sum(const float (&v)[CH]) {
+    float s[CH];
 #pragma unroll
-    for (int d = 1; d < kWave; d *= 2) v += __shfl_xor(v, d);
-    if (waves == 1) return v;
-    lds[half][threadIdx.x / kWave] = v;
+    for (int c = 0; c < CH; ++c) s[c] = wave_sum(v[c]);
+    float t = 0.f;
+    if (waves == 1) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) t += s[c];
+      return t;
+    }
+    if (threadIdx.x % kWave == 0)
+#pragma unroll
+      for (int c = 0; c < CH; ++c) lds[half][c * waves + int(threadIdx.x) / kWave] = s[c];
     __syncthreads();
-    float s = 0.f;
-    for (int w = 0; w < waves; ++w) s += lds[half][w];
+    for (int p = 0; p < CH * waves; ++p) t += lds[half][p];
     half ^= 1;
-    return s;
+    return t;
   }
   // Of fp32 bits with the sign cleared.
   __device__ __forceinline__ uint32_t max_bits(uint32_t v) {
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) v = max(v, uint32_t(__shfl_xor(int(v), d)));
+    v = wave_max(v);
     if (waves == 1) return v;
     lds[half][threadIdx.x / kWave] = __uint_as_float(v);
     __syncthreads();

@@ -15,7 +15,7 @@ namespace {
 template <typename E, int CH>
 __global__ __launch_bounds__(1024) void int8_rows_kernel(const E* __restrict__ x, uint8_t* __restrict__ q,
                                                          float* __restrict__ scale, int64_t M, int I, int T) {
-  __shared__ float lds[2][kRowMaxWaves];
+  __shared__ float lds[2][kRowMaxParts];
   RowThreads row_threads{lds, T / kWave, 0};
   const int li = int(threadIdx.x) % T, rows = int(blockDim.x) / T;
   for (int64_t row = int64_t(blockIdx.x) * rows + int(threadIdx.x) / T; row < M; row += int64_t(gridDim.x) * rows) {

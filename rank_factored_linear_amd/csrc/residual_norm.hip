@@ -10,6 +10,12 @@
 // fp32: z is made from h' as it is before it is rounded to be stored.  Each
 // element is read and written once, so the call is bound by HBM for many rows
 // and by latency (two sums over the row, one behind the other) for a few.
+//
+// h' goes past the caches: the block that reads it next has a layer's weights
+// before it, while z is read at once.  With y the z of the call before and h
+// cold, bf16: 4096 x 5376 36.3 us (4.9 TB/s) against 37.5 with both kept and 38.1
+// with both past them, 1024 x 5376 10.4 (11.5, 10.0), 4096 x 1152 9.2 (10.6, 8.9).
+// Loading the next row ahead of the present one gained nothing (40.9 -> 41.9 us).
 #include "int8_device.h"
 
 #include <algorithm>
@@ -37,30 +43,57 @@ __device__ __forceinline__ void load_v(const E* p, bool ok, float (&f)[V]) {
   }
 }
 
-template <typename E, int V>
+// PASS: written past the caches where the piece allows it.
+template <typename T, bool PASS>
+__device__ __forceinline__ void put(T* p, const T& v) {
+  if constexpr (PASS) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+template <typename E, int V, bool PASS>
 __device__ __forceinline__ void store_v(E* p, const float (&f)[V]) {
   if constexpr (V == 1) {
     *p = from_f32<E>(f[0]);
   } else if constexpr (sizeof(E) == 2) {
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    put<fp8::u32x4, PASS>(reinterpret_cast<fp8::u32x4*>(p), fp8::u32x4{pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                                                       pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7])});
   } else {
-    reinterpret_cast<f32x4*>(p)[0] = f32x4{f[0], f[1], f[2], f[3]};
-    reinterpret_cast<f32x4*>(p)[1] = f32x4{f[4], f[5], f[6], f[7]};
+    put<f32x4, PASS>(reinterpret_cast<f32x4*>(p), f32x4{f[0], f[1], f[2], f[3]});
+    put<f32x4, PASS>(reinterpret_cast<f32x4*>(p) + 1, f32x4{f[4], f[5], f[6], f[7]});
   }
+}
+
+// The sum of a row's squares.  Pieces of eight: by groups of 64 consecutive pieces
+// (a wave's), so that it does not depend on the threads that hold the row, which
+// depend on how many rows there are: a row's results are the same in any batch.
+// (The threads for single elements depend on n alone.)
+template <int V, int CH>
+__device__ __forceinline__ float square_sum(const float (&f)[CH][V], RowThreads& row_threads) {
+  constexpr int kParts = V == 8 ? CH : 1;
+  float s[kParts];
+#pragma unroll
+  for (int c = 0; c < kParts; ++c) s[c] = 0.f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[kParts == 1 ? 0 : c] = __builtin_fmaf(f[c][e], f[c][e], s[kParts == 1 ? 0 : c]);
+  return row_threads.sum<kParts>(s);
 }
 
 // What z is held in.
 enum Held { kWide, kInt8, kE4m3F32, kE4m3E8m0 };
 
 // E: type of y, the gate, the weights and a wide z; H: of the residual.  A row
-// is held in CH pieces of V elements by each of T threads.
+// is held in CH pieces of V elements by each of T threads: one wave, with four
+// rows to a workgroup, or a whole workgroup.
 template <typename E, typename H, int Z, int V, int CH>
 __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
-  __shared__ float lds[2][kRowMaxWaves];
+  // Fused where it is written so: what the compiler would choose may differ from one CH to another.
+#pragma clang fp contract(off)
+  __shared__ float lds[2][kRowMaxParts];
   RowThreads row_threads{lds, a.T / kWave, 0};
-  const int li = int(threadIdx.x) % a.T, rows = int(blockDim.x) / a.T;
-  for (int64_t row = int64_t(blockIdx.x) * rows + int(threadIdx.x) / a.T; row < a.M; row += int64_t(gridDim.x) * rows) {
+  const int li = a.T == kWave ? int(threadIdx.x) % kWave : int(threadIdx.x), rows = a.T == kWave ? int(blockDim.x) / kWave : 1;
+  for (int64_t row = int64_t(blockIdx.x) * rows + (rows > 1 ? int(threadIdx.x) / kWave : 0); row < a.M;
+       row += int64_t(gridDim.x) * rows) {
     float f[CH][V];
     {
       const H* h = static_cast<const H*>(a.r.h) + row * a.r.h_stride;
@@ -73,20 +106,13 @@ __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
     if (a.r.y) {
       float y[CH][V];
       const E* yr = static_cast<const E*>(a.r.y) + row * a.r.y_stride;
-      float sum = 0.f;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int at = (c * a.T + li) * V;
         load_v<E, V>(yr + at, at < a.n, y[c]);
       }
       float r = 1.f;
-      if (a.post) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int e = 0; e < V; ++e) sum += y[c][e] * y[c][e];
-        r = 1.f / sqrtf(row_threads.sum(sum) * a.inv_n + a.eps);
-      }
+      if (a.post) r = 1.f / sqrtf(square_sum<V, CH>(y, row_threads) * a.inv_n + a.eps);
       const E* pw = static_cast<const E*>(a.r.post_weight);
       const E* gate = static_cast<const E*>(a.r.gate);
       float whole = 1.f;   // one gate for the row
@@ -119,17 +145,12 @@ __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
           }
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) f[c][e] = f[c][e] * a.scale + y[c][e];
-        if (at < a.n) store_v<H, V>(out + at, f[c]);
+        for (int e = 0; e < V; ++e) f[c][e] = __builtin_fmaf(f[c][e], a.scale, y[c][e]);
+        if (at < a.n) store_v<H, V, true>(out + at, f[c]);
       }
     }
     if (!a.r.z) continue;
-    float sum = 0.f;
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-      for (int e = 0; e < V; ++e) sum += f[c][e] * f[c][e];
-    const float r = 1.f / sqrtf(row_threads.sum(sum) * a.inv_n + a.eps);
+    const float r = 1.f / sqrtf(square_sum<V, CH>(f, row_threads) * a.inv_n + a.eps);
     const E* wt = static_cast<const E*>(a.r.weight);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -148,7 +169,7 @@ __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int at = (c * a.T + li) * V;
-        if (at < a.n) store_v<E, V>(z + at, f[c]);
+        if (at < a.n) store_v<E, V, false>(z + at, f[c]);
       }
     } else {
       static_assert(Z == kWide || V == 8, "8-bit results are written eight at a time");
@@ -183,8 +204,7 @@ __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
 #pragma unroll
           for (int e = 0; e < V; ++e)
             if (at < a.n) top = max(top, fp8::abs_bits(f[c][e]));
-#pragma unroll
-          for (int d = 1; d < 16; d *= 2) top = max(top, uint32_t(__shfl_xor(int(top), d)));
+          top = max16(top);
           fp8::scale_t<SC> stored;
           float by;
           fp8::block_scale<SC>(top, stored, by);
@@ -202,9 +222,14 @@ __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
 
 template <typename E, typename H, int Z, int V>
 hipError_t norm_sized(NormArgs& a, hipStream_t stream) {
-  // The fewest threads that hold the row in four pieces of eight each.
+  // For many rows the fewest threads that hold a row in three pieces each (4096 x
+  // 5376: 40.9 us with 256 threads, 43.2 with 512, 51 with 1024), for fewer up to
+  // one piece each, as long as there are no more than 1024 threads for every
+  // compute unit (1 x 5376: 4.1 us with 1024 threads, 4.5 with 512, 5.5 with 256;
+  // 512 x 5376: 7.5 with 512, 7.7 with 1024).
+  constexpr int kMost = V == 8 ? 3 : 8;
   a.T = kWave;
-  while (a.T < 1024 && a.T * 32 < a.n) a.T *= 2;
+  while (a.T < 1024 && (int64_t(a.T) * V * kMost < a.n || (V == 8 && a.T * V < a.n && a.M * a.T * 2 <= 1 << 18))) a.T *= 2;
   const int ch = (a.n + V * a.T - 1) / (V * a.T), threads = a.T == kWave ? 256 : a.T, rows = threads / a.T;
   const dim3 grid(unsigned(std::min<int64_t>((a.M + rows - 1) / rows, 1 << 20)));
   auto go = [&](auto kernel) {
@@ -214,7 +239,8 @@ hipError_t norm_sized(NormArgs& a, hipStream_t stream) {
   if constexpr (V == 8) {
     if (ch == 1) return go(residual_norm_kernel<E, H, Z, V, 1>);
     if (ch == 2) return go(residual_norm_kernel<E, H, Z, V, 2>);
-    if (ch <= 4) return go(residual_norm_kernel<E, H, Z, V, 4>);
+    if (ch == 3) return go(residual_norm_kernel<E, H, Z, V, 3>);
+    if (ch == 4) return go(residual_norm_kernel<E, H, Z, V, 4>);
   } else {
     if (ch <= 8) return go(residual_norm_kernel<E, H, Z, V, 8>);
     if (ch <= 32) return go(residual_norm_kernel<E, H, Z, V, 32>);

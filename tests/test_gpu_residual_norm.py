@@ -282,3 +282,22 @@ def test_a_layer_in_8_bits(m, kind):
     h2, z = tb.residual_norm(h1, block, w, post_norm=True, gate=randn((n,), 6, 1.0), weight_offset=1.0, outs=(h1, block))
     assert h2 is h1 and z is block and h2.isfinite().all() and z.isfinite().all()
     assert abs(float(z.float().pow(2).mean()) - 1) < 0.5   # normed rows, weights near one
+
+
+@pytest.mark.parametrize("held", [None, I8, "e4m3"])
+@pytest.mark.parametrize("dtype,stream", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("n", [72, 77, 1152, 1155, 2056, 5376, 8192])
+def test_a_row_is_the_same_in_any_batch(n, dtype, stream, held):
+    """However many rows there are, which decides how many threads hold one."""
+    if held is not None and n % 8:
+        pytest.skip("8-bit results need rows of eights")
+    m = 2100
+    a = inputs(m, n, dtype, stream)
+    kw = dict(weight=a["weight"], post_weight=a["post_weight"], post_norm=True, gate=randn((n,), 5, 1.0, dtype),
+              weight_offset=1.0, residual_scale=0.7, out_dtype=tb.E4M3 if held == "e4m3" else held)
+    flat = lambda z: [z] if held is None else [t.float() for t in z]   # noqa: E731
+    ho, z = tb.residual_norm(a["h"], a["y"], **kw)
+    for first, k in ((0, 1), (7, 3), (2, 300), (1000, 600), (11, 1100)):
+        h1, z1 = tb.residual_norm(a["h"][first:first + k], a["y"][first:first + k], **kw)
+        assert torch.equal(h1, ho[first:first + k]), k
+        assert all(torch.equal(p, q[first:first + k]) for p, q in zip(flat(z1), flat(z))), k
