@@ -43,12 +43,15 @@ struct HeadArgs {
   float eps, offset, inv_d;
 };
 
-// What a launch with several axes knows besides; SPAN: pairs lie within the span of their axis.
+// What a launch with several axes knows besides.  Where each axis comes in one run
+// of pairs that is where the runs begin; else a table, read only then.
 struct AxesTable {
-  int axes, norm;
-  uint32_t axis[TB_MAX_HEAD_DIM / 2 / 16];   // of pair p: two bits at 2 (p % 16) of word p / 16
-  int start[kMaxAxes], count[kMaxAxes];      // an axis's first pair and pairs, where pairs lie within its span
+  int norm, table;
+  int begin[kMaxAxes];                       // runs: their first pairs (behind the last run: none)
+  int64_t row[kMaxAxes];                     // where the positions of a run's axis (with a table: of an axis) start
+  uint32_t axis[TB_MAX_HEAD_DIM / 2 / 16];   // table: of pair p two bits at 2 (p % 16) of word p / 16
 };
+// SPAN: pairs lie within the span of their axis (there are runs).
 template <bool SPAN_> struct AxesArgs : HeadArgs {
   static constexpr bool kAxes = true, kSpan = SPAN_;
   AxesTable m;
@@ -57,7 +60,26 @@ struct OneAxisArgs : HeadArgs {
   static constexpr bool kAxes = false, kSpan = false;
 };
 
-__device__ __forceinline__ int axis_of(const AxesTable& m, int p) { return int(m.axis[p >> 4] >> (2 * (p & 15)) & 3u); }
+// The table's words over a wave's lanes, as many as there are pairs for.
+__device__ __forceinline__ uint32_t axis_words(const AxesTable& m, int half) {
+  const int l = int(threadIdx.x) & 63;
+  uint32_t word = 0;
+#pragma unroll
+  for (int c = 0; c < TB_MAX_HEAD_DIM / 2 / 16; c += 8)
+    if (c * 16 < half)
+#pragma unroll
+      for (int k = c; k < c + 8; ++k) word = l == k ? m.axis[k] : word;
+  return word;
+}
+// One of four values, each a variable of its own: with an array, filled in a loop,
+// the compiler chooses among the elements' addresses, and the array goes to memory
+// (1009 tokens of 32 heads of 72 in fp32: 21 us against 8.3).
+static_assert(kMaxAxes == 4, "two bits name an axis");
+template <typename T> struct Four { T a, b, c, d; };
+template <typename T> __device__ __forceinline__ T pick(const Four<T>& v, int i) {
+  const T lo = i == 0 ? T(v.a) : T(v.b), hi = i == 2 ? T(v.c) : T(v.d);
+  return i < 2 ? T(lo) : T(hi);
+}
 
 // V consecutive elements as they are in memory.
 template <typename E, int V> struct Raw { uint4 v; };
@@ -129,6 +151,29 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(A a) {
   // rotated units take V elements from V u and their partners R/2 further on,
   // and the units after them 2V consecutive elements of the rest.
   int ea[UPL], eb[UPL];
+  uint32_t axes[UPL];   // of the unit's pairs, two bits each: with a table their axes, else their runs
+  Four<int> begin{};
+  if constexpr (A::kAxes) {
+    begin = Four<int>{a.m.begin[0], a.m.begin[1], a.m.begin[2], a.m.begin[3]};
+    if (a.m.table) {
+      const uint32_t words = axis_words(a.m, a.half);
+#pragma unroll
+      for (int k = 0; k < UPL; ++k) {
+        const int p0 = (lane + k * a.G) * V;   // (V divides 16: a unit's pairs lie in one word)
+        axes[k] = uint32_t(__shfl(int(words), p0 >> 4 & 63)) >> (2 * (p0 & 15));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < UPL; ++k) {
+        axes[k] = 0;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const int p = (lane + k * a.G) * V + e;
+          axes[k] |= uint32_t((p >= begin.b) + (p >= begin.c) + (p >= begin.d)) << (2 * e);
+        }
+      }
+    }
+  }
 #pragma unroll
   for (int k = 0; k < UPL; ++k) {
     const int u = lane + k * a.G;
@@ -144,9 +189,10 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(A a) {
     }
     if constexpr (A::kSpan)
       if (u * V < a.half) {   // (V divides every axis's pairs: a unit belongs to one)
-        const int ax = axis_of(a.m, u * V);
-        ea[k] = a.m.start[ax] + u * V;
-        eb[k] = ea[k] + a.m.count[ax];
+        const int r = int(axes[k] & 3u), first = pick(begin, r);
+        const Four<int> end{min(begin.b, a.half), min(begin.c, a.half), min(begin.d, a.half), a.half};
+        ea[k] = first + u * V;
+        eb[k] = ea[k] + pick(end, r) - first;
       }
   }
 
@@ -170,11 +216,14 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(A a) {
   fetch(g0, j);   // under way while the angles are computed
 
   float cs[UPL][V], sn[UPL][V];
-  const double where = a.half > 0 ? double(a.pos[t]) : 0.;
-  double on[kMaxAxes] = {where, 0., 0., 0.};
-  if constexpr (A::kAxes)
-#pragma unroll
-    for (int i = 1; i < kMaxAxes; ++i) on[i] = i < a.m.axes ? double(a.pos[i * a.T + t]) : 0.;
+  double where = 0.;
+  Four<double> on{};
+  if constexpr (A::kAxes) {   // (unused ones: the first axis's)
+    on = Four<double>{double(a.pos[a.m.row[0] + t]), double(a.pos[a.m.row[1] + t]), double(a.pos[a.m.row[2] + t]),
+                      double(a.pos[a.m.row[3] + t])};
+  } else {
+    where = a.half > 0 ? double(a.pos[t]) : 0.;
+  }
 #pragma unroll
   for (int k = 0; k < UPL; ++k)
 #pragma unroll
@@ -184,10 +233,7 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(A a) {
       sn[k][e] = 0.f;
       if (p < a.half) {
         double at = where;
-        if constexpr (A::kAxes) {
-          const int ax = axis_of(a.m, p);
-          at = ax < 2 ? (ax == 0 ? on[0] : on[1]) : ax == 2 ? on[2] : on[3];
-        }
+        if constexpr (A::kAxes) at = pick(on, int(axes[k] >> (2 * e) & 3u));
         const double turns = at * a.freq[p] * 0.15915494309189533577;   // 1 / (2 pi)
         sincospif(2.f * float(turns - rint(turns)), &sn[k][e], &cs[k][e]);
       }
@@ -230,10 +276,13 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(A a) {
       while (g + 1 >= a.first[j + 1]) ++j;
       fetch(g + 1, j);
     }
-    for (int d = 1; d < a.G; d *= 2) sum += __shfl_xor(sum, d);
-    float r = 1.f / sqrtf(sum * a.inv_d + a.eps);
-    if constexpr (A::kAxes)
-      if (!a.m.norm) r = 1.f;
+    float r = 1.f;
+    bool normed = true;
+    if constexpr (A::kAxes) normed = a.m.norm;
+    if (normed) {
+      for (int d = 1; d < a.G; d *= 2) sum += __shfl_xor(sum, d);
+      r = 1.f / sqrtf(sum * a.inv_d + a.eps);
+    }
     E* y = static_cast<E*>(a.part[jn].y) + t * a.part[jn].y_token_stride + h * a.part[jn].y_head_stride;
     const bool live = h < int(a.part[jn].heads);
 #pragma unroll
@@ -275,11 +324,20 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(A a) {
 template <typename E, int V>
 hipError_t heads_typed(HeadArgs& a, bool interleaved, bool span, const AxesTable* axes, hipStream_t stream) {
   const int units = (a.D + 2 * V - 1) / (2 * V);
-  a.G = 1;
-  while (a.G < kWave && a.G < units) a.G *= 2;
-  const int upl = (units + a.G - 1) / a.G, slots = kWave / a.G;
-  for (int j = 0; j < a.n; ++j) a.first[j + 1] = a.first[j] + int((a.part[j].heads + slots - 1) / slots);
-  const int groups = a.first[a.n];
+  // Units of a lane: as few as the lanes allow, so that a few tokens have many lanes.  Pieces of two or one element
+  // leave a lane little to do for each step of its wave: where there are many tokens and no norm, four units are taken
+  // (4096 tokens of 32 heads of 72 in bf16: 15.4 us against 19.9; but 64 of them 5.2 against 3.6).  With a norm its sums
+  // would then depend on how many tokens there are.
+  auto spread = [&](int per) {
+    a.G = 1;
+    while (a.G < kWave && a.G * per < units) a.G *= 2;
+    const int slots = kWave / a.G;
+    for (int j = 0; j < a.n; ++j) a.first[j + 1] = a.first[j] + int((a.part[j].heads + slots - 1) / slots);
+    return a.first[a.n];
+  };
+  int groups = spread(1);
+  if (V <= 2 && axes && !axes->norm && groups * a.T >= 32768) groups = spread(4);
+  const int upl = (units + a.G - 1) / a.G;
   // A wave walks all of a token's heads, computing its angles once (4096 tokens
   // of 32 + 8 heads of 256: 34 us, against 40 in two waves and 56 in ten),
   // unless that leaves too few waves for the chip.
@@ -319,8 +377,8 @@ template <typename E>
 bool chunks_fit(const HeadArgs& a, bool interleaved, bool span, const AxesTable* axes, int V) {
   if (a.D % V != 0 || (!interleaved && a.half % V != 0)) return false;
   if (span)
-    for (int i = 0; i < axes->axes; ++i)
-      if (axes->count[i] % V != 0) return false;
+    for (int b : axes->begin)   // (half is a multiple of V, too)
+      if (b < a.half && b % V != 0) return false;
   for (int j = 0; j < a.n; ++j) {
     const tb_head_part& p = a.part[j];
     if (p.heads > 0 &&
@@ -376,14 +434,25 @@ hipError_t launch_heads_axes(tb_dtype dtype, int n, const tb_head_part* parts, i
                         eps, offset, stream);
   HeadArgs a = head_args(n, parts, tokens, head_dim, rot_dim, positions, freqs, eps, offset);
   AxesTable m{};
-  m.axes = axes.axes;
   m.norm = axes.norm;
-  for (int p = a.half - 1; p >= 0; --p) {
+  unsigned seen = 0;
+  int runs = 0;
+  for (int p = 0; p < a.half; ++p) {
     const int ax = axes.pair_axis[p];
     m.axis[p / 16] |= uint32_t(ax) << (2 * (p % 16));
-    m.start[ax] = p;
-    ++m.count[ax];
+    if (p > 0 && ax == axes.pair_axis[p - 1]) continue;
+    if (seen >> ax & 1u) m.table = 1;
+    seen |= 1u << ax;
+    if (runs < kMaxAxes) {
+      m.begin[runs] = p;
+      m.row[runs] = ax * tokens;
+    }
+    ++runs;
   }
+  if (m.table)
+    for (int i = 0; i < kMaxAxes; ++i) m.row[i] = i < axes.axes ? i * tokens : 0;
+  else
+    for (int i = runs; i < kMaxAxes; ++i) m.begin[i] = 1 << 30;
   const bool interleaved = axes.pairs == TB_PAIRS_INTERLEAVED, span = axes.pairs == TB_PAIRS_AXIS;
   return dtype == TB_BF16 ? heads_vec<bf16_t>(a, interleaved, span, &m, stream)
                           : heads_vec<float>(a, interleaved, span, &m, stream);

@@ -240,8 +240,7 @@ __global__ __launch_bounds__(kDecodeThreads) void int8_decode_kernel(DecodeArgs 
 // all banks.  With few tiles the reduction is cut into S slices; each writes its
 // sums and a second launch adds and scales them.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 128, TM = 64, kSlots = 3;   // outputs and tokens of a tile; LDS slots
-constexpr int kThreads = 256;
+constexpr int kTile = 128, kSlots = 3;   // outputs of a tile; LDS slots
 
 struct Args {
   const uint8_t* x;
@@ -249,7 +248,7 @@ struct Args {
   const uint8_t* w;
   const float* ws;
   void* y;
-  int* part;   // [S][tiles][8][kThreads] pieces of four, or NULL with one slice
+  int* part;   // [S][tiles][8][4 TM] pieces of four, or NULL with one slice
   int M, O, I, KB;
   int tiles_m, tiles_n, S;
   int wide;
@@ -257,15 +256,17 @@ struct Args {
 
 // Tile u's first token and output: groups of eight token tiles walked column
 // by column, so that workgroups that run together share rows in L2.
+template <int TM>
 __device__ __forceinline__ void tile_at(const Args& a, int u, int& m0, int& n0) {
   const int per_group = 8 * a.tiles_n, first = u / per_group * 8, gs = min(a.tiles_m - first, 8), r = u % per_group;
   m0 = (first + r % gs) * TM;
   n0 = r / gs * kTile;
 }
 
-template <typename YE>
-__global__ __launch_bounds__(kThreads, 2) void int8_ring_kernel(Args a) {
-  constexpr int kX = kTile * 128, kSlot = kX + TM * 128, kLoads = 6;   // loads of a wave and step: four of W, two of x
+template <typename YE, int TM>
+__global__ __launch_bounds__(4 * TM, 2) void int8_ring_kernel(Args a) {
+  constexpr int kThreads = 4 * TM, kWaves = TM / 16, kW = 16 / kWaves;   // kW, 2: loads of W and x per wave and step
+  constexpr int kX = kTile * 128, kSlot = kX + TM * 128, kLoads = kW + 2;
   __shared__ __attribute__((aligned(16))) uint8_t ring[kSlots * kSlot];
   lds_byte* const base = (lds_byte*)ring;
   const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave), l = int(threadIdx.x) % kWave;
@@ -276,7 +277,7 @@ __global__ __launch_bounds__(kThreads, 2) void int8_ring_kernel(Args a) {
   const int at = xcd * (total / 8) + min(xcd, total % 8) + int(blockIdx.x) / 8;
   const int slice = at / tiles, tile = at % tiles;
   int m0, n0;
-  tile_at(a, tile, m0, n0);
+  tile_at<TM>(a, tile, m0, n0);
   const int kb0 = int(int64_t(slice) * a.KB / a.S), kb1 = int(int64_t(slice + 1) * a.KB / a.S);
 
   const int rows_w = min(a.O - n0, kTile), rows_x = min(a.M - m0, TM);
@@ -292,8 +293,8 @@ __global__ __launch_bounds__(kThreads, 2) void int8_ring_kernel(Args a) {
     const int ve = pe * 16 < left ? dr * a.I + pe * 16 : kPast, vo = po * 16 < left ? dr * a.I + po * 16 : kPast;
     const unsigned d = b0 + unsigned(slot * kSlot);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row8 = w * 4 + j;
+    for (int j = 0; j < kW; ++j) {
+      const int row8 = w * kW + j;
       dma(d + row8 * 1024, rw, (row8 & 1) ? vo : ve, k + row8 * 8 * a.I);
     }
 #pragma unroll
@@ -364,12 +365,13 @@ __global__ __launch_bounds__(kThreads, 2) void int8_ring_kernel(Args a) {
 
 // The slices' sums of a split product: one workgroup for the pieces of 16
 // outputs of each of a tile's waves.
-template <typename YE>
-__global__ __launch_bounds__(kThreads) void int8_join_kernel(Args a) {
+template <typename YE, int TM>
+__global__ __launch_bounds__(4 * TM) void int8_join_kernel(Args a) {
+  constexpr int kThreads = 4 * TM;
   const int w = int(threadIdx.x) / kWave, l = int(threadIdx.x) % kWave, lr = l & 15, q = l >> 4, wo = w & 1, wt = w >> 1;
   const int tile = int(blockIdx.x) >> 2, tiles = a.tiles_m * a.tiles_n, i = int(blockIdx.x) & 3;
   int m0, n0;
-  tile_at(a, tile, m0, n0);
+  tile_at<TM>(a, tile, m0, n0);
   const i32x4* p = reinterpret_cast<const i32x4*>(a.part) + (size_t(tile) * 4 + i) * 2 * kThreads + threadIdx.x;
   i32x4 sum[2];
 #pragma unroll
@@ -389,12 +391,13 @@ __global__ __launch_bounds__(kThreads) void int8_join_kernel(Args a) {
   }
 }
 
-template <typename YE>
+template <typename YE, int TM>
 hipError_t ring_go(const Args& a, hipStream_t stream) {
-  hipLaunchKernelGGL((int8_ring_kernel<YE>), dim3(unsigned(a.tiles_m * a.tiles_n * a.S)), dim3(kThreads), 0, stream, a);
+  const unsigned tiles = unsigned(a.tiles_m * a.tiles_n);
+  hipLaunchKernelGGL((int8_ring_kernel<YE, TM>), dim3(tiles * unsigned(a.S)), dim3(4 * TM), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.S == 1) return e;
-  hipLaunchKernelGGL((int8_join_kernel<YE>), dim3(unsigned(a.tiles_m * a.tiles_n * 4)), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((int8_join_kernel<YE, TM>), dim3(tiles * 4), dim3(4 * TM), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -457,24 +460,37 @@ Int8Plan plan_int8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, t
     p.bytes = at;
     return p;
   }
-  p.big = ((m + 255) / 256) * ((out_dim + 255) / 256) * 2 >= cus;
+  // 256 x 256 tiles where they busy half of the compute units, or where their slices are long (products given x, us:
+  // 512 x 5376 x 21504 77, against 86 with 128 tokens to a tile; but 512 x 8192 x 5376, slices of 10 blocks, 42 against 26).
+  p.tile = plan_int8_tiles(m, out_dim, in_dim, cus);
+  const int64_t big_tiles = int64_t(p.tile.tiles_m) * p.tile.tiles_n;
+  p.big = 2 * big_tiles >= cus || (m >= 256 && KB / p.tile.S >= 24);
   if (p.big) {
-    p.tile = plan_int8_tiles(m, out_dim, in_dim, cus);
     p.off_part = at;
     p.bytes = at + p.tile.part_bytes;
     return p;
   }
   p.tiles_n = int((out_dim + kTile - 1) / kTile);
-  p.tiles_m = int((m + TM - 1) / TM);
-  // Slices for the two workgroups that a compute unit holds, of at least four
-  // blocks, where that saves more than the second launch costs (as much as
-  // about 12 blocks).
-  const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
-  const int64_t s = std::min<int64_t>(2 * cus / tiles, KB / 4);
-  if (s > 1 && KB - KB / s >= 12) p.S = int(s);
+  // 128 tokens to a tile where long reductions of nearly full tiles busy nearly every unit in every round (512 x 8192 x
+  // 5376: 26.3 us against 31.1 with 64; 128 x 5376 x 21504 in six slices 32.0 against 37.6; but 256 x 1152 x 6912 14.0
+  // against 12.3).
+  p.tm = 128;
+  p.tiles_m = int((m + 127) / 128);
+  int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
+  p.S = int(std::max<int64_t>(1, cus / tiles));
+  const int64_t units = tiles * p.S, rounds = (units + cus - 1) / cus;
+  if (KB / p.S < 24 || units * 20 < rounds * cus * 17 || (m % 128 != 0 && m % 128 <= 64)) {
+    p.tm = 64;
+    p.tiles_m = int((m + 63) / 64);
+    tiles = int64_t(p.tiles_m) * p.tiles_n;
+    // Slices for as many workgroups as there are units, of at least four blocks, where that saves more than the second
+    // launch costs, as much as about 12 blocks (777 x 1152 x 6912: 17.7 us with two slices, 18.8 with four, 22.4 with one).
+    const int64_t s = std::min<int64_t>(cus / tiles, KB / 4);
+    p.S = s > 1 && KB - KB / s >= 12 ? int(s) : 1;
+  }
   if (p.S > 1) {
     p.off_part = at;
-    at += size_t(p.S) * tiles * kTile * TM * 4;
+    at += size_t(p.S) * tiles * kTile * p.tm * 4;
   }
   p.bytes = at;
   return p;
@@ -505,7 +521,8 @@ hipError_t launch_int8_product(const Int8Plan& p, tb_dtype x_dtype, tb_dtype y_d
   const Args a{static_cast<const uint8_t*>(x), xs, static_cast<const uint8_t*>(w), ws, y,
                reinterpret_cast<int*>(data + p.off_part), int(m), int(out_dim), int(in_dim), int(fp8_blocks(in_dim)),
                p.tiles_m, p.tiles_n, p.S, wide};
-  return y_dtype == TB_BF16 ? ring_go<bf16_t>(a, stream) : ring_go<float>(a, stream);
+  if (p.tm == 128) return y_dtype == TB_BF16 ? ring_go<bf16_t, 128>(a, stream) : ring_go<float, 128>(a, stream);
+  return y_dtype == TB_BF16 ? ring_go<bf16_t, 64>(a, stream) : ring_go<float, 64>(a, stream);
 }
 
 }  // namespace tb

@@ -146,3 +146,22 @@ def test_many_tokens_no_tokens_and_a_graph():
         torch.cuda.synchronize()
         want, = tb.head_norm_rotate([(x, w)], pos, fr, axes=axes)
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,sizes,pairs", [(72, (18, 18), "axis"), (130, (30, 33), "half"), (15, (3, 4), "interleaved"),
+                                           (250, (60, 61), "half"), (256, (32, 48, 48), "half"), (1000, (200, 201), "axis")])
+def test_a_token_is_the_same_in_any_batch(d, sizes, pairs, dtype, norm):
+    """However many tokens there are, which decides how many lanes hold a head."""
+    t, heads, axes = 4200, 8, spans(sizes)
+    x, w, fr = randn((t, heads, d), 1, 1.0, dtype), randn((d,), 2, 0.1, dtype) if norm else None, frequencies(2 * sum(sizes))
+    pos = grid(len(sizes), t)
+    kw = dict(axes=axes, interleaved=pairs == "interleaved", axis_halves=pairs == "axis", norm=norm)
+    y, = tb.head_norm_rotate([(x, w)], pos, fr, **kw)
+    at = [0, 1, 2000, 4199]
+    check(y[at], x[at], w, pos[:, at], axes, fr, pairs, norm)
+    for k in (1, 3, 70, 1100):
+        few, = tb.head_norm_rotate([(x[7:7 + k], w)], pos[:, 7:7 + k].contiguous(), fr, **kw)
+        assert torch.equal(few, y[7:7 + k]), k
+        check(few[:3], x[7:7 + min(k, 3)], w, pos[:, 7:7 + min(k, 3)], axes, fr, pairs, norm)
