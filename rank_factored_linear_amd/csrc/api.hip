@@ -969,7 +969,7 @@ tb_status tb_dense_forward_int8_workspace_size(int64_t m, int64_t out_dim, int64
   if (m == 0) return ok();
   int cus = 0;
   if (int e = device_cu_count(&cus)) return hip_fail(hipError_t(e), "querying the compute-unit count");
-  *bytes_out = plan_int8(m, out_dim, in_dim, x_dtype == TB_INT8, y_dtype, cus).bytes;
+  *bytes_out = plan_int8(m, out_dim, in_dim, x_dtype, cus).bytes;
   return ok();
 }
 
@@ -991,7 +991,7 @@ tb_status tb_dense_forward_int8(const void* x, const float* x_scale, const void*
     return fail(TB_ERR_UNSUPPORTED, "scales and y must be aligned to their element size");
   int cus = 0;
   if (int e = device_cu_count(&cus)) return hip_fail(hipError_t(e), "querying the compute-unit count");
-  const Int8Plan p = plan_int8(m, out_dim, in_dim, quantised, y_dtype, cus);
+  const Int8Plan p = plan_int8(m, out_dim, in_dim, x_dtype, cus);
   if (p.bytes > 0) {
     if (!workspace) return fail(TB_ERR_INVALID_ARGUMENT, "workspace must be non-NULL");
     if (!aligned_to(workspace, 256)) return fail(TB_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");

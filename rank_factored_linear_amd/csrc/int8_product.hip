@@ -75,23 +75,33 @@ struct DecodeArgs {
 // that the pieces of 16 tokens spread over the banks.
 constexpr int x_pitch(int KB) { return KB * kBlock + 16; }
 
-// All tokens (at most 16) into LDS by the whole workgroup: P2 of them side by
-// side, each by an equal share of the threads, in two passes over x (the second
-// finds it in the nearest caches).  red: kDecodeWaves words.
+// All tokens (at most 16) into LDS by the whole workgroup: a power of two of them
+// side by side, each by an equal share of the threads, which keep their first
+// kHeld pieces in registers between the maximum and the rounding and read any
+// others again.  red: kDecodeWaves words.
+constexpr int kHeld = 6;
 template <typename XE>
 __device__ __forceinline__ void quantise_tokens(const DecodeArgs& a, uint8_t* xq, float* xs, uint32_t* red) {
   int p2 = 1;
   while (p2 < a.M) p2 *= 2;
   const int G = kDecodeThreads / p2, t = int(threadIdx.x) / G, li = int(threadIdx.x) % G;
   const XE* x = static_cast<const XE*>(a.x) + size_t(min(t, a.M - 1)) * a.I;
+  Frag8<XE> held[kHeld];
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    const int c = (j * G + li) * 8;
+    held[j] = load_frag_if<XE>(x + c, c < a.I);
+  }
   uint32_t top = 0;
-#pragma unroll 4
-  for (int c = li * 8; c < a.I; c += G * 8) {
+  auto raise = [&](const Frag8<XE>& p) {
     float f[8];
-    unpack8(load_frag<XE>(x + c), f);
+    unpack8(p, f);
 #pragma unroll
     for (int e = 0; e < 8; ++e) top = max(top, abs_bits(f[e]));
-  }
+  };
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) raise(held[j]);
+  for (int c = (kHeld * G + li) * 8; c < a.I; c += G * 8) raise(load_frag<XE>(x + c));
   for (int d = 1; d < min(G, kWave); d *= 2) top = max(top, uint32_t(__shfl_xor(int(top), d)));
   if (G > kWave) {
     const int w = int(threadIdx.x) / kWave, per = G / kWave;
@@ -101,17 +111,19 @@ __device__ __forceinline__ void quantise_tokens(const DecodeArgs& a, uint8_t* xq
   }
   float stored, by;
   int8::row_scale(top, stored, by);
-  if (t < a.M) {
-    if (li == 0) xs[t] = stored;
-    uint8_t* q = xq + t * x_pitch(a.KB);
-#pragma unroll 4
-    for (int c = li * 8; c < a.I; c += G * 8) {
-      float f[8];
-      unpack8(load_frag<XE>(x + c), f);
-      *reinterpret_cast<u32x2*>(q + c) = u32x2{int8::pack4(f[0], f[1], f[2], f[3], by), int8::pack4(f[4], f[5], f[6], f[7], by)};
-    }
-    // Columns past the last up to a whole block meet weights that were read as zeros.
-  }
+  if (t >= a.M) return;
+  if (li == 0) xs[t] = stored;
+  uint8_t* q = xq + t * x_pitch(a.KB);
+  auto put = [&](const Frag8<XE>& p, int c) {
+    float f[8];
+    unpack8(p, f);
+    *reinterpret_cast<u32x2*>(q + c) = u32x2{int8::pack4(f[0], f[1], f[2], f[3], by), int8::pack4(f[4], f[5], f[6], f[7], by)};
+  };
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j)
+    if ((j * G + li) * 8 < a.I) put(held[j], (j * G + li) * 8);
+  for (int c = (kHeld * G + li) * 8; c < a.I; c += G * 8) put(load_frag<XE>(x + c), c);
+  // Columns past the last up to a whole block meet weights that were read as zeros.
 }
 
 constexpr int kLdsX = 65536;   // bytes of Q(x) a workgroup keeps
@@ -240,7 +252,6 @@ __global__ __launch_bounds__(kDecodeThreads) void int8_decode_kernel(DecodeArgs 
 // all banks.  With few tiles the reduction is cut into S slices; each writes its
 // sums and a second launch adds and scales them.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 128, kSlots = 3;   // outputs of a tile; LDS slots
 
 struct Args {
   const uint8_t* x;
@@ -248,7 +259,7 @@ struct Args {
   const uint8_t* w;
   const float* ws;
   void* y;
-  int* part;   // [S][tiles][8][4 TM] pieces of four, or NULL with one slice
+  int* part;   // [S][tiles][TN / 16][4 TM] pieces of four, or NULL with one slice
   int M, O, I, KB;
   int tiles_m, tiles_n, S;
   int wide;
@@ -256,17 +267,18 @@ struct Args {
 
 // Tile u's first token and output: groups of eight token tiles walked column
 // by column, so that workgroups that run together share rows in L2.
-template <int TM>
+template <int TM, int TN>
 __device__ __forceinline__ void tile_at(const Args& a, int u, int& m0, int& n0) {
   const int per_group = 8 * a.tiles_n, first = u / per_group * 8, gs = min(a.tiles_m - first, 8), r = u % per_group;
   m0 = (first + r % gs) * TM;
-  n0 = r / gs * kTile;
+  n0 = r / gs * TN;
 }
 
-template <typename YE, int TM>
-__global__ __launch_bounds__(4 * TM, 2) void int8_ring_kernel(Args a) {
-  constexpr int kThreads = 4 * TM, kWaves = TM / 16, kW = 16 / kWaves;   // kW, 2: loads of W and x per wave and step
-  constexpr int kX = kTile * 128, kSlot = kX + TM * 128, kLoads = kW + 2;
+template <typename YE, int TM, int TN, int kSlots>
+__global__ __launch_bounds__(4 * TM) void int8_ring_kernel(Args a) {
+  constexpr int kThreads = 4 * TM, kWaves = TM / 16, kW = TN / 8 / kWaves;   // kW, 2: loads of W and x per wave and step
+  constexpr int kI = TN / 32;   // W fragments of a wave
+  constexpr int kX = TN * 128, kSlot = kX + TM * 128, kLoads = kW + 2;
   __shared__ __attribute__((aligned(16))) uint8_t ring[kSlots * kSlot];
   lds_byte* const base = (lds_byte*)ring;
   const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / kWave), l = int(threadIdx.x) % kWave;
@@ -277,10 +289,10 @@ __global__ __launch_bounds__(4 * TM, 2) void int8_ring_kernel(Args a) {
   const int at = xcd * (total / 8) + min(xcd, total % 8) + int(blockIdx.x) / 8;
   const int slice = at / tiles, tile = at % tiles;
   int m0, n0;
-  tile_at<TM>(a, tile, m0, n0);
+  tile_at<TM, TN>(a, tile, m0, n0);
   const int kb0 = int(int64_t(slice) * a.KB / a.S), kb1 = int(int64_t(slice + 1) * a.KB / a.S);
 
-  const int rows_w = min(a.O - n0, kTile), rows_x = min(a.M - m0, TM);
+  const int rows_w = min(a.O - n0, TN), rows_x = min(a.M - m0, TM);
   const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + size_t(n0) * a.I, int64_t(rows_w) * a.I);
   const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x + size_t(m0) * a.I, int64_t(rows_x) * a.I);
   // Load j of an operand: row 8 (w loads + j) + l / 8, the piece that the
@@ -301,49 +313,67 @@ __global__ __launch_bounds__(4 * TM, 2) void int8_ring_kernel(Args a) {
     for (int j = 0; j < 2; ++j) dma(d + kX + (w * 2 + j) * 1024, rx, j ? vo : ve, k + (w * 2 + j) * 8 * a.I);
   };
 
-  i32x4 acc[4][2];
+  i32x4 acc[kI][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < kI; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
 
+  // A step's fragments are read while the step before multiplies.
+  struct Fragments {
+    u32x4 w[2][kI], x[2][2];
+  } f[2];
   const int sw = (lr >> 1) & 7, p0 = (q ^ sw) << 4, p1 = ((q + 4) ^ sw) << 4;
-  auto step = [&](auto which, int kb) {
-    constexpr int slot = decltype(which)::value;
-    wait_loads<kLoads>();             // block kb has landed; kb + 1 may be out
-    __builtin_amdgcn_s_barrier();     // published; and every wave has left the slot filled next
-    issue((slot + 2) % kSlots, kb + 2);
+  auto read = [&](int slot, Fragments& g) {
     const lds_byte* const s = base + slot * kSlot;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int p = h ? p1 : p0;
-      u32x4 fx[2], fw[4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) fx[j] = *reinterpret_cast<const lds_u32x4*>(s + kX + (wt * 32 + j * 16 + lr) * 128 + p);
+      for (int j = 0; j < 2; ++j) g.x[h][j] = *reinterpret_cast<const lds_u32x4*>(s + kX + (wt * 32 + j * 16 + lr) * 128 + p);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) fw[i] = *reinterpret_cast<const lds_u32x4*>(s + (wo * 64 + i * 16 + lr) * 128 + p);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = int8::mma(fw[i], fx[j], acc[i][j]);
+      for (int i = 0; i < kI; ++i)
+        g.w[h][i] = *reinterpret_cast<const lds_u32x4*>(s + (wo * (TN / 2) + i * 16 + lr) * 128 + p);
     }
   };
-  issue(0, kb0);
-  issue(1, kb0 + 1);
-  int kb = kb0;
-  for (; kb + 2 < kb1; kb += 3) {
+  auto step = [&](auto which, int kb) {
+    constexpr int U = decltype(which)::value;
+    if (kb >= kb1) return;
+    wait_loads<kLoads*(kSlots - 2)>();   // block kb + 1 has landed, those behind it may be out; this wave holds block kb
+    __builtin_amdgcn_s_barrier();        // and so does every other
+    issue(U % kSlots, kb + kSlots);
+    read((U + 1) % kSlots, f[(U + 1) & 1]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < kI; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = int8::mma(f[U & 1].w[h][i], f[U & 1].x[h][j], acc[i][j]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+#pragma unroll
+  for (int d = 0; d < kSlots; ++d) issue(d, kb0 + d);
+  wait_loads<kLoads*(kSlots - 1)>();
+  __builtin_amdgcn_s_barrier();
+  read(0, f[0]);
+  constexpr int kUnroll = kSlots % 2 ? 2 * kSlots : kSlots;
+  for (int kb = kb0; kb < kb1; kb += kUnroll) {
     step(std::integral_constant<int, 0>{}, kb);
     step(std::integral_constant<int, 1>{}, kb + 1);
     step(std::integral_constant<int, 2>{}, kb + 2);
+    step(std::integral_constant<int, 3>{}, kb + 3);
+    if constexpr (kUnroll > 4) {
+      step(std::integral_constant<int, 4>{}, kb + 4);
+      step(std::integral_constant<int, 5>{}, kb + 5);
+    }
   }
-  if (kb < kb1) step(std::integral_constant<int, 0>{}, kb);
-  if (kb + 1 < kb1) step(std::integral_constant<int, 1>{}, kb + 1);
   wait_loads<0>();   // nothing lands in LDS after the workgroup has ended
 
   if (a.S > 1) {
-    i32x4* p = reinterpret_cast<i32x4*>(a.part) + (size_t(slice) * tiles + tile) * 8 * kThreads + threadIdx.x;
+    i32x4* p = reinterpret_cast<i32x4*>(a.part) + (size_t(slice) * tiles + tile) * 2 * kI * kThreads + threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kI; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) p[(i * 2 + j) * kThreads] = acc[i][j];
     return;
@@ -354,8 +384,8 @@ __global__ __launch_bounds__(4 * TM, 2) void int8_ring_kernel(Args a) {
     if (t >= a.M) continue;
     const float xs = a.xs[t];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int o = n0 + wo * 64 + i * 16 + q * 4;
+    for (int i = 0; i < kI; ++i) {
+      const int o = n0 + wo * (TN / 2) + i * 16 + q * 4;
       if (o < a.O)
         store_out4(static_cast<YE*>(a.y) + size_t(t) * a.O + o,
                    int8::scaled(acc[i][j], xs, channel_scales(a.ws, o, a.O)), a.O - o, a.wide && o + 4 <= a.O);
@@ -365,21 +395,21 @@ __global__ __launch_bounds__(4 * TM, 2) void int8_ring_kernel(Args a) {
 
 // The slices' sums of a split product: one workgroup for the pieces of 16
 // outputs of each of a tile's waves.
-template <typename YE, int TM>
+template <typename YE, int TM, int TN>
 __global__ __launch_bounds__(4 * TM) void int8_join_kernel(Args a) {
-  constexpr int kThreads = 4 * TM;
+  constexpr int kThreads = 4 * TM, kI = TN / 32;
   const int w = int(threadIdx.x) / kWave, l = int(threadIdx.x) % kWave, lr = l & 15, q = l >> 4, wo = w & 1, wt = w >> 1;
-  const int tile = int(blockIdx.x) >> 2, tiles = a.tiles_m * a.tiles_n, i = int(blockIdx.x) & 3;
+  const int tile = int(blockIdx.x) / kI, tiles = a.tiles_m * a.tiles_n, i = int(blockIdx.x) % kI;
   int m0, n0;
-  tile_at<TM>(a, tile, m0, n0);
-  const i32x4* p = reinterpret_cast<const i32x4*>(a.part) + (size_t(tile) * 4 + i) * 2 * kThreads + threadIdx.x;
+  tile_at<TM, TN>(a, tile, m0, n0);
+  const i32x4* p = reinterpret_cast<const i32x4*>(a.part) + (size_t(tile) * kI + i) * 2 * kThreads + threadIdx.x;
   i32x4 sum[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) sum[j] = p[j * kThreads];
   for (int s = 1; s < a.S; ++s)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) sum[j] += p[(size_t(s) * tiles * 8 + j) * kThreads];
-  const int o = n0 + wo * 64 + i * 16 + q * 4;
+    for (int j = 0; j < 2; ++j) sum[j] += p[(size_t(s) * tiles * 2 * kI + j) * kThreads];
+  const int o = n0 + wo * (TN / 2) + i * 16 + q * 4;
   if (o >= a.O) return;
   const f32x4 ws = channel_scales(a.ws, o, a.O);
 #pragma unroll
@@ -391,13 +421,13 @@ __global__ __launch_bounds__(4 * TM) void int8_join_kernel(Args a) {
   }
 }
 
-template <typename YE, int TM>
+template <typename YE, int TM, int TN, int SLOTS>
 hipError_t ring_go(const Args& a, hipStream_t stream) {
   const unsigned tiles = unsigned(a.tiles_m * a.tiles_n);
-  hipLaunchKernelGGL((int8_ring_kernel<YE, TM>), dim3(tiles * unsigned(a.S)), dim3(4 * TM), 0, stream, a);
+  hipLaunchKernelGGL((int8_ring_kernel<YE, TM, TN, SLOTS>), dim3(tiles * unsigned(a.S)), dim3(4 * TM), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.S == 1) return e;
-  hipLaunchKernelGGL((int8_join_kernel<YE, TM>), dim3(tiles * 4), dim3(4 * TM), 0, stream, a);
+  hipLaunchKernelGGL((int8_join_kernel<YE, TM, TN>), dim3(tiles * (TN / 32)), dim3(4 * TM), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -440,58 +470,80 @@ int decode_rows(int64_t m, int64_t out_dim, int cus) {
   return int(m <= 16 ? rows : (rows + 3) / 4 * 4);
 }
 
+// The kernel, its tiles and its slices are those that a simple estimate finds
+// fastest (us, at 256 compute units).  It was set by the sizes below and 30 like them, from
+// 1 to 4000 tokens, x given; what it picks was the fastest of everything measured
+// there, or within 10 % of it.
+//   Few-token kernel: a start, and the rates at which a unit reads its rows (from
+//   HBM) and x (from its XCD's L2): 16 x 5376 x 5376 8.4 us (64 x 64 tiles 10.6),
+//   but 16 x 5376 x 21504 29.2 (24.4), 33 x 5376 x 21504 48 (25.2) and 64 x 21504 x 5376
+//   47 (28.6 with 64 x 128).
+//   Tiles: a start, and a step for every 128 columns; a unit's workgroups share it;
+//   no less than the weights take from HBM.  Slices are written, read and joined by
+//   another launch.  300 x 1536 x 1152 5.4 with 64 x 64, 7.9 with 64 x 128, 9.5 with 128 x
+//   128; 777 x 1152 x 6912 15.0, 17.5 in two slices, 19.0 in three; 512 x 8192 x 5376
+//   34.5, 30.9, 25.6, and 41.8 with 256 x 256 in four; 128 x 5376 x 21504 42.3 in three,
+//   37.5 in three, 32.3 in six; 2000 x 8192 x 5376 127, 106, 96 and 66 with 256 x 256.
+struct Shape { int tm, tn; double start, step; };
+constexpr Shape kShapes[] = {{64, 64, 4.2, 0.22}, {64, 128, 5.2, 0.37}, {128, 128, 5.5, 0.57}};
+
+double joined(int64_t slices, double sums) { return slices > 1 ? 3.5 + double(slices) * sums * 8 / 6e6 : 0.; }
+
+double streamed(int64_t m, int64_t out_dim, int64_t in_dim, int rows, int cus) {
+  const int64_t rounds = ((out_dim + rows - 1) / rows + cus - 1) / cus;
+  return 1. + double(rounds) * (2.5 + double(rows) * double(in_dim) / 25e3 + double(m) * double(in_dim) / 45e3);
+}
+
 }  // namespace
 
-Int8Plan plan_int8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, tb_dtype y_dtype, int cus) {
+Int8Plan plan_int8(int64_t m, int64_t out_dim, int64_t in_dim, tb_dtype x_dtype, int cus) {
   Int8Plan p{};
   const int64_t KB = fp8_blocks(in_dim);
+  const double weights = 2. + double(out_dim) * double(in_dim) / 6e6;
+  p.tile = plan_int8_tiles(m, out_dim, in_dim, cus);
+  const int64_t big_tiles = int64_t(p.tile.tiles_m) * p.tile.tiles_n, cut = p.tile.S > 1 ? p.tile.split_tiles : 0;
+  p.big = 1;
   p.S = 1;
-  p.decode = m <= kDecodeMaxTokens;
-  p.rows = p.decode ? decode_rows(m, out_dim, cus) : 0;
-  p.fused = p.decode && !quantised && m <= 16 && m * x_pitch(int(KB)) <= kLdsX;
+  double best = std::max(weights, 4. + 1.6 * (double((big_tiles - cut + cus - 1) / cus) * double(KB) +
+                                              (cut > 0 ? double((KB + p.tile.S - 1) / p.tile.S) : 0.))) +
+                joined(p.tile.S, double(cut) * 65536);
+  for (const Shape& t : kShapes) {
+    const int64_t tm = (m + t.tm - 1) / t.tm, tn = (out_dim + t.tn - 1) / t.tn;
+    for (int64_t s = 1; s <= 8 && (s == 1 || s * 4 <= KB); ++s) {
+      const double cost =
+          std::max(weights, t.start + t.step * double((tm * tn * s + cus - 1) / cus) * double((KB + s - 1) / s)) +
+          joined(s, double(m) * double(out_dim));
+      if (cost >= best) continue;
+      best = cost;
+      p.big = 0;
+      p.tm = t.tm;
+      p.tn = t.tn;
+      p.tiles_m = int(tm);
+      p.tiles_n = int(tn);
+      p.S = int(s);
+    }
+  }
+  if (m <= kDecodeMaxTokens) {
+    // Up to 16 tokens the few-token kernel can quantise x itself, which costs each workgroup a pass over x and a wait
+    // (about 1.5 us) instead of a launch (about 3.5).
+    p.rows = decode_rows(m, out_dim, cus);
+    const bool quantises = x_dtype != TB_INT8 && m <= 16 && m * x_pitch(int(KB)) <= kLdsX;
+    const double passes = 1.5 + double(m * in_dim) * (x_dtype == TB_BF16 ? 2 : 4) / 60e3, launch = x_dtype != TB_INT8 ? 3.5 : 0.;
+    p.fused = quantises && passes < launch;
+    p.decode = streamed(m, out_dim, in_dim, p.rows, cus) + (p.fused ? passes : launch) <= best + launch;
+    p.fused = p.fused && p.decode;
+  }
   size_t at = 0;
-  if (!quantised && !p.fused) {
+  if (x_dtype != TB_INT8 && !p.fused) {
     p.off_xq = at;
     at = align_up(at + size_t(m) * in_dim, 256);
     p.off_xs = at;
     at = align_up(at + size_t(m) * 4, 256);
   }
-  if (p.decode) {
-    p.bytes = at;
-    return p;
-  }
-  // 256 x 256 tiles where they busy half of the compute units, or where their slices are long (products given x, us:
-  // 512 x 5376 x 21504 77, against 86 with 128 tokens to a tile; but 512 x 8192 x 5376, slices of 10 blocks, 42 against 26).
-  p.tile = plan_int8_tiles(m, out_dim, in_dim, cus);
-  const int64_t big_tiles = int64_t(p.tile.tiles_m) * p.tile.tiles_n;
-  p.big = 2 * big_tiles >= cus || (m >= 256 && KB / p.tile.S >= 24);
-  if (p.big) {
-    p.off_part = at;
-    p.bytes = at + p.tile.part_bytes;
-    return p;
-  }
-  p.tiles_n = int((out_dim + kTile - 1) / kTile);
-  // 128 tokens to a tile where long reductions of nearly full tiles busy nearly every unit in every round (512 x 8192 x
-  // 5376: 26.3 us against 31.1 with 64; 128 x 5376 x 21504 in six slices 32.0 against 37.6; but 256 x 1152 x 6912 14.0
-  // against 12.3).
-  p.tm = 128;
-  p.tiles_m = int((m + 127) / 128);
-  int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
-  p.S = int(std::max<int64_t>(1, cus / tiles));
-  const int64_t units = tiles * p.S, rounds = (units + cus - 1) / cus;
-  if (KB / p.S < 24 || units * 20 < rounds * cus * 17 || (m % 128 != 0 && m % 128 <= 64)) {
-    p.tm = 64;
-    p.tiles_m = int((m + 63) / 64);
-    tiles = int64_t(p.tiles_m) * p.tiles_n;
-    // Slices for as many workgroups as there are units, of at least four blocks, where that saves more than the second
-    // launch costs, as much as about 12 blocks (777 x 1152 x 6912: 17.7 us with two slices, 18.8 with four, 22.4 with one).
-    const int64_t s = std::min<int64_t>(cus / tiles, KB / 4);
-    p.S = s > 1 && KB - KB / s >= 12 ? int(s) : 1;
-  }
-  if (p.S > 1) {
-    p.off_part = at;
-    at += size_t(p.S) * tiles * kTile * p.tm * 4;
-  }
+  p.off_part = at;
+  if (!p.decode && p.big) at += p.tile.part_bytes;
+  else if (!p.decode && p.S > 1)
+    at += size_t(p.S) * size_t(p.tiles_m) * size_t(p.tiles_n) * size_t(p.tm) * size_t(p.tn) * 4;
   p.bytes = at;
   return p;
 }
@@ -521,8 +573,14 @@ hipError_t launch_int8_product(const Int8Plan& p, tb_dtype x_dtype, tb_dtype y_d
   const Args a{static_cast<const uint8_t*>(x), xs, static_cast<const uint8_t*>(w), ws, y,
                reinterpret_cast<int*>(data + p.off_part), int(m), int(out_dim), int(in_dim), int(fp8_blocks(in_dim)),
                p.tiles_m, p.tiles_n, p.S, wide};
-  if (p.tm == 128) return y_dtype == TB_BF16 ? ring_go<bf16_t, 128>(a, stream) : ring_go<float, 128>(a, stream);
-  return y_dtype == TB_BF16 ? ring_go<bf16_t, 64>(a, stream) : ring_go<float, 64>(a, stream);
+  auto go = [&](auto tm, auto tn, auto slots) {
+    constexpr int TM = decltype(tm)::value, TN = decltype(tn)::value, SLOTS = decltype(slots)::value;
+    return y_dtype == TB_BF16 ? ring_go<bf16_t, TM, TN, SLOTS>(a, stream) : ring_go<float, TM, TN, SLOTS>(a, stream);
+  };
+  using std::integral_constant;
+  if (p.tm == 128) return go(integral_constant<int, 128>{}, integral_constant<int, 128>{}, integral_constant<int, 3>{});
+  if (p.tn == 128) return go(integral_constant<int, 64>{}, integral_constant<int, 128>{}, integral_constant<int, 3>{});
+  return go(integral_constant<int, 64>{}, integral_constant<int, 64>{}, integral_constant<int, 4>{});
 }
 
 }  // namespace tb

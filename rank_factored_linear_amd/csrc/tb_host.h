@@ -261,13 +261,12 @@ struct Int8Plan {
   int decode;              // 1: the few-token kernel (m <= kDecodeMaxTokens)
   int fused;               // x is quantised inside it
   int rows;                // output rows of its workgroups
-  int big;                 // 1: the 256 x 256 tiles of `tile`; 0: tiles of tm tokens x 128 outputs
+  int big;                 // else 1: the 256 x 256 tiles of `tile`; 0: tiles of tm tokens x tn outputs
   Int8TilePlan tile;
-  int tm, tiles_m, tiles_n, S;   // those tiles and their slices of in_dim
+  int tm, tn, tiles_m, tiles_n, S;   // those tiles and their slices of in_dim
   size_t off_xq, off_xs, off_part, bytes;   // Q(x), its scales and the slices' sums in the workspace
 };
-// quantised: x comes in 8 bits with its scales.
-Int8Plan plan_int8(int64_t m, int64_t out_dim, int64_t in_dim, bool quantised, tb_dtype y_dtype, int cus);
+Int8Plan plan_int8(int64_t m, int64_t out_dim, int64_t in_dim, tb_dtype x_dtype, int cus);
 hipError_t launch_int8_product(const Int8Plan& p, tb_dtype x_dtype, tb_dtype y_dtype, const void* x, const float* xs,
                                const void* w, const float* ws, void* y, int64_t m, int64_t out_dim, int64_t in_dim,
                                char* data, hipStream_t stream);

@@ -281,3 +281,22 @@ def test_a_large_product_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(y, want[k % 2])
         assert torch.equal(tb.dense_forward_int8(xs[1], wq, ws), want[1])
+
+
+# Few tokens, many outputs: every number of 16-row tiles that a workgroup of the few-token kernel holds, cut ones too.
+MANY = [(1, 24000, 144), (16, 13000, 272), (9, 11001, 80), (5, 6000, 400), (3, 40000, 64), (20, 15000, 128), (30, 10002, 256),
+        (25, 6000, 272), (40, 12000, 128), (60, 7001, 160), (64, 4000, 96), (16, 3000, 4096), (2, 5000, 32768), (7, 260, 8208)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("m,out,n", MANY)
+def test_few_tokens(m, out, n, dtype):
+    print(m, out, n, dtype, flush=True)
+    x, wq, ws = randn((m, n), 1, 2.0, dtype), ints((out, n), 2), scales(out, 4)
+    xq, xs = tb.quantize_rows_int8(x)
+    y = torch.full((m * out + 16,), 7.0, dtype=dtype, device=DEV)
+    given, within = y[8:8 + m * out].view(m, out), tb.dense_forward_int8(x, wq, ws)
+    tb.dense_forward_int8(xq, wq, ws, xs, out=given)
+    check_on_gpu(given, xq, xs, wq, ws)
+    assert torch.equal(within, given)
+    assert (y[:8] == 7).all() and (y[8 + m * out:] == 7).all()
