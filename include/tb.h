@@ -527,7 +527,7 @@ tb_status tb_quantize_rows_int8(const void *x, void *q, float *scale, int64_t m,
  *   0 <= m <= TB_FP8_MAX_TOKENS (0: nothing is enqueued), out_dim >= 1, in_dim %
  *   16 == 0 and <= TB_INT8_MAX_IN_DIM; x, wq 16-byte aligned; the matrix must fit
  *   one launch as in tb_dense_forward_fp8.  q of -128 is allowed for.  The product
- *   xs * ws of two scales must be finite in fp32.
+ *   xs * ws of two scales must be finite in fp32 (and loses digits below 2^-126).
  *   workspace: at least tb_dense_forward_int8_workspace_size() bytes, 256-byte
  *   aligned, no initial contents (NULL when 0).  Calls that may run at the same
  *   time must not share it.  The size does not grow with m everywhere: query each m.

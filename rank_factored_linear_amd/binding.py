@@ -831,10 +831,10 @@ def residual_norm(h: torch.Tensor, y: torch.Tensor | None = None, weight: torch.
 
     h' = residual_scale * h + gate * a with a = y, or y normed and weighted by post_weight (post_norm); z is h' normed and
     weighted by weight, for the next projection.  h [m, n] may be float32 beside bfloat16 blocks.  gate: [n], or [g, n] or
-    [g, 1] whose rows serve m / g rows each.  Weights count as weight + weight_offset.  z is in y's dtype (h's without a
-    y), or with out_dtype int8 or float8_e4m3fn a pair (numbers, scales) that the 8-bit projections take.  Without y h' is
-    h itself; with norm=False z is None.  outs: (h', z or None), h' may be h and z y; h, y and the outputs may be strided
-    with adjacent elements (an 8-bit z is dense)."""
+    [g, 1] whose rows serve m / g rows each.  Weights count as weight + weight_offset.  z is in y's dtype (without a y in
+    the weight's, else out_dtype's or h's), or with out_dtype int8 or float8_e4m3fn a pair (numbers, scales) that the 8-bit
+    projections take.  Without y h' is h itself; with norm=False z is None.  outs: (h', z or None), h' may be h and z y; h,
+    y and the outputs may be strided with adjacent elements (an 8-bit z is dense)."""
     ho = zo = so = None
     if outs is not None:
         ho, zo = outs
@@ -843,7 +843,12 @@ def residual_norm(h: torch.Tensor, y: torch.Tensor | None = None, weight: torch.
             scale_dtype = so.dtype
             if out_dtype is None:
                 out_dtype = zo.dtype
-    dtype = h.dtype if y is None else y.dtype
+    if y is not None:
+        dtype = y.dtype
+    elif weight is not None:
+        dtype = weight.dtype
+    else:
+        dtype = out_dtype if out_dtype in (torch.bfloat16, torch.float32) else h.dtype
     if out_dtype is dtype:
         out_dtype = None
     m, n, code, h_code, z_code, sc, z_kind, scales, gate_rows = _residual_dims(

@@ -1041,12 +1041,6 @@ tb_status tb_residual_norm(const tb_residual* tensors, int64_t m, int64_t n, flo
     const void* p;
     int64_t stride, bytes, size;   // stride and row in bytes
   };
-  const Rows in[2] = {{"h", r.h, r.h_stride * int64_t(hs), n * int64_t(hs), int64_t(hs)},
-                      {"y", r.y, r.y_stride * int64_t(es), n * int64_t(es), int64_t(es)}};
-  const int64_t scales = z_dtype == TB_INT8 ? 4 : blocks * int64_t(ss);
-  const Rows out[3] = {{"h_out", r.h_out, r.h_out_stride * int64_t(hs), n * int64_t(hs), int64_t(hs)},
-                       {"z", r.z, held ? n : r.z_stride * int64_t(es), n * zes, zes},
-                       {"z_scale", r.z ? r.z_scale : nullptr, scales, scales, int64_t(ss)}};
   if (m > 1) {
     const struct { const char* name; const void* p; int64_t s; } strides[4] = {
         {"h", r.h, r.h_stride}, {"y", r.y, r.y_stride}, {"h_out", r.h_out, r.h_out_stride},
@@ -1062,6 +1056,13 @@ tb_status tb_residual_norm(const tb_residual* tensors, int64_t m, int64_t n, flo
     if (r.gate_stride < 0) return fail(TB_ERR_INVALID_ARGUMENT, "the stride of gate is negative");
     if (r.gate_stride > (int64_t(1) << 35)) return fail(TB_ERR_UNSUPPORTED, "the stride of gate exceeds 2^35");
   }
+  const int64_t step = m > 1;   // (the strides of a single row are not used)
+  const Rows in[2] = {{"h", r.h, step * r.h_stride * int64_t(hs), n * int64_t(hs), int64_t(hs)},
+                      {"y", r.y, step * r.y_stride * int64_t(es), n * int64_t(es), int64_t(es)}};
+  const int64_t scales = z_dtype == TB_INT8 ? 4 : blocks * int64_t(ss);
+  const Rows out[3] = {{"h_out", r.h_out, step * r.h_out_stride * int64_t(hs), n * int64_t(hs), int64_t(hs)},
+                       {"z", r.z, held ? n : step * r.z_stride * int64_t(es), n * zes, zes},
+                       {"z_scale", r.z ? r.z_scale : nullptr, scales, scales, int64_t(ss)}};
   for (const Rows& t : in)
     if (!aligned_to(t.p, size_t(t.size))) return fail(TB_ERR_UNSUPPORTED, "%s must be aligned to its element size", t.name);
   for (const Rows& t : out)

@@ -55,6 +55,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, in
 // into registers, kDepth blocks ahead: each byte is used once.  A lane's 32
 // bytes of a block are two 16-byte pieces 64 apart, so that one load of a wave
 // covers 64 contiguous bytes of each of 16 rows.
+//
+// Bound by HBM for large weights and few tokens (1 x 5376 x 21504, x given: 21.6 us,
+// 5.4 TB/s; quantised in the kernel 24.9), by latency for small ones (1 x 1536 x 1152:
+// 4.2 us, quantised), and with more tokens by the reads of x, which every workgroup
+// repeats (plan_int8).
 // ---------------------------------------------------------------------------
 constexpr int kDecodeWaves = 8, kDecodeThreads = kDecodeWaves * kWave;
 static_assert(kDecodeThreads == kFp8DecodeThreads, "what the launch's size is checked against");
@@ -245,14 +250,21 @@ __global__ __launch_bounds__(kDecodeThreads) void int8_decode_kernel(DecodeArgs 
 }
 
 // ---------------------------------------------------------------------------
-// 64 tokens x 128 outputs per workgroup, four waves of 64 outputs x 32 tokens,
-// 128 columns per step.  Both operands come straight into a ring of three LDS
-// slots, two steps ahead.  Rows of 128 bytes keep their 16-byte pieces
-// XOR-swizzled by (row >> 1) & 7, so that the fragment reads of 16 rows meet
-// all banks.  With few tiles the reduction is cut into S slices; each writes its
-// sums and a second launch adds and scales them.
+// Tiles of TM tokens x TN outputs (64 or 128 each): TM / 16 waves, each 32 tokens
+// by half of the outputs, 128 columns per step.  Both operands come straight into a
+// ring of LDS slots, and a step's fragments are read while the step before
+// multiplies.  Rows of 128 bytes keep their 16-byte pieces XOR-swizzled by (row >>
+// 1) & 7, so that the fragment reads of 16 rows meet all banks.  With few tiles the
+// reduction is cut into S slices; each writes its sums and a second launch adds
+// and scales them.
+//
+// Bound by the rate at which blocks reach LDS: 64 x 64 tiles take a step of 16 KB in
+// 0.2 us (80 GB/s a unit, 20 TB/s in all), 128 x 128 tiles one of 32 KB in 0.55.  Rings
+// of three to six slots, fragments read a step ahead or not, and waves of 64 x 64 that
+// share the columns and read up to half as much from LDS all took the same within
+// 3 %, hot or cold.  777 x 1152 x 6912 15 to 16 us, 512 x 8192 x 5376 25.6 (1.76 Pop/s).
+// Which tiles a call takes: plan_int8.
 // ---------------------------------------------------------------------------
-
 struct Args {
   const uint8_t* x;
   const float* xs;
@@ -510,6 +522,7 @@ Int8Plan plan_int8(int64_t m, int64_t out_dim, int64_t in_dim, tb_dtype x_dtype,
   for (const Shape& t : kShapes) {
     const int64_t tm = (m + t.tm - 1) / t.tm, tn = (out_dim + t.tn - 1) / t.tn;
     for (int64_t s = 1; s <= 8 && (s == 1 || s * 4 <= KB); ++s) {
+      if (tm * tn * s * (4 * t.tm) >= int64_t(1) << 32) continue;   // (a launch holds fewer threads)
       const double cost =
           std::max(weights, t.start + t.step * double((tm * tn * s + cus - 1) / cus) * double((KB + s - 1) / s)) +
           joined(s, double(m) * double(out_dim));

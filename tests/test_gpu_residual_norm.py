@@ -301,3 +301,29 @@ def test_a_row_is_the_same_in_any_batch(n, dtype, stream, held):
         h1, z1 = tb.residual_norm(a["h"][first:first + k], a["y"][first:first + k], **kw)
         assert torch.equal(h1, ho[first:first + k]), k
         assert all(torch.equal(p, q[first:first + k]) for p, q in zip(flat(z1), flat(z))), k
+
+
+@pytest.mark.parametrize("n", [264, 1155, 5376])
+def test_the_first_norm_of_a_residual_in_fp32(n):
+    """No block before it: z in the type of the weight, of out_dtype, or of the residual; 8 bits from either."""
+    h, w = randn((5, n), 1, 3.0, F32), randn((n,), 2, 0.2)
+    for kw, dtype in ((dict(weight=w, weight_offset=1.0), BF), (dict(weight=w.float()), F32), (dict(), F32)):
+        got = tb.residual_norm(h, **kw)
+        assert got[1].dtype == dtype
+        check(got, h, **kw)
+    got = tb.residual_norm(h, out_dtype=BF)
+    assert got[1].dtype == BF
+    check(got, h)
+    if n % 8 == 0:
+        for weight in (w, None):
+            for kind in (I8, tb.E4M3):
+                check(tb.residual_norm(h, None, weight, out_dtype=kind), h, None, weight)
+
+
+def test_a_single_row_takes_any_stride():
+    """The stride between rows that a tensor of one row reports is not looked at."""
+    w, big = randn((264,), 3), randn((40, 264), 1)
+    h = big.as_strided((1, 264), (7, 1))
+    want = tb.residual_norm(h.contiguous(), big[3:4], w)
+    got = tb.residual_norm(h, big.as_strided((1, 264), (1 << 40, 1), 3 * 264), w)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

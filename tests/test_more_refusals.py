@@ -169,6 +169,7 @@ def test_binding_refuses_wrong_norm_operands():
     refused(lambda: f(h, y, w, outs=(h, (y.to(I8), torch.zeros(5)))), INV, "out")
     refused(lambda: f(h, y, w, out_dtype=I8, outs=(h, y)), INV, "out")
     refused(lambda: f(h, None, w.float(), outs=(h, h)), INV, "without a y")
+    refused(lambda: f(h, None, w.half()), UNS, "float16")
 
 
 # ---- rotation over several axes --------------------------------------------------------------------------------------
