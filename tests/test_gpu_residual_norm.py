@@ -327,3 +327,42 @@ def test_a_single_row_takes_any_stride():
     want = tb.residual_norm(h.contiguous(), big[3:4], w)
     got = tb.residual_norm(h, big.as_strided((1, 264), (1 << 40, 1), 3 * 264), w)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def off_by(t, offset, pad):
+    """(t's values `offset` elements into a buffer of NaN, rows `pad` apart beyond their length; the buffer)"""
+    m, n = (1, len(t)) if t.dim() == 1 else t.shape
+    big = torch.full((offset + m * (n + pad) + 8,), float("nan"), dtype=t.dtype, device=DEV)
+    view = big.as_strided((m, n), (n + pad, 1), offset)
+    view.copy_(t.view(m, n))
+    return (view[0] if t.dim() == 1 else view), big
+
+
+def untouched(big, offset, m, n, pad):
+    inside = torch.zeros(len(big), dtype=torch.bool, device=DEV)
+    inside.as_strided((m, n), (n + pad, 1), offset).fill_(True)
+    return bool(big[~inside].isnan().all()) and not bool(big[inside].isnan().any())
+
+
+@pytest.mark.parametrize("dtype,stream", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("n", [1, 5, 7, 8, 9, 10, 11, 12, 13, 14, 15, 264, 519, 1157, 5376, 5377, 8199, 16391, 24579, 32766])
+def test_rows_at_any_address(n, dtype, stream):
+    """Rows whose length, stride and address fit no 16 bytes, NaN around them: nothing of the neighbours' comes in or is
+    written, also in place, and a row has the bits that it has elsewhere."""
+    m, pad = 5, 3
+    at = dict(h=1, y=2, weight=3, post_weight=5, gate=7)
+    given = dict(inputs(m, n, dtype, stream), gate=randn((m, n), 9, 0.5, dtype))
+    kw = dict(post_norm=True, residual_scale=0.7, weight_offset=1.0)
+    v = {k: off_by(t, at[k], 0 if t.dim() == 1 else pad) for k, t in given.items()}
+    views = {k: t[0] for k, t in v.items()}
+    out_h, big_h = off_by(torch.zeros(m, n, dtype=stream), 3, pad)
+    out_z, big_z = off_by(torch.zeros(m, n, dtype=dtype), 1, pad)
+    got = tb.residual_norm(**views, **kw, outs=(out_h, out_z))
+    assert got[0] is out_h and got[1] is out_z
+    check(got, **given, **kw)
+    assert untouched(big_h, 3, m, n, pad) and untouched(big_z, 1, m, n, pad)
+    want = tb.residual_norm(**given, **kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    tb.residual_norm(**views, **kw, outs=(views["h"], views["y"]))
+    assert torch.equal(views["h"], want[0]) and torch.equal(views["y"], want[1])
+    assert untouched(v["h"][1], 1, m, n, pad) and untouched(v["y"][1], 2, m, n, pad)
