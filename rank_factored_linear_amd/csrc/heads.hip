@@ -51,14 +51,72 @@ struct AxesTable {
   int64_t row[kMaxAxes];                     // where the positions of a run's axis (with a table: of an axis) start
   uint32_t axis[TB_MAX_HEAD_DIM / 2 / 16];   // table: of pair p two bits at 2 (p % 16) of word p / 16
 };
-// SPAN: pairs lie within the span of their axis (there are runs).
-template <bool SPAN_> struct AxesArgs : HeadArgs {
+// SPAN: pairs lie within the span of their axis (there are runs).  LANES: of the
+// narrow layout (spread(1) below) whose units a lane holds, each summed by itself.
+template <bool SPAN_, int LANES_> struct AxesArgs : HeadArgs {
   static constexpr bool kAxes = true, kSpan = SPAN_;
+  static constexpr int kLanes = LANES_;
   AxesTable m;
 };
 struct OneAxisArgs : HeadArgs {
   static constexpr bool kAxes = false, kSpan = false;
+  static constexpr int kLanes = 1;
 };
+
+// What lanes l and l ^ D hold, added: within sixteen lanes by a cross-lane add (the
+// mirrors reach a lane that holds the same as l ^ D, as all smaller D are done).
+template <int CTRL> __device__ __forceinline__ float add_dpp(float v) {
+  return v + __uint_as_float(uint32_t(__builtin_amdgcn_update_dpp(0, int(__float_as_uint(v)), CTRL, 0xf, 0xf, false)));
+}
+template <int D> __device__ __forceinline__ float add_lanes(float v) {
+  if constexpr (D == 1) return add_dpp<0xb1>(v);         // neighbours
+  else if constexpr (D == 2) return add_dpp<0x4e>(v);    // pairs
+  else if constexpr (D == 4) return add_dpp<0x141>(v);   // eight mirrored
+  else if constexpr (D == 8) return add_dpp<0x140>(v);   // sixteen mirrored
+  else return v + __shfl_xor(v, D);
+}
+// N sums over G lanes each, then with one another, in the order of a tree over N G lanes.
+template <int N> __device__ __forceinline__ float sum_lanes(float (&s)[N], int G) {
+  auto step = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    if (D < G) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] = add_lanes<D>(s[i]);
+    }
+  };
+  step(std::integral_constant<int, 1>{});
+  step(std::integral_constant<int, 2>{});
+  step(std::integral_constant<int, 4>{});
+  step(std::integral_constant<int, 8>{});
+  step(std::integral_constant<int, 16>{});
+  step(std::integral_constant<int, 32>{});
+#pragma unroll
+  for (int w = 1; w < N; w *= 2)
+#pragma unroll
+    for (int i = 0; i < N; i += 2 * w) s[i] += s[i + w];
+  return s[0];
+}
+
+// With several axes which operations are fused is written out: of a a + b b either
+// product may be, and what the compiler takes differs from one number of units to
+// another, which is chosen by the number of tokens.  It is what the compiler takes for
+// one axis (in all but fp32 heads of 512 and more), where a pair's second element adds
+// the other way round if a lane of the narrow layout holds one unit of one pair.
+__device__ __forceinline__ float plus_squares(float sum, float a, float b) {
+#pragma clang fp contract(off)
+  return sum + __builtin_fmaf(a, a, b * b);
+}
+template <bool ONE_PAIR>
+__device__ __forceinline__ void turn(float x0, float x1, float c, float s, float& y0, float& y1) {
+#pragma clang fp contract(off)
+  y0 = __builtin_fmaf(x0, c, -(x1 * s));
+  y1 = ONE_PAIR ? __builtin_fmaf(x0, s, x1 * c) : __builtin_fmaf(x1, c, x0 * s);
+}
+__device__ __forceinline__ float fraction(double at, double freq) {   // of a turn
+#pragma clang fp contract(off)
+  const double turns = at * freq * 0.15915494309189533577;   // 1 / (2 pi)
+  return float(turns - rint(turns));
+}
 
 // The table's words over a wave's lanes, as many as there are pairs for.
 __device__ __forceinline__ uint32_t axis_words(const AxesTable& m, int half) {
@@ -233,9 +291,13 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(A a) {
       sn[k][e] = 0.f;
       if (p < a.half) {
         double at = where;
-        if constexpr (A::kAxes) at = pick(on, int(axes[k] >> (2 * e) & 3u));
-        const double turns = at * a.freq[p] * 0.15915494309189533577;   // 1 / (2 pi)
-        sincospif(2.f * float(turns - rint(turns)), &sn[k][e], &cs[k][e]);
+        if constexpr (A::kAxes) {
+          at = pick(on, int(axes[k] >> (2 * e) & 3u));
+          sincospif(2.f * fraction(at, a.freq[p]), &sn[k][e], &cs[k][e]);
+        } else {
+          const double turns = at * a.freq[p] * 0.15915494309189533577;   // 1 / (2 pi)
+          sincospif(2.f * float(turns - rint(turns)), &sn[k][e], &cs[k][e]);
+        }
       }
     }
 
@@ -263,13 +325,16 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(A a) {
       }
     }
     float fa[UPL][V], fb[UPL][V];
-    float sum = 0.f;
+    float sum = 0.f, sums[A::kLanes] = {};   // (sums: with several axes, of each lane of the narrow layout)
 #pragma unroll
     for (int k = 0; k < UPL; ++k) {
       widen<E, V>(ra[k], fa[k]);
       widen<E, V>(rb[k], fb[k]);
 #pragma unroll
-      for (int e = 0; e < V; ++e) sum += fa[k][e] * fa[k][e] + fb[k][e] * fb[k][e];
+      for (int e = 0; e < V; ++e) {
+        if constexpr (A::kAxes) sums[k % A::kLanes] = plus_squares(sums[k % A::kLanes], fa[k][e], fb[k][e]);
+        else sum += fa[k][e] * fa[k][e] + fb[k][e] * fb[k][e];
+      }
     }
     const int jn = j;
     if (g + 1 < g1) {   // the next group loads while this one is finished
@@ -280,8 +345,12 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(A a) {
     bool normed = true;
     if constexpr (A::kAxes) normed = a.m.norm;
     if (normed) {
-      for (int d = 1; d < a.G; d *= 2) sum += __shfl_xor(sum, d);
-      r = 1.f / sqrtf(sum * a.inv_d + a.eps);
+      if constexpr (A::kAxes) {
+        r = 1.f / sqrtf(__builtin_fmaf(sum_lanes(sums, a.G), a.inv_d, a.eps));
+      } else {
+        for (int d = 1; d < a.G; d *= 2) sum += __shfl_xor(sum, d);
+        r = 1.f / sqrtf(sum * a.inv_d + a.eps);
+      }
     }
     E* y = static_cast<E*>(a.part[jn].y) + t * a.part[jn].y_token_stride + h * a.part[jn].y_head_stride;
     const bool live = h < int(a.part[jn].heads);
@@ -301,18 +370,36 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(A a) {
         for (int e = 0; e < V; e += 2) {
           const float x0 = fa[k][e], x1 = fa[k][e + 1], c0 = cs[k][e / 2], s0 = sn[k][e / 2];
           const bool ta = p0 + e / 2 < a.half, tb = p0 + V / 2 + e / 2 < a.half;
-          fa[k][e] = ta ? x0 * c0 - x1 * s0 : x0;
-          fa[k][e + 1] = ta ? x1 * c0 + x0 * s0 : x1;
+          if constexpr (A::kAxes) {
+            float y0, y1;
+            turn<false>(x0, x1, c0, s0, y0, y1);
+            fa[k][e] = ta ? y0 : x0;
+            fa[k][e + 1] = ta ? y1 : x1;
+          } else {
+            fa[k][e] = ta ? x0 * c0 - x1 * s0 : x0;
+            fa[k][e + 1] = ta ? x1 * c0 + x0 * s0 : x1;
+          }
           const float z0 = fb[k][e], z1 = fb[k][e + 1], c1 = cs[k][V / 2 + e / 2], s1 = sn[k][V / 2 + e / 2];
-          fb[k][e] = tb ? z0 * c1 - z1 * s1 : z0;
-          fb[k][e + 1] = tb ? z1 * c1 + z0 * s1 : z1;
+          if constexpr (A::kAxes) {
+            float y0, y1;
+            turn<false>(z0, z1, c1, s1, y0, y1);
+            fb[k][e] = tb ? y0 : z0;
+            fb[k][e + 1] = tb ? y1 : z1;
+          } else {
+            fb[k][e] = tb ? z0 * c1 - z1 * s1 : z0;
+            fb[k][e + 1] = tb ? z1 * c1 + z0 * s1 : z1;
+          }
         }
       } else if (p0 < a.half) {   // V divides half: a unit is rotated as a whole
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float x0 = fa[k][e], x1 = fb[k][e];
-          fa[k][e] = x0 * cs[k][e] - x1 * sn[k][e];
-          fb[k][e] = x1 * cs[k][e] + x0 * sn[k][e];
+          if constexpr (A::kAxes) {
+            turn<V == 1 && UPL <= A::kLanes>(x0, x1, cs[k][e], sn[k][e], fa[k][e], fb[k][e]);
+          } else {
+            fa[k][e] = x0 * cs[k][e] - x1 * sn[k][e];
+            fb[k][e] = x1 * cs[k][e] + x0 * sn[k][e];
+          }
         }
       }
       if (live && ea[k] < a.D) store_chunk<E, V>(y + ea[k], fa[k]);
@@ -325,9 +412,10 @@ template <typename E, int V>
 hipError_t heads_typed(HeadArgs& a, bool interleaved, bool span, const AxesTable* axes, hipStream_t stream) {
   const int units = (a.D + 2 * V - 1) / (2 * V);
   // Units of a lane: as few as the lanes allow, so that a few tokens have many lanes.  Pieces of two or one element
-  // leave a lane little to do for each step of its wave: where there are many tokens and no norm, four units are taken
-  // (4096 tokens of 32 heads of 72 in bf16: 15.4 us against 19.9; but 64 of them 5.2 against 3.6).  With a norm its sums
-  // would then depend on how many tokens there are.
+  // leave a lane little to do for each step of its wave: with several axes and many tokens four units are taken (4096
+  // tokens of 32 + 8 heads of 180 in bf16: 27.5 us against 57.4; but 64 of 32 heads of 72, not normed, 5.2 against
+  // 3.6).  A head's squares are added in the order that the narrow layout has, so its results do not depend on how many
+  // tokens there are.
   auto spread = [&](int per) {
     a.G = 1;
     while (a.G < kWave && a.G * per < units) a.G *= 2;
@@ -336,7 +424,9 @@ hipError_t heads_typed(HeadArgs& a, bool interleaved, bool span, const AxesTable
     return a.first[a.n];
   };
   int groups = spread(1);
-  if (V <= 2 && axes && !axes->norm && groups * a.T >= 32768) groups = spread(4);
+  const int narrow = a.G;
+  if (V <= 2 && axes && groups * a.T >= 32768) groups = spread(4);
+  const int lanes = narrow / a.G;   // 1, 2 or 4
   const int upl = (units + a.G - 1) / a.G;
   // A wave walks all of a token's heads, computing its angles once (4096 tokens
   // of 32 + 8 heads of 256: 34 us, against 40 in two waves and 56 in ten),
@@ -354,9 +444,17 @@ hipError_t heads_typed(HeadArgs& a, bool interleaved, bool span, const AxesTable
     if (!axes)
       return interleaved ? launch(heads_kernel<E, V, UPL, true, OneAxisArgs>, OneAxisArgs{})
                          : launch(heads_kernel<E, V, UPL, false, OneAxisArgs>, OneAxisArgs{});
-    if (interleaved) return launch(heads_kernel<E, V, UPL, true, AxesArgs<false>>, AxesArgs<false>{});
-    return span ? launch(heads_kernel<E, V, UPL, false, AxesArgs<true>>, AxesArgs<true>{})
-                : launch(heads_kernel<E, V, UPL, false, AxesArgs<false>>, AxesArgs<false>{});
+    auto several = [&](auto lanes) {
+      constexpr int L = decltype(lanes)::value;
+      if (interleaved) return launch(heads_kernel<E, V, UPL, true, AxesArgs<false, L>>, AxesArgs<false, L>{});
+      return span ? launch(heads_kernel<E, V, UPL, false, AxesArgs<true, L>>, AxesArgs<true, L>{})
+                  : launch(heads_kernel<E, V, UPL, false, AxesArgs<false, L>>, AxesArgs<false, L>{});
+    };
+    if constexpr (V <= 2 && UPL == 4)
+      if (lanes == 4) return several(std::integral_constant<int, 4>{});
+    if constexpr (V <= 2 && (UPL == 2 || UPL == 4))
+      if (lanes == 2) return several(std::integral_constant<int, 2>{});
+    return several(std::integral_constant<int, 1>{});
   };
   if (upl == 1) return go(std::integral_constant<int, 1>{});
   if constexpr (V <= 4)

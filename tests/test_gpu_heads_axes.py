@@ -165,3 +165,23 @@ def test_a_token_is_the_same_in_any_batch(d, sizes, pairs, dtype, norm):
         few, = tb.head_norm_rotate([(x[7:7 + k], w)], pos[:, 7:7 + k].contiguous(), fr, **kw)
         assert torch.equal(few, y[7:7 + k]), k
         check(few[:3], x[7:7 + min(k, 3)], w, pos[:, 7:7 + min(k, 3)], axes, fr, pairs, norm)
+
+
+@pytest.mark.parametrize("pairs", ["half", "interleaved", "axis"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d,sizes", [(2, (1,)), (3, (1,)), (5, (1, 1)), (6, (2, 1)), (12, (2, 4)), (20, (4, 5)), (36, (9, 9)),
+                                     (66, (11, 20)), (114, (17, 13, 20)), (130, (30, 35)), (180, (20, 30, 30)), (250, (61, 62)),
+                                     (258, (64, 65)), (300, (40, 60, 50)), (516, (130, 128)), (1022, (200, 111, 200))])
+def test_every_layout_adds_a_head_in_one_order(d, sizes, dtype, pairs):
+    """Many tokens spread a head over fewer lanes than a few do: the same bits, and the oracle's values."""
+    tokens = 33000 if d <= 36 else 8200 if d < 130 else 4200   # enough of them for each head size
+    axes = spans(sizes)
+    x, w = randn((tokens, 8, d), 1, dtype=dtype), randn((d,), 2, 0.3, dtype=dtype)
+    pos, fr = grid(len(sizes), tokens), frequencies(2 * len(axes))
+    kw = dict(weight_offset=1.0, axes=axes, interleaved=pairs == "interleaved", axis_halves=pairs == "axis")
+    many, = tb.head_norm_rotate([(x, w)], pos, fr, **kw)
+    for first in (0, tokens - 7):
+        rows = slice(first, first + 7)
+        few, = tb.head_norm_rotate([(x[rows].contiguous(), w)], pos[:, rows].contiguous(), fr, **kw)
+        assert torch.equal(few, many[rows])
+        check(few, x[rows], w, pos[:, rows], axes, fr, pairs, offset=1.0)
