@@ -52,6 +52,20 @@ __device__ __forceinline__ i32x4 mma(fp8::u32x4 a, fp8::u32x4 b, i32x4 c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
 
+// Behind a group of products.  Each adds to an accumulator that an earlier one
+// has added to, and takes operands from registers that vector code may be given
+// next: the form that mfma_operand_guard is for.  The integer products have never
+// been wrong (every test of them is bit for bit), but the cause in the others is
+// not known, so they keep the same distance: products_issued waits behind the
+// group's last product.  Operands that are kept behind it have registers of their
+// own until then.
+__device__ __forceinline__ void keep(const fp8::u32x4& operand) { asm volatile("" ::"v"(operand)); }
+__device__ __forceinline__ void products_issued() {
+  __builtin_amdgcn_sched_barrier(0);
+  mfma_operand_guard();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // Four sums of one token, whose scale is xs, and their outputs' scales ws.
 __device__ __forceinline__ f32x4 scaled(i32x4 sum, float xs, const f32x4& ws) {
   f32x4 y;

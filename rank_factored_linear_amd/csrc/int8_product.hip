@@ -179,16 +179,24 @@ __global__ __launch_bounds__(kDecodeThreads) void int8_decode_kernel(DecodeArgs 
   };
   auto multiply = [&](const Stage& s, int i) {
     const int k = (w + i * kDecodeWaves) * kBlock;
+    u32x4 x[2][NT];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        u32x4 x;
-        if constexpr (kFused) x = *reinterpret_cast<const u32x4*>(xl[n] + k + 64 * h);
-        else x = s.x[h][n];
+        if constexpr (kFused) x[h][n] = *reinterpret_cast<const u32x4*>(xl[n] + k + 64 * h);
+        else x[h][n] = s.x[h][n];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) acc[r][n] = int8::mma(s.w[h][r], x, acc[r][n]);
+        for (int r = 0; r < RT; ++r) acc[r][n] = int8::mma(s.w[h][r], x[h][n], acc[r][n]);
       }
+    int8::products_issued();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) int8::keep(s.w[h][r]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) int8::keep(x[h][n]);
+    }
   };
 
 #pragma unroll
@@ -363,6 +371,9 @@ __global__ __launch_bounds__(4 * TM) void int8_ring_kernel(Args a) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = int8::mma(f[U & 1].w[h][i], f[U & 1].x[h][j], acc[i][j]);
     __builtin_amdgcn_sched_barrier(0);
+    // With the wait and the barrier, mfma_operand_guard's distance to the vector code of the next step; in 64 x 64 tiles,
+    // where it would take 3 % (777 x 1152 x 6912), they alone are enough.
+    if constexpr (TN == 128) asm volatile("s_nop 7");
   };
 #pragma unroll
   for (int d = 0; d < kSlots; ++d) issue(d, kb0 + d);
@@ -380,6 +391,7 @@ __global__ __launch_bounds__(4 * TM) void int8_ring_kernel(Args a) {
       step(std::integral_constant<int, 5>{}, kb + 5);
     }
   }
+  int8::products_issued();
   wait_loads<0>();   // nothing lands in LDS after the workgroup has ended
 
   if (a.S > 1) {

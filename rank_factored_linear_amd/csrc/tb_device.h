@@ -135,9 +135,10 @@ __device__ __forceinline__ f32x4 mma_k32(const Frag8<float>& a, const Frag8<floa
 // about: such a chain, single 16x16x32 and single 16x16x128 ops with both
 // operands overwritten 0, 1, 2, 4, 8 or 24 wait states behind the last op, in
 // workgroups of eight waves, gave 0 wrong lanes of 2.1e8 each.  So the cause is not
-// known beyond the form, and every chain of this form is guarded; ops that
-// start from zero or rotate over accumulators (16x16x128 and 32x32x16 here) have
-// never been wrong and are not.
+// known beyond the form, and every chain of this form is guarded, those of
+// 16x16x64 integer products too, which have never been wrong; ops that start from
+// zero or rotate over accumulators (16x16x128 and 32x32x16 here) have never been
+// wrong and are not.
 __device__ __forceinline__ void mfma_operand_guard() { asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: ); }
 
 // Agent-scope read-modify-write with acquire/release semantics.  On gfx950
