@@ -839,6 +839,8 @@ def residual_norm(h: torch.Tensor, y: torch.Tensor | None = None, weight: torch.
     if outs is not None:
         ho, zo = outs
         if isinstance(zo, (tuple, list)):
+            if len(zo) != 2 or zo[0] is None or zo[1] is None:
+                raise TBError(TB_ERR_INVALID_ARGUMENT, "an 8-bit z comes with its scales")
             zo, so = zo
             scale_dtype = so.dtype
             if out_dtype is None:
