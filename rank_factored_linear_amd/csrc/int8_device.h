@@ -57,10 +57,15 @@ __device__ __forceinline__ i32x4 mma(fp8::u32x4 a, fp8::u32x4 b, i32x4 c) {
 // next: the form that mfma_operand_guard is for.  The integer products have never
 // been wrong (every test of them is bit for bit), but the cause in the others is
 // not known, so they keep the same distance: products_issued waits behind the
-// group's last product.  Operands that are kept behind it have registers of their
-// own until then.
+// group's last product, which the sums passed through it keep in front of it.
+// Operands that are kept behind it have registers of their own until then.
 __device__ __forceinline__ void keep(const fp8::u32x4& operand) { asm volatile("" ::"v"(operand)); }
-__device__ __forceinline__ void products_issued() {
+template <int R, int N>
+__device__ __forceinline__ void products_issued(i32x4 (&acc)[R][N]) {
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int n = 0; n < N; ++n) asm volatile("" : "+v"(acc[r][n]));
   __builtin_amdgcn_sched_barrier(0);
   mfma_operand_guard();
   __builtin_amdgcn_sched_barrier(0);

@@ -297,7 +297,7 @@ __device__ __forceinline__ void k_run(const Args& a, const Source& s, const Lane
     k_step<1>(a, s, ln, kb + 1, kb1, fa, fb, acc);
   }
   if (kb < kb1) k_step<0>(a, s, ln, kb, kb1, fa, fb, acc);
-  int8::products_issued();
+  int8::products_issued(acc);
   wait_loads<0>();
   __syncthreads();   // the ring is free
 }

@@ -164,67 +164,83 @@ __global__ __launch_bounds__(kDecodeThreads) void int8_decode_kernel(DecodeArgs 
     u32x4 w[2][RT], x[2][kFused ? 1 : NT];
   } st[kDepth];
 
-  auto fetch = [&](Stage& s, int i) {
-    const int k = (w + i * kDecodeWaves) * kBlock, left = a.I - k;   // I % 16 == 0: a piece is all in or all out
+  // Lane offsets of the two pieces of this wave's block i.
+  struct Where { int at[2]; };
+  auto where = [&](int i) {
+    const int left = a.I - (w + i * kDecodeWaves) * kBlock;   // I % 16 == 0: a piece is all in or all out
+    return Where{{kq < left ? row : kPast, kq + 64 < left ? row + 64 : kPast}};
+  };
+  auto fetch = [&](Stage& s, const Where& p, int i) {
+    const int k = (w + i * kDecodeWaves) * kBlock;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int at = kq + 64 * h < left ? row + 64 * h : kPast;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) s.w[h][r] = __builtin_amdgcn_raw_buffer_load_b128(rw, at, k + r * 16 * a.I, 0);
+      for (int r = 0; r < RT; ++r) s.w[h][r] = __builtin_amdgcn_raw_buffer_load_b128(rw, p.at[h], k + r * 16 * a.I, 0);
       if constexpr (!kFused) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) s.x[h][n] = __builtin_amdgcn_raw_buffer_load_b128(rx, at, k + n * 16 * a.I, 0);
+        for (int n = 0; n < NT; ++n) s.x[h][n] = __builtin_amdgcn_raw_buffer_load_b128(rx, p.at[h], k + n * 16 * a.I, 0);
       }
     }
   };
+  struct Tokens { u32x4 v[2][NT]; };
   auto multiply = [&](const Stage& s, int i) {
     const int k = (w + i * kDecodeWaves) * kBlock;
-    u32x4 x[2][NT];
+    Tokens x;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        if constexpr (kFused) x[h][n] = *reinterpret_cast<const u32x4*>(xl[n] + k + 64 * h);
-        else x[h][n] = s.x[h][n];
+        if constexpr (kFused) x.v[h][n] = *reinterpret_cast<const u32x4*>(xl[n] + k + 64 * h);
+        else x.v[h][n] = s.x[h][n];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) acc[r][n] = int8::mma(s.w[h][r], x[h][n], acc[r][n]);
+        for (int r = 0; r < RT; ++r) acc[r][n] = int8::mma(s.w[h][r], x.v[h][n], acc[r][n]);
       }
-    int8::products_issued();
+    return x;
+  };
+  auto keep_tokens = [&](const Tokens& x) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int r = 0; r < RT; ++r) int8::keep(s.w[h][r]);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) int8::keep(x[h][n]);
-    }
+      for (int n = 0; n < NT; ++n) int8::keep(x.v[h][n]);
   };
 
 #pragma unroll
   for (int d = 0; d < kDepth; ++d)
-    if (d < nkb) fetch(st[d], d);
+    if (d < nkb) fetch(st[d], where(d), d);
   // The first weight blocks are on their way while x is quantised.
   if constexpr (kFused) {
     quantise_tokens<XE>(a, xlds, xslds, tops);
     __syncthreads();
   }
   // Rounds without a branch: a branch around a refill would make the compiler
-  // wait for the refill itself before it uses the next stage.
+  // wait for the refill itself before it uses the next stage.  A refill's offsets are
+  // made before the products, so that it leaves right behind them, and the guard's wait
+  // is spent while it is on its way.
   int i = 0;
   for (; i + 2 * kDepth <= nkb; i += kDepth) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
-      multiply(st[d], i + d);
+      const Where next = where(i + d + kDepth);
       __builtin_amdgcn_sched_barrier(0);
-      fetch(st[d], i + d + kDepth);
+      const Tokens x = multiply(st[d], i + d);
       __builtin_amdgcn_sched_barrier(0);
+      fetch(st[d], next, i + d + kDepth);
+      int8::products_issued(acc);
+      if constexpr (kFused) keep_tokens(x);
     }
   }
   for (; i < nkb; i += kDepth) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
       if (i + d < nkb) {
-        multiply(st[d], i + d);
-        if (i + d + kDepth < nkb) fetch(st[d], i + d + kDepth);
+        const Tokens x = multiply(st[d], i + d);
+        int8::products_issued(acc);
+        keep_tokens(x);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < RT; ++r) int8::keep(st[d].w[h][r]);
+        if (i + d + kDepth < nkb) fetch(st[d], where(i + d + kDepth), i + d + kDepth);
       }
     }
   }
@@ -371,9 +387,9 @@ __global__ __launch_bounds__(4 * TM) void int8_ring_kernel(Args a) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = int8::mma(f[U & 1].w[h][i], f[U & 1].x[h][j], acc[i][j]);
     __builtin_amdgcn_sched_barrier(0);
-    // With the wait and the barrier, mfma_operand_guard's distance to the vector code of the next step; in 64 x 64 tiles,
-    // where it would take 3 % (777 x 1152 x 6912), they alone are enough.
-    if constexpr (TN == 128) asm volatile("s_nop 7");
+    // With the wait and the barrier, mfma_operand_guard's distance to the vector code of the next step; in 64 x 64 tiles
+    // they alone are enough (eight states more take 3 % there: 777 x 1152 x 6912).
+    if constexpr (TN == 128) asm volatile("s_nop 3");
   };
 #pragma unroll
   for (int d = 0; d < kSlots; ++d) issue(d, kb0 + d);
@@ -391,7 +407,7 @@ __global__ __launch_bounds__(4 * TM) void int8_ring_kernel(Args a) {
       step(std::integral_constant<int, 5>{}, kb + 5);
     }
   }
-  int8::products_issued();
+  int8::products_issued(acc);
   wait_loads<0>();   // nothing lands in LDS after the workgroup has ended
 
   if (a.S > 1) {
