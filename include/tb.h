@@ -577,12 +577,13 @@ typedef struct tb_residual {
  *   0 <= m <= TB_FP8_MAX_TOKENS (0: nothing is enqueued), 1 <= n <=
  *   TB_MAX_NORM_DIM; an 8-bit z needs n % 8 == 0, rows (the gate's too where it has
  *   channels) and weights 16-byte aligned.  A wide z takes any n and element
- *   alignment; rows, weights and strides in multiples of 16 bytes are read and
- *   written in pieces of eight elements, everything else element by element, more
- *   slowly.  Strides of tensors with several rows are 0 .. 2^35, those of outputs
- *   >= n.  h_out may be h, and a z in dtype may be y (same strides); other
- *   overlaps of an output with another tensor are refused, but for rows that
- *   interleave at one stride.  Without y there is no gate, post_norm or residual
+ *   alignment: 16-byte pieces where n and the strides are multiples of eight and
+ *   rows and weights 16-byte aligned; else the same pieces at element alignment
+ *   (1.1 to 2.6 times as long, the most for the longest rows), and rows of fewer
+ *   than eight elements one by one.  Strides of tensors with several rows are
+ *   0 .. 2^35, those of outputs >= n.  h_out may be h, and a z in dtype may be y
+ *   (same strides); other overlaps of an output with another tensor are refused,
+ *   but for rows that interleave at one stride.  Without y there is no gate, post_norm or residual
  *   scale (1).  eps >= 0; rows must be small enough for their squares to sum up in
  *   fp32 (and, where eps is 0, large enough for the sum not to vanish).
  *   Errors: TB_ERR_INVALID_ARGUMENT, TB_ERR_UNSUPPORTED, TB_ERR_HIP.
