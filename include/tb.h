@@ -583,9 +583,10 @@ typedef struct tb_residual {
  *   than eight elements one by one.  Strides of tensors with several rows are
  *   0 .. 2^35, those of outputs >= n.  h_out may be h, and a z in dtype may be y
  *   (same strides); other overlaps of an output with another tensor are refused,
- *   but for rows that interleave at one stride.  Without y there is no gate, post_norm or residual
- *   scale (1).  eps >= 0; rows must be small enough for their squares to sum up in
- *   fp32 (and, where eps is 0, large enough for the sum not to vanish).
+ *   but for rows that interleave at one stride.  Without y there is no gate,
+ *   post_norm or residual scale (1).  eps >= 0; rows must be small enough for their
+ *   squares to sum up in fp32 (and, where eps is 0, large enough for the sum not to
+ *   vanish).
  *   Errors: TB_ERR_INVALID_ARGUMENT, TB_ERR_UNSUPPORTED, TB_ERR_HIP.
  */
 tb_status tb_residual_norm(const tb_residual *tensors, int64_t m, int64_t n, float residual_scale, float eps,

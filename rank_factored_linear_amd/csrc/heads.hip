@@ -12,7 +12,10 @@
 // works on one token and keeps its cosines and sines in registers while it
 // walks heads, so they are computed once per token, chunk and wave.  Angles
 // are fp64 products reduced to a fraction of a turn in fp64 (a position of a
-// million leaves fp32 no correct digits of the fraction), then fp32.
+// million leaves fp32 no correct digits of the fraction), then fp32, which is what
+// sincospif takes: that rounds the fraction by up to 2^-26 of a turn, so a cosine or
+// sine is off by up to 1e-7 beside its own rounding.  A bf16 result does not see it; in
+// fp32 ones it shows in the last place.
 //
 // With several axes (time, height, width) a token has a position on each, and a
 // pair's angle takes the one of its axis; pairs may then lie within the span of

@@ -13,11 +13,12 @@
 // LDS with its first loads, so that its end waits for nothing.
 //
 // 8192 x 8192 x 8192: 400 us (2.75 Pop/s; a library product 446 to 507); 4096 x
-// 21504 x 5376: 365 and 15 to join (2.49 with the join; a library product 438 to
-// 473).  The products alone,
+// 21504 x 5376: 365 to 386 from card to card and 15 to join (2.36 to 2.49 with the join;
+// a library product 438 to 473).  The products alone,
 // in registers, run at 4.1 (power; 32 x 32 x 32 ones at 3.5).  With zeros, which draw
-// less power, it takes 10 % less, so most of the rest is waiting: for blocks to reach
-// LDS.  Tried at 4096 x 4096 x 32768 (412 us): four waves of 128 x 128, which read a
+// less power, it takes 10 % less, so most of the rest is waiting: the matrix cores are
+// busy for 65 % of the time, waves wait in a third of their cycles, L1 for L2 in 56 %.
+// Tried at 4096 x 4096 x 32768 (412 us): four waves of 128 x 128, which read a
 // third less from LDS but leave nothing to run at a barrier, 427; stages of 64
 // columns, four in the ring, whose loads fetch half lines, 503.
 #include "int8_device.h"

@@ -56,9 +56,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* base, in
 // bytes of a block are two 16-byte pieces 64 apart, so that one load of a wave
 // covers 64 contiguous bytes of each of 16 rows.
 //
-// Bound by HBM for large weights and few tokens (1 x 5376 x 21504, x given: 21.6 us,
-// 5.4 TB/s; quantised in the kernel 24.9), by latency for small ones (1 x 1536 x 1152:
-// 4.2 us, quantised), and with more tokens by the reads of x, which every workgroup
+// Bound by HBM for large weights and few tokens (1 x 5376 x 21504, x given: 22.0 us,
+// 5.3 TB/s; quantised in the kernel 24.9), by latency for small ones (1 x 1536 x 1152:
+// 4.6 us, quantised), and with more tokens by the reads of x, which every workgroup
 // repeats (plan_int8).
 // ---------------------------------------------------------------------------
 constexpr int kDecodeWaves = 8, kDecodeThreads = kDecodeWaves * kWave;
@@ -282,11 +282,14 @@ __global__ __launch_bounds__(kDecodeThreads) void int8_decode_kernel(DecodeArgs 
 // reduction is cut into S slices; each writes its sums and a second launch adds
 // and scales them.
 //
-// Bound by the rate at which blocks reach LDS: 64 x 64 tiles take a step of 16 KB in
-// 0.2 us (80 GB/s a unit, 20 TB/s in all), 128 x 128 tiles one of 32 KB in 0.55.  Rings
-// of three to six slots, fragments read a step ahead or not, and waves of 64 x 64 that
-// share the columns and read up to half as much from LDS all took the same within
-// 3 %, hot or cold.  777 x 1152 x 6912 15 to 16 us, 512 x 8192 x 5376 25.6 (1.76 Pop/s).
+// A step of 64 x 64 tiles (16 KB) takes 0.2 us, one of 128 x 128 tiles (32 KB) 0.55.  No
+// unit that was counted is full: with 64 x 64 tiles the matrix cores are busy for 20 %
+// of the time that a unit works (128 x 128: 39 %), its L1 returns data for half of it
+// and waits for L2 in 45 %, which answers in 370 cycles, and waves wait in 40 % of their
+// cycles.  Rings of three to six slots, fragments read a step ahead or not, and waves of
+// 64 x 64 that share the columns and read up to half as much from LDS all took the same
+// within 3 %, hot or cold.  777 x 1152 x 6912 15 to 16 us (16.8 in a trace), 512 x 8192 x
+// 5376 28.8 (1.57 Pop/s).
 // Which tiles a call takes: plan_int8.
 // ---------------------------------------------------------------------------
 struct Args {
@@ -515,15 +518,15 @@ int decode_rows(int64_t m, int64_t out_dim, int cus) {
 // 1 to 4000 tokens, x given; what it picks was the fastest of everything measured
 // there, or within 10 % of it.
 //   Few-token kernel: a start, and the rates at which a unit reads its rows (from
-//   HBM) and x (from its XCD's L2): 16 x 5376 x 5376 8.4 us (64 x 64 tiles 10.6),
-//   but 16 x 5376 x 21504 29.2 (24.4), 33 x 5376 x 21504 48 (25.2) and 64 x 21504 x 5376
-//   47 (28.6 with 64 x 128).
+//   HBM) and x (from its XCD's L2): 16 x 5376 x 5376 8.8 us (64 x 64 tiles 12.0),
+//   but 16 x 5376 x 21504 27.4 (25.3), 33 x 5376 x 21504 46 (26.1) and 64 x 21504 x 5376
+//   47 (29.8 with 64 x 128).
 //   Tiles: a start, and a step for every 128 columns; a unit's workgroups share it;
 //   no less than the weights take from HBM.  Slices are written, read and joined by
-//   another launch.  300 x 1536 x 1152 5.4 with 64 x 64, 7.9 with 64 x 128, 9.5 with 128 x
-//   128; 777 x 1152 x 6912 15.0, 17.5 in two slices, 19.0 in three; 512 x 8192 x 5376
-//   34.5, 30.9, 25.6, and 41.8 with 256 x 256 in four; 128 x 5376 x 21504 42.3 in three,
-//   37.5 in three, 32.3 in six; 2000 x 8192 x 5376 127, 106, 96 and 66 with 256 x 256.
+//   another launch.  300 x 1536 x 1152 6.0 with 64 x 64, 8.3 with 64 x 128, 9.9 with 128 x
+//   128; 777 x 1152 x 6912 15.5, 18.5 in two slices, 20.2 in three; 512 x 8192 x 5376
+//   39.3, 32.4, 28.9, and 42.4 with 256 x 256 in four; 128 x 5376 x 21504 43.1 in three,
+//   39.2 in three, 33.3 in six; 2000 x 8192 x 5376 143, 114, 108 and 71 with 256 x 256.
 struct Shape { int tm, tn; double start, step; };
 constexpr Shape kShapes[] = {{64, 64, 4.2, 0.22}, {64, 128, 5.2, 0.37}, {128, 128, 5.5, 0.57}};
 

@@ -6,15 +6,16 @@
 // with z in the type that the next projection takes: wide, 8-bit integers with a
 // scale per row, or e4m3 with a scale per 128 columns.
 //
-// A row's threads hold it in registers from its load to its last store, in
-// fp32: z is made from h' as it is before it is rounded to be stored.  Each
-// element is read and written once, so the call is bound by HBM for many rows
-// and by latency (two sums over the row, one behind the other) for a few.
+// A row's threads hold it from its load to its last store, in fp32 and in registers
+// (but for what spills, see Reach): z is made from h' as it is before it is rounded
+// to be stored.  Each element is read and written once, so the call is bound by HBM
+// for many rows and by latency (two sums over the row, one behind the other) for a
+// few.
 //
 // h' goes past the caches: the block that reads it next has a layer's weights
 // before it, while z is read at once.  With y the z of the call before and h
-// cold, bf16: 4096 x 5376 36.3 us against 37.5 with both kept and 38.1 with both past
-// them, 1024 x 5376 10.4 (11.5, 10.0), 4096 x 1152 9.2 (10.6, 8.9).  All loads of a row,
+// cold, bf16: 4096 x 5376 33.4 us against 34.2 with both kept and 35.4 with both past
+// them, 1024 x 5376 10.9 (12.0, 10.3), 4096 x 1152 9.3 (10.7, 8.9).  All loads of a row,
 // y's behind h's, before the first use: 37.4 -> 34.2 (5.15 TB/s).  Loading the next row
 // ahead of the present one gained nothing.
 #include "int8_device.h"
@@ -38,8 +39,11 @@ struct NormArgs {
 // (n >= 8: the last piece is then read as the row's last eight elements, so that no
 // load needs a branch around it, and shifted; what it holds of its neighbour's, which
 // may be written already, is dropped); or, in rows shorter than a piece, element by
-// element.  1022 rows, bf16, per call: of 5376 10.6 us, 5377 11.7 (by single elements
-// 30), 8193 20 (235), 16384 26.6, 16385 42.5 (393).
+// element.  1022 rows, bf16, per call: of 5376 10.3 us, 5377 11.7 (by single elements
+// 30), 8193 20 (235), 16384 26.6, 16385 42.5 (393), 24583 94, 32768 48.  Part of what kAny
+// takes longer are spills: a launch may have 1024 threads, which leaves a thread 128
+// registers, and three pieces of a row spill 6 to 22 of them, four (rows of more than
+// 24576) 43 to 64.  With kPieces it is 4 to 25 with four pieces, none with fewer.
 enum Reach { kPieces, kAny, kShort };
 
 // Sixteen bytes as they are reached (an alignment does not pass through a template's type argument).
@@ -293,10 +297,10 @@ __global__ __launch_bounds__(1024) void residual_norm_kernel(NormArgs a) {
 template <typename E, typename H, int Z, int R>
 hipError_t norm_sized(NormArgs& a, hipStream_t stream) {
   // For many rows the fewest threads that hold a row in three pieces each (4096 x
-  // 5376: 40.9 us with 256 threads, 43.2 with 512, 51 with 1024), for fewer up to
+  // 5376: 33.0 us with 256 threads, 37.9 with 512, 43.6 with 1024), for fewer up to
   // one piece each, as long as there are no more than 1024 threads for every
-  // compute unit (1 x 5376: 4.1 us with 1024 threads, 4.5 with 512, 5.5 with 256;
-  // 512 x 5376: 7.5 with 512, 7.7 with 1024).
+  // compute unit (1 x 5376: 3.6 us with 1024 threads, 3.8 with 512, 4.4 with 256;
+  // 512 x 5376: 7.1 with 512, 7.2 with 1024).
   a.T = kWave;
   while (a.T < 1024 && (a.T * 24 < a.n || (a.T * 8 < a.n && a.M * a.T * 2 <= 1 << 18))) a.T *= 2;
   const int ch = (a.n + 8 * a.T - 1) / (8 * a.T), threads = a.T == kWave ? 256 : a.T, rows = threads / a.T;
